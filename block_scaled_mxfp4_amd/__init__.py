@@ -10,8 +10,9 @@ built, every entry point raises; there is no CPU fallback.
 
 Names mirror the C entry points: situ_moe_plan, situ_moe_valid_tactics,
 situ_moe_run, situ_moe_run_profiled, situ_moe_run_static, situ_moe_route, situ_moe_quantize_mxfp8,
-situ_moe_tile_weights, situ_moe_status_string,
-situ_moe_last_error, situ_moe_build_info, situ_moe_tactic_name,
+situ_moe_tile_weights, situ_moe_quantize_fp8_block128, situ_moe_matmul_fp8_block128,
+situ_moe_grouped_matmul, situ_moe_grouped_matmul_dgrad,
+situ_moe_grouped_matmul_wgrad, situ_moe_status_string, situ_moe_last_error, situ_moe_build_info, situ_moe_tactic_name,
 situ_moe_abi_version, and the measurement aid situ_moe_measure_mfma_peak.
 situ_moe(...) is the keyword-only one-call form.
 """
@@ -26,6 +27,8 @@ __all__ = [
     "situ_moe_quantize_mxfp8", "situ_moe_tile_weights", "situ_moe_measure_mfma_peak", "situ_moe_status_string",
     "situ_moe_last_error",
     "situ_moe_build_info", "situ_moe_tactic_name", "situ_moe_abi_version", "situ_moe",
+    "SituMoeFp8Matmul", "SituMoeGrouped", "situ_moe_quantize_fp8_block128", "situ_moe_matmul_fp8_block128",
+    "situ_moe_grouped_matmul", "situ_moe_grouped_matmul_dgrad", "situ_moe_grouped_matmul_wgrad",
     "make_problem", "make_tensors", "new_workspace", "workspace_view", "ACT_W4A16", "ACT_W4A8", "OUT_F32", "OUT_BF16",
 ]
 
@@ -107,6 +110,11 @@ def load():
         "situ_moe_run_static": (c_int, [P(SituMoePlan), P(SituMoeTensors), vp]),
         "situ_moe_quantize_mxfp8": (c_int, [vp, c_i64, c_int, vp, vp, vp]),
         "situ_moe_tile_weights": (c_int, [vp, vp, c_int, c_int, c_int, vp, vp, vp]),
+        "situ_moe_quantize_fp8_block128": (c_int, [vp, c_i64, c_int, c_i64, vp, vp, vp]),
+        "situ_moe_matmul_fp8_block128": (c_int, [P(SituMoeFp8Matmul), vp]),
+        "situ_moe_grouped_matmul": (c_int, [P(SituMoeGrouped), vp]),
+        "situ_moe_grouped_matmul_dgrad": (c_int, [P(SituMoeGrouped), vp]),
+        "situ_moe_grouped_matmul_wgrad": (c_int, [P(SituMoeGrouped), vp]),
         "situ_moe_measure_mfma_peak": (c_int, [c_int, P(ctypes.c_double)]),
         "situ_moe_status_string": (ctypes.c_char_p, [c_int]),
         "situ_moe_last_error": (ctypes.c_char_p, []),
@@ -415,3 +423,8 @@ def situ_moe(*, hidden_states, hidden_states_scale=None, topk_ids=None, topk_wei
                       gate_up_lora_delta=gate_up_lora_delta, activation_lora_input=activation_lora_input)
     situ_moe_run(plan, ts, workspace, stream_obj)
     return out
+
+
+from .grouped import (SituMoeFp8Matmul, SituMoeGrouped, situ_moe_grouped_matmul,  # noqa: E402
+                      situ_moe_grouped_matmul_dgrad, situ_moe_grouped_matmul_wgrad, situ_moe_matmul_fp8_block128,
+                      situ_moe_quantize_fp8_block128)

@@ -3,7 +3,7 @@
     python -m block_scaled_mxfp4_amd.build [--jobs N] [--verbose]
 
 Compiles every kernel source (csrc/*.hip) and the host planner
-(csrc/situ_moe_api.cpp) to objects under _build/, then links
+and entry points (csrc/*.cpp) to objects under _build/, then links
 block_scaled_mxfp4_amd/lib/libsitu_moe.so.  Every call compiles again; no
 step is skipped because an output already exists.
 """
@@ -49,7 +49,7 @@ def build(jobs=None, verbose=False):
     os.makedirs(LIBDIR, exist_ok=True)
     common = [f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-Wall", "-Wno-unused-result",
               f'-DSITU_GIT_REV="{_git_rev()}"', "-I", os.path.join(ROOT, "include")]
-    srcs = sorted(glob.glob(os.path.join(CSRC, "*.hip"))) + [os.path.join(CSRC, "situ_moe_api.cpp")]
+    srcs = sorted(glob.glob(os.path.join(CSRC, "*.hip")) + glob.glob(os.path.join(CSRC, "*.cpp")))
     objs = []
 
     def compile_one(src):

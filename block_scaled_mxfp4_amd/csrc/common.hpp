@@ -103,6 +103,15 @@ __device__ __forceinline__ void fp4x8_to_bf16x8_mul(uint32_t w, float s, uint32_
 // Value of an E4M3 code (OCP FN variant: bias 7, 0x7F / 0xFF NaN) by the hardware decode.
 __device__ __forceinline__ float e4m3_to_f32(uint32_t code) { return __builtin_amdgcn_cvt_f32_fp8((int)code, 0); }
 
+// Eight E4M3 codes (two dwords) as eight bf16 in element order; exact.
+__device__ __forceinline__ bf16x8 fp8x8_to_bf16x8(uint32_t lo, uint32_t hi) {
+  const i32x4 r = {__builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false)),
+                   __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true)),
+                   __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false)),
+                   __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true))};
+  return __builtin_bit_cast(bf16x8, r);
+}
+
 // One lane's 32 E2M1 weights of a K block (16 bytes) as 16 dwords of bf16:
 // MXFP4 with the block's E8M0 code in s, or (NV) NVFP4 with the two E4M3
 // scales of its 16-element halves in the two low bytes of s.

@@ -115,6 +115,9 @@ inline bool general_epilogue(const GemmArgs& a) {
 // (the planner's error reporting, shared with the other entry points).
 situ_status fail_status(situ_status status, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
 
+// SITU_E_DEVICE unless the current device is a gfx950; its CU count.
+situ_status require_device(int* cus);
+
 // Workgroups of `kernel` resident per CU at this block size and dynamic LDS
 // size (hipOccupancyMaxActiveBlocksPerMultiprocessor, cached; thread-safe).
 int resident_per_cu(const void* kernel, int threads, uint32_t lds_bytes);

@@ -215,6 +215,14 @@ situ_status launch_status(hipError_t e, const char* what) {
   return fail(SITU_E_LAUNCH, "%s launch failed: %s", what, hipGetErrorString(e));
 }
 
+}  // namespace
+
+namespace situ {
+situ_status require_device(int* cus) { return device_check(cus); }
+}  // namespace situ
+
+namespace {
+
 situ_status check_run_args(const situ_moe_plan_t* plan, const situ_moe_tensors* t, void* ws, uint64_t ws_bytes,
                            bool route_only) {
   if (!plan) return fail(SITU_E_NULL_ARG, "plan is NULL");

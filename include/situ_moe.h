@@ -255,6 +255,90 @@ situ_status situ_moe_tile_weights(const uint8_t* w, const uint8_t* w_scale, int3
 situ_status situ_moe_quantize_mxfp8(const uint16_t* x_bf16, int64_t rows, int32_t cols,
                                     uint8_t* codes, uint8_t* scales, void* hip_stream);
 
+/* E4M3 quantization of bf16 rows with one fp32 scale per row and 128 columns
+ * (the activations of situ_moe_matmul_fp8_block128):
+ *   scale = max(max |x|, 2^-100) / 448 of the block, code = E4M3
+ *   round-to-nearest-even of x / scale.
+ * x bf16 [rows, cols], `x_stride` elements between rows; codes uint8 [rows,
+ * cols]; scales float [rows, ceil(cols / 128)], the last block of a row
+ * being shorter where cols ends inside one (all device).  cols a positive
+ * multiple of 16, x_stride a multiple of 8 and >= cols, x 16-byte and codes
+ * 8-byte aligned.  A NaN gives a NaN code and does not enter the scale; a
+ * block with an infinity gives scale inf and NaN codes. */
+situ_status situ_moe_quantize_fp8_block128(const uint16_t* x_bf16, int64_t rows, int32_t cols, int64_t x_stride,
+                                           uint8_t* codes, float* scales, void* hip_stream);
+
+/* Product of E4M3 matrices with a scale for each block of 128, dense or with
+ * the rows grouped by expert (the FP8 block format of dense projections and
+ * experts beside MXFP4 ones, "bring up Kimi K3 NVFP4 with CUTLASS and
+ * cuteDSL MegaMoE SiTU", the FP8 attention weights with 128 x 128 scales):
+ *   out[r, j] = sum_b a_scale[r, b] * w_scale[e, j / 128, b] *
+ *               sum_{i in block b} a[r, i] * w[e, j, i]
+ * in fp32, rounded once to bf16 for SITU_OUT_BF16.  e is the group of row r:
+ * group e holds rows offsets[e] .. offsets[e + 1] - 1.  Rows outside every
+ * group are not written.  Sizes: rows 0 .. 2^24, n 1 .. 2^18, k a multiple
+ * of 16 up to 2^18, experts 1 .. 1024.  a and w 16-byte aligned, a_stride a
+ * multiple of 16; out may have any row stride >= n (rows that start on 16
+ * bytes are stored fastest).  The outputs must not overlap the inputs. */
+typedef struct situ_moe_fp8_matmul_t {
+  int32_t rows, n, k;
+  int32_t experts;            /* groups; 1 for a dense product */
+  int32_t out_dtype;          /* SITU_OUT_F32 or SITU_OUT_BF16 */
+  int32_t reserved;           /* 0 */
+  int64_t a_stride;           /* elements between rows of a */
+  int64_t a_scale_stride;     /* elements between rows of a_scale */
+  int64_t out_stride;         /* elements between rows of out */
+  const uint8_t* a;           /* (device) E4M3 [rows, k] */
+  const float* a_scale;       /* (device) [rows, ceil(k / 128)] */
+  const uint8_t* w;           /* (device) E4M3 [experts, n, k], dense */
+  const float* w_scale;       /* (device) [experts, ceil(n / 128), ceil(k / 128)], dense */
+  const int32_t* offsets;     /* (device) [experts + 1], ascending within [0, rows]; NULL (experts 1): one group of all
+                                 rows.  Other values give unspecified outputs, but no access outside the arrays */
+  void* out;                  /* (device) [rows, n] */
+} situ_moe_fp8_matmul_t;
+situ_status situ_moe_matmul_fp8_block128(const situ_moe_fp8_matmul_t* args, void* hip_stream);
+
+/* bf16 products with rows grouped by expert, and their gradients: the LoRA
+ * adapters behind gate_up_lora_delta and activation_lora_input, or whole
+ * bf16 expert matrices.  Group e holds positions offsets[e] ..
+ * offsets[e + 1] - 1, and position r stands for row
+ *   x_row(r) = r             (x_div = 0)  or  pairs[r] / x_div
+ *   y_row(r) = r             (y_div = 0)  or  pairs[r] / y_div
+ * of the x and y sides, so that with the layer's own routing tables (offsets
+ * and perm in the workspace) x_div = top_k reads the token rows of a pair,
+ * and y_div = 1 writes rows t * top_k + s as gate_up_lora_delta wants them.
+ *   situ_moe_grouped_matmul        y[y_row(r)] = w[e] x[x_row(r)]
+ *   situ_moe_grouped_matmul_dgrad  x[x_row(r)] = w[e]^T y[y_row(r)]
+ *   situ_moe_grouped_matmul_wgrad  w[e] = sum_r y[y_row(r)] x[x_row(r)]^T
+ * (for the gradients y, x and w hold dy, dx and dw).  Inputs are bf16, sums
+ * fp32; the output is fp32 or rounded once to bf16.  Rows of an output that
+ * no position stands for are not written; the dw of an empty group is zero.
+ * The written side's div is 0 or 1, and its rows must be distinct.  Sizes:
+ * rows 0 .. 2^24, n and k 1 .. 2^18, experts 1 .. 1024; k a multiple of 8,
+ * and n too for the gradients.  Inputs 16-byte aligned with strides of a
+ * multiple of 8; the output may have any stride (rows that start on 16 bytes
+ * are stored fastest).  The output must not overlap the inputs. */
+typedef struct situ_moe_grouped_t {
+  int32_t rows;               /* positions */
+  int32_t n, k, experts;
+  int32_t x_rows, y_rows;     /* rows of the x and y arrays (of no account where the div is 0: `rows`) */
+  int32_t x_div, y_div;
+  int32_t out_dtype;          /* SITU_OUT_F32 or SITU_OUT_BF16 */
+  int32_t reserved;           /* 0 */
+  int64_t x_stride, y_stride; /* elements between rows */
+  const int32_t* offsets;     /* (device) [experts + 1], ascending within [0, rows]; NULL (experts 1): one group of all
+                                 positions */
+  const int32_t* pairs;       /* (device) [rows]; NULL if both divs are 0.  Wrong offsets or pairs give unspecified
+                                 outputs, but no access outside the arrays; an output row outside y_rows / x_rows is
+                                 not written */
+  void* x;                    /* (device) [x_rows, k] */
+  void* y;                    /* (device) [y_rows, n] */
+  void* w;                    /* (device) [experts, n, k], dense */
+} situ_moe_grouped_t;
+situ_status situ_moe_grouped_matmul(const situ_moe_grouped_t* args, void* hip_stream);
+situ_status situ_moe_grouped_matmul_dgrad(const situ_moe_grouped_t* args, void* hip_stream);
+situ_status situ_moe_grouped_matmul_wgrad(const situ_moe_grouped_t* args, void* hip_stream);
+
 /* Measurement aid for the roofline of the w4a8 GEMMs (not part of the
  * layer): the sustained rate of v_mfma_scale_f32_16x16x128_f8f6f4 with E2M1 x
  * E4M3 operands (the instruction the w4a8 FC1 kernels issue; 65536 flops
