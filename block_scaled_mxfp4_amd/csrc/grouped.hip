@@ -31,7 +31,7 @@
 // the store.
 #include "common.hpp"
 #include "dma.hpp"
-#include "grouped.hpp"
+#include "grouped_dev.hpp"
 
 namespace situ {
 
@@ -56,25 +56,6 @@ __device__ __forceinline__ void gdma16(const uint8_t* p, uint32_t lds) {
 __device__ __forceinline__ void gdma4(const void* p, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off"
                ::"s"(__builtin_amdgcn_readfirstlane(lds)), "v"(p) : "memory", "m0");
-}
-
-__device__ __forceinline__ int row_of(const RowDiv& d, int pair) {
-  return d.div == 1 ? pair : (int)(__umulhi((uint32_t)pair, d.mul) >> d.shift);
-}
-// Row of a matrix for position r of the group order (-1: outside it).
-__device__ __forceinline__ int index_row(const RowDiv& d, const int32_t* pairs, int r, int n_rows) {
-  if (d.div == 0) return r;
-  const int p = pairs[r];
-  const int row = p < 0 ? -1 : row_of(d, p);
-  return row < n_rows ? row : -1;
-}
-
-// First and one-past-last row of group e.  Offsets that do not ascend within
-// [0, rows] give wrong groups, never a row outside [0, rows).
-__device__ __forceinline__ void group_rows(const GroupedArgs& a, int e, int& lo, int& hi) {
-  if (!a.offsets) { lo = 0; hi = a.rows; return; }
-  lo = min(max(a.offsets[e], 0), a.rows);
-  hi = min(max(a.offsets[e + 1], lo), a.rows);
 }
 
 struct Tile {
@@ -332,31 +313,6 @@ struct Kernel {
     }
   }
 
-  static __device__ __forceinline__ void store4(const GroupedArgs& a, uint8_t* row, int col, const f32x4& v) {
-    if (a.out_f32) {
-      float* o = reinterpret_cast<float*>(row) + col;
-      if (a.vec && col + 4 <= a.N) {
-        *reinterpret_cast<f32x4*>(o) = v;
-      } else {
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (col + k < a.N) o[k] = v[k];
-      }
-    } else {
-      uint16_t* o = reinterpret_cast<uint16_t*>(row) + col;
-      uint32_t b[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) b[k] = f32_to_bf16_rne(v[k]);
-      if (a.vec && col + 4 <= a.N) {
-        *reinterpret_cast<uint2*>(o) = make_uint2(b[0] | b[1] << 16, b[2] | b[3] << 16);
-      } else {
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (col + k < a.N) o[k] = (uint16_t)b[k];
-      }
-    }
-  }
-
   static __device__ __forceinline__ void epilogue(const GroupedArgs& a, const Tile& x, int wm, int wn, int lane,
                                                   f32x4 (&acc)[C::CT][C::TT]) {
     const int l = lane & 15, g = lane >> 4;
@@ -543,11 +499,12 @@ using Mid = Cfg<64, 128, 2, 2, 3, 2>;
 }  // namespace
 
 hipError_t launch_grouped(GroupedMode mode, GroupedArgs& a, int cus, hipStream_t s) {
+  if (mode == kGFwd8 && a.out_f32) mode = kGFwd8x;
+  if ((mode == kGFwd || mode == kGFwd8 || mode == kGFwd8x) && few_rows(a)) return launch_grouped_few(mode, a, cus, s);
   switch (mode) {
     case kGFwd: return launch_as<Mid, kGFwd, false>(a, cus, s);
-    case kGFwd8:
-      if (a.out_f32) return launch_as<Mid, kGFwd8x, false>(a, cus, s);
-      return launch_as<Mid, kGFwd8, false>(a, cus, s);
+    case kGFwd8: return launch_as<Mid, kGFwd8, false>(a, cus, s);
+    case kGFwd8x: return launch_as<Mid, kGFwd8x, false>(a, cus, s);
     case kGDgrad: return launch_as<Mid, kGDgrad, false>(a, cus, s);
     case kGWgrad:
       if (a.pairs && (a.t_div.div || a.c_div.div)) return launch_as<Mid, kGWgrad, true>(a, cus, s);

@@ -58,6 +58,10 @@ struct GroupedArgs {
 
 hipError_t launch_grouped(GroupedMode mode, GroupedArgs& a, int cus, hipStream_t s);
 
+// The forward products where groups hold few rows (grouped_few.hip).
+bool few_rows(const GroupedArgs& a);
+hipError_t launch_grouped_few(GroupedMode mode, GroupedArgs& a, int cus, hipStream_t s);
+
 struct QuantBlockArgs {
   const uint16_t* x;
   int64_t x_stride;           // elements

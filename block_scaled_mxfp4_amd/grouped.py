@@ -8,7 +8,6 @@ for the current stream of the tensors' device).  Calls run on the tensors'
 device whichever device is current.
 """
 
-import contextlib
 import ctypes
 
 import block_scaled_mxfp4_amd as _B
@@ -72,27 +71,31 @@ def _out_code(out_dtype):
 class _Place:
     """The device and stream of a call: makes both current while outputs are
     allocated and the kernel is enqueued, where they are not already."""
+    __slots__ = ("handle", "entered")
 
     def __init__(self, device, stream):
         import torch
-        self.stack = contextlib.ExitStack()
-        if device.index != torch.cuda.current_device():
-            self.stack.enter_context(torch.cuda.device(device))
+        self.entered = ()
+        if stream is None and device.index == torch.cuda.current_device():
+            self.handle = torch._C._cuda_getCurrentRawStream(device.index)   # as current_stream(), 2 us sooner
+            return
         if stream is None:
-            self.handle = torch.cuda.current_stream(device).cuda_stream
-        else:
-            if not isinstance(stream, torch.cuda.Stream):
-                stream = torch.cuda.ExternalStream(int(stream), device=device)
-            elif stream.device != device:
-                _fail(2, f"the stream is of {stream.device}, the tensors are on {device}")
-            self.handle = stream.cuda_stream
-            self.stack.enter_context(torch.cuda.stream(stream))
+            stream = torch.cuda.current_stream(device)
+        elif not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), device=device)
+        elif stream.device != device:
+            _fail(2, f"the stream is of {stream.device}, the tensors are on {device}")
+        self.handle = stream.cuda_stream
+        self.entered = (torch.cuda.device(device), torch.cuda.stream(stream))
 
     def __enter__(self):
+        for c in self.entered:
+            c.__enter__()
         return self.handle
 
     def __exit__(self, *e):
-        return self.stack.__exit__(*e)
+        for c in reversed(self.entered):
+            c.__exit__(*e)
 
 
 def situ_moe_quantize_fp8_block128(x, codes=None, scales=None, stream=None):
