@@ -29,6 +29,10 @@
 //
 // Rounding: products and sums in fp32 but for that, one rounding to bf16 at
 // the store.
+#include <algorithm>
+#include <cmath>
+#include <type_traits>
+
 #include "common.hpp"
 #include "dma.hpp"
 #include "grouped_dev.hpp"
@@ -53,6 +57,21 @@ __device__ __forceinline__ void gdma16(const uint8_t* p, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
                ::"s"(__builtin_amdgcn_readfirstlane(lds)), "v"(p) : "memory", "m0");
 }
+template <class T>
+__device__ __forceinline__ const T* uniform(const T* p) {
+  const uint64_t u = (uint64_t)p;
+  return reinterpret_cast<const T*>((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)u) |
+                                    (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(u >> 32)) << 32);
+}
+// The same from a uniform base and a lane's offset.
+__device__ __forceinline__ void gdma16s(const uint8_t* base, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+               ::"s"(__builtin_amdgcn_readfirstlane(lds)), "v"(off), "s"(uniform(base)) : "memory", "m0");
+}
+__device__ __forceinline__ void gdma4s(const float* base, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2"
+               ::"s"(__builtin_amdgcn_readfirstlane(lds)), "v"(off), "s"(uniform(base)) : "memory", "m0");
+}
 __device__ __forceinline__ void gdma4(const void* p, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off"
                ::"s"(__builtin_amdgcn_readfirstlane(lds)), "v"(p) : "memory", "m0");
@@ -73,18 +92,23 @@ __device__ __forceinline__ uint32_t pair_mask(int valid, int d) {
   return valid >= 2 * d + 2 ? 0xffffffffu : (valid == 2 * d + 1 ? 0xffffu : 0u);
 }
 
-template <class C, int MODE>
+// WIDE: rows of T (and of C in kGWgrad) may lie anywhere in their array;
+// otherwise within 4 GiB of a tile's first row, or of the array's where they
+// are gathered (narrow_ok), and a lane's address is a uniform base and 32 bits.
+template <class C, int MODE, bool WIDE>
 struct Kernel {
+  typedef typename std::conditional<WIDE, int64_t, uint32_t>::type Off;
+  typedef C Config;
   static constexpr bool kX = MODE == kGFwd8x, kF8 = MODE == kGFwd8 || kX, kWg = MODE == kGWgrad;
   static constexpr bool kTRows = !kWg;                          // T rows run along q
   static constexpr bool kCRows = MODE == kGFwd || kF8;
   static constexpr int kTBytes = C::BM * 128, kCBytes = C::BN * 128;
-  static constexpr int kSBytes = kF8 ? (C::BM + 63) / 64 * 256 + 256 : 0;   // scales of a step
+  static constexpr int kSBytes = kF8 ? (C::BM + 63) / 64 * 256 + 256 : 0;   // scales of a step: rows, then columns / 128
   static constexpr int kStage = kTBytes + kCBytes + kSBytes;
   static constexpr int kTD = C::BM / 8 / C::W, kCD = C::BN / 8 / C::W;   // DMAs of a wave and step
   static constexpr int kThreads = C::W * 64;
   static constexpr int kIds = kWg ? 8 * 64 * 4 : 0;             // ring of row indices, 64 per step
-  static_assert(!kF8 || (C::BM + 63) / 64 < C::W, "a wave for each 64 row scales and one for the block scales");
+  static constexpr int kTW = (C::BM + 63) / 64, kSD = kF8 ? (kTW + C::W) / C::W : 0;   // blocks of row scales, scale DMAs of a wave
 
   // Byte offset, within an operand stored as 64 rows of q and R columns, of
   // the 16-byte slot holding the chunk of columns 8 c .. + 7 of row r: units
@@ -95,113 +119,144 @@ struct Kernel {
     return u ^ (((r & 3) | ((r >> 1) & 4)) & (R / 16 - 1));
   }
 
+  // A lane's requests: `base` + `off`, step by step.
   struct Geo {
-    const uint8_t* t[kTD];     // kTRows: row address + chunk; else operand + column chunk
-    const uint8_t* c[kCD];
-    const float* s;            // kF8: this lane's scale at step 0
+    const uint8_t* tb;
+    const uint8_t* cb;
+    const float* sb[kSD + 1];
+    Off t[kTD], c[kCD];        // rows along q: row and chunk; else the columns' chunk
+    uint32_t s[kSD + 1];
     int t_chunk, c_chunk;      // byte of the lane's chunk within a step
   };
+
+  static __device__ __forceinline__ void request(const uint8_t* base, Off off, uint32_t lds) {
+    if constexpr (WIDE) gdma16(base + off, lds);
+    else gdma16s(base, off, lds);
+  }
 
   static __device__ __forceinline__ Geo geometry(const GroupedArgs& a, const Tile& x, int wave, int lane) {
     Geo g{};
     if constexpr (kTRows) {
+      const bool near = !WIDE && a.t_div.div == 0;             // rows from the tile's first one
+      g.tb = a.t + (near ? (int64_t)x.m0 * a.t_stride : 0);
       g.t_chunk = ((lane & 7) ^ (lane >> 3)) * 16;
 #pragma unroll
       for (int i = 0; i < kTD; ++i) {
         const int r = min(x.m0 + (wave + C::W * i) * 8 + (lane >> 3), x.hi - 1);
         const int row = max(index_row(a.t_div, a.pairs, r, a.t_rows), 0);
-        g.t[i] = a.t + (int64_t)row * a.t_stride + g.t_chunk;
+        g.t[i] = (Off)(near ? row - x.m0 : row) * (Off)a.t_stride + g.t_chunk;
       }
     } else {
+      g.tb = a.t;
 #pragma unroll
       for (int i = 0; i < kTD; ++i) {
         const int p = (wave + C::W * i) * 64 + lane, r = p / (C::BM / 8), s = p % (C::BM / 8);
         const int col = x.m0 + 16 * unit_slot<C::BM>(r, s >> 1) + 8 * (s & 1);
-        g.t[i] = a.t + 2 * (col < a.M ? col : 0);
+        g.t[i] = 2 * (col < a.M ? col : 0);
       }
     }
-    const uint8_t* w = a.c + (int64_t)(kWg ? 0 : x.e) * a.c_expert;
     if constexpr (kCRows) {
+      g.cb = a.c + (int64_t)x.e * a.c_expert + (int64_t)x.n0 * a.c_stride;
       g.c_chunk = ((lane & 7) ^ swz_c(8 * wave + (lane >> 3))) * 16;   // W is even: the same for every i
 #pragma unroll
       for (int i = 0; i < kCD; ++i) {
-        const int n = min(x.n0 + (wave + C::W * i) * 8 + (lane >> 3), a.N - 1);
-        g.c[i] = w + (int64_t)n * a.c_stride + g.c_chunk;
+        const int n = min((wave + C::W * i) * 8 + (lane >> 3), a.N - 1 - x.n0);
+        g.c[i] = (Off)n * (Off)a.c_stride + g.c_chunk;
       }
     } else {
+      g.cb = a.c + (kWg ? 0 : (int64_t)x.e * a.c_expert);
 #pragma unroll
       for (int i = 0; i < kCD; ++i) {
         const int p = (wave + C::W * i) * 64 + lane, r = p / (C::BN / 8), s = p % (C::BN / 8);
         const int col = x.n0 + 16 * unit_slot<C::BN>(r, s >> 1) + 8 * (s & 1);
-        g.c[i] = w + 2 * (col < a.N ? col : 0);
+        g.c[i] = 2 * (col < a.N ? col : 0);
       }
     }
-    if constexpr (kF8) {
-      constexpr int kTW = (C::BM + 63) / 64;
-      if (wave < kTW) {
-        const int r = min(x.m0 + 64 * wave + lane, x.hi - 1);
-        const int row = max(index_row(a.t_div, a.pairs, r, a.t_rows), 0);
-        g.s = a.t_scale + (int64_t)row * a.ts_stride;
+#pragma unroll
+    for (int i = 0; i < kSD; ++i) {
+      const int b = wave + C::W * i;
+      if (b < kTW) {
+        const int r = x.m0 + 64 * b;
+        g.sb[i] = a.t_scale + (int64_t)min(r, x.hi - 1) * a.ts_stride;
+        g.s[i] = (uint32_t)max(min(lane, x.hi - 1 - r), 0) * (uint32_t)a.ts_stride * 4u;
       } else {                       // one per 128 columns of the tile, lane after lane
-        const int nb = (a.N + 127) / 128, kb = (a.K + 127) / 128;
-        g.s = a.c_scale + ((int64_t)x.e * nb + min(x.n0 / 128 + lane, nb - 1)) * kb;
+        const int nb = (a.N + 127) / 128, kb = (a.K + 127) / 128, n = x.n0 / 128;
+        g.sb[i] = a.c_scale + ((int64_t)x.e * nb + n) * kb;
+        g.s[i] = (uint32_t)min(lane, nb - 1 - n) * (uint32_t)kb * 4u;
       }
     }
     return g;
   }
 
-  // Request step j into the stage at `st`.
+  // The row indices of the first N steps (kGWgrad).
+  template <int N>
+  static __device__ __forceinline__ void first_ids(const GroupedArgs& a, const Tile& x, uint8_t* ids, int wave, int lane) {
+    for (int s = wave; s < N; s += C::W)
+      reinterpret_cast<int32_t*>(ids)[s * 64 + lane] = a.pairs[min(x.lo + 64 * s + lane, x.hi - 1)];
+  }
+
+  // One request (1 KB a wave) of step j into the stage at `st`: block i of
+  // this wave's share of T or C, a block of scales, the row indices.  A chunk
+  // past the end of q repeats its row's first one.
+  static __device__ __forceinline__ Off chunk_at(const GroupedArgs& a, int j, int chunk, Off off) {
+    const int q = 128 * j;
+    return q + chunk < a.K * (kF8 ? 1 : 2) ? off + (Off)q : off - (Off)chunk;
+  }
+  template <bool IDX>
+  static __device__ __forceinline__ void issue_t(const GroupedArgs& a, const Tile& x, const Geo& g, uint32_t st,
+                                                 const uint8_t* ids, int j, int i, int wave, int lane) {
+    const uint32_t to = st + (wave + C::W * i) * 1024;
+    if constexpr (kTRows) {
+      request(g.tb, chunk_at(a, j, g.t_chunk, g.t[i]), to);
+    } else {
+      request_q<IDX>(a, x, a.t_div, g.tb, a.t_stride, a.t_rows, ids, j, ((wave + C::W * i) * 64 + lane) / (C::BM / 8),
+                     g.t[i], to);
+    }
+  }
+  template <bool IDX>
+  static __device__ __forceinline__ void issue_c(const GroupedArgs& a, const Tile& x, const Geo& g, uint32_t st,
+                                                 const uint8_t* ids, int j, int i, int wave, int lane) {
+    const uint32_t to = st + kTBytes + (wave + C::W * i) * 1024;
+    const int r = ((wave + C::W * i) * 64 + lane) / (C::BN / 8);
+    if constexpr (kCRows) request(g.cb, chunk_at(a, j, g.c_chunk, g.c[i]), to);
+    else if constexpr (kWg) request_q<IDX>(a, x, a.c_div, g.cb, a.c_stride, a.c_rows, ids, j, r, g.c[i], to);
+    else request(g.cb + (int64_t)(64 * j) * a.c_stride, (Off)min(r, a.K - 1 - 64 * j) * (Off)a.c_stride + g.c[i], to);
+  }
+  // kGWgrad: columns `col` of the matrix row of element r of step j (the last
+  // one's past the end; a row of wrong pairs is some row of the matrix).
+  template <bool IDX>
+  static __device__ __forceinline__ void request_q(const GroupedArgs& a, const Tile& x, const RowDiv& d,
+                                                   const uint8_t* base, int64_t stride, int n_rows, const uint8_t* ids,
+                                                   int j, int r, Off col, uint32_t to) {
+    if (IDX && d.div != 0) {
+      const int p = max(reinterpret_cast<const int32_t*>(ids)[(j & 7) * 64 + r], 0);
+      request(base, (Off)min(row_of(d, p), n_rows - 1) * (Off)stride + col, to);
+    } else {
+      const int lo = x.lo + 64 * j;
+      request(base + (int64_t)lo * stride, (Off)min(r, x.hi - 1 - lo) * (Off)stride + col, to);
+    }
+  }
+  static __device__ __forceinline__ void issue_s(const Geo& g, uint32_t st, int j, int wave) {
+#pragma unroll
+    for (int i = 0; i < kSD; ++i)
+      gdma4s(g.sb[i] + j, g.s[i], st + kTBytes + kCBytes + min(wave + C::W * i, kTW) * 256);
+  }
+  static __device__ __forceinline__ void issue_ids(const GroupedArgs& a, const Tile& x, const uint8_t* ids, int s, int lane) {
+    gdma4(a.pairs + min(x.lo + 64 * (int64_t)s + lane, (int64_t)x.hi - 1), lds_addr_of(ids) + (s & 7) * 256);
+  }
+
+  // Request all of step j.
   template <bool IDX>
   static __device__ __forceinline__ void issue(const GroupedArgs& a, const Tile& x, const Geo& g, uint32_t st,
                                                const uint8_t* ids, int j, int wave, int lane) {
-    if constexpr (IDX) {             // the row indices of a later step go ahead of this step's rows
-      const int s = j + C::ST - 1;
-      gdma4(a.pairs + min(x.lo + 64 * (int64_t)s + lane, (int64_t)x.hi - 1), lds_addr_of(ids) + (s & 7) * 256);
-    }
-    const int64_t q = (int64_t)j * 128;
-    if constexpr (kTRows) {
-      // a chunk past the end of q repeats the row's first one
-      const int64_t at = q + g.t_chunk < (int64_t)a.K * (kF8 ? 1 : 2) ? q : -g.t_chunk;
+    if constexpr (IDX) issue_ids(a, x, ids, j + C::ST - 1, lane);   // of a later step, ahead of this step's rows
 #pragma unroll
-      for (int i = 0; i < kTD; ++i) gdma16(g.t[i] + at, st + (wave + C::W * i) * 1024);
-    } else {
+    for (int i = 0; i < kTD; ++i) issue_t<IDX>(a, x, g, st, ids, j, i, wave, lane);
 #pragma unroll
-      for (int i = 0; i < kTD; ++i) {
-        const int r = ((wave + C::W * i) * 64 + lane) / (C::BM / 8);
-        gdma16(g.t[i] + q_row<IDX>(a, x, a.t_div, a.t_rows, ids, j, r) * a.t_stride, st + (wave + C::W * i) * 1024);
-      }
-    }
-    if constexpr (kCRows) {
-      const int64_t at = q + g.c_chunk < (int64_t)a.K * (kF8 ? 1 : 2) ? q : -g.c_chunk;
-#pragma unroll
-      for (int i = 0; i < kCD; ++i) gdma16(g.c[i] + at, st + kTBytes + (wave + C::W * i) * 1024);
-    } else {
-#pragma unroll
-      for (int i = 0; i < kCD; ++i) {
-        const int r = ((wave + C::W * i) * 64 + lane) / (C::BN / 8);
-        const int64_t row = kWg ? q_row<IDX>(a, x, a.c_div, a.c_rows, ids, j, r) : min(64 * j + r, a.K - 1);
-        gdma16(g.c[i] + row * a.c_stride, st + kTBytes + (wave + C::W * i) * 1024);
-      }
-    }
-    if constexpr (kF8) {
-      constexpr int kTW = (C::BM + 63) / 64;
-      gdma4(g.s + j, st + kTBytes + kCBytes + min(wave, kTW) * 256);
-    }
+    for (int i = 0; i < kCD; ++i) issue_c<IDX>(a, x, g, st, ids, j, i, wave, lane);
+    issue_s(g, st, j, wave);
   }
-  static constexpr int dmas(bool idx) { return kTD + kCD + (kF8 ? 1 : 0) + (idx ? 1 : 0); }
-
-  // kGWgrad: the matrix row of element r of step j.
-  template <bool IDX>
-  static __device__ __forceinline__ int64_t q_row(const GroupedArgs& a, const Tile& x, const RowDiv& d, int n_rows,
-                                                  const uint8_t* ids, int j, int r) {
-    if constexpr (IDX) {
-      if (d.div != 0) {
-        const int p = max(reinterpret_cast<const int32_t*>(ids)[(j & 7) * 64 + r], 0);
-        return min(row_of(d, p), n_rows - 1);
-      }
-    }
-    return min((int64_t)x.lo + 64 * (int64_t)j + r, (int64_t)x.hi - 1);
-  }
+  static constexpr int dmas(bool idx) { return kTD + kCD + kSD + (idx ? 1 : 0); }
 
   // Eight consecutive elements of q (half h of a step, group g of lanes) of
   // the 16 columns of unit u, from an operand stored as 64 rows of q.
@@ -223,77 +278,92 @@ struct Kernel {
     return v;
   }
 
-  // Multiply one staged step into the accumulators; TAIL: `left` elements of
-  // q remain in it, the others are cleared.
+  // The fragments of one staged step: `st` its stage, (t0, c0) the wave's
+  // first 16-row and 16-column tiles; TAIL: `left` elements of q remain in
+  // the step, the others are cleared.
+  template <bool TAIL>
+  static __device__ __forceinline__ void clear(uint4& v, int h, int g, int left) {
+    if constexpr (TAIL) {
+      uint32_t* d = reinterpret_cast<uint32_t*>(&v);
+      const int valid = kF8 ? left - 16 * (4 * h + g) : left - 32 * h - 8 * g;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) d[i] &= kF8 ? (valid > 0 ? 0xffffffffu : 0u) : pair_mask(valid, i);
+    }
+  }
+  template <bool TAIL>
+  static __device__ __forceinline__ uint4 read_t(const uint8_t* st, int tile, int h, int lane, int left) {
+    const int l = lane & 15, g = lane >> 4;
+    uint4 v;
+    if constexpr (kTRows) v = *reinterpret_cast<const uint4*>(st + (16 * tile + l) * 128 + (((g + 4 * h) ^ swz_t(l)) * 16));
+    else v = read_tr<C::BM>(st, tile, h, lane);
+    clear<TAIL>(v, h, g, left);
+    return v;
+  }
+  template <bool TAIL>
+  static __device__ __forceinline__ uint4 read_c(const uint8_t* st, int tile, int h, int lane, int left) {
+    const int l = lane & 15, g = lane >> 4;
+    uint4 v;
+    if constexpr (kCRows) {
+      // tiles 2 p and 2 p + 1 share 32 columns: row 4 a + b of them is column 8 a + b and 8 a + 4 + b, so a lane's
+      // results are eight consecutive columns
+      const int row = 16 * (tile & ~1) + 8 * (l >> 2) + (l & 3) + 4 * (tile & 1);
+      v = *reinterpret_cast<const uint4*>(st + kTBytes + row * 128 + (((g + 4 * h) ^ swz_c(row)) * 16));
+    } else {
+      v = read_tr<C::BN>(st + kTBytes, tile, h, lane);
+    }
+    clear<TAIL>(v, h, g, left);
+    return v;
+  }
+  static __device__ __forceinline__ i32x8 join(const uint4& lo, const uint4& hi) {
+    return i32x8{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
+  }
+  static __device__ __forceinline__ const float* scales(const uint8_t* st) {
+    return reinterpret_cast<const float*>(st + kTBytes + kCBytes);
+  }
+
+  // Multiply one staged step into the accumulators.
   template <bool TAIL>
   static __device__ __forceinline__ void compute(const uint8_t* st, int wm, int wn, int lane, int left,
                                                  f32x4 (&acc)[C::CT][C::TT]) {
-    const int l = lane & 15, g = lane >> 4;
-    const int t0 = wm * C::TT, c0 = wn * C::CT;     // the wave's first 16-row and 16-column tiles
-    auto clear = [&](uint4& v, int h) {
-      if constexpr (TAIL) {
-        uint32_t* d = reinterpret_cast<uint32_t*>(&v);
-        const int valid = kF8 ? left - 16 * (4 * h + g) : left - 32 * h - 8 * g;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) d[i] &= kF8 ? (valid > 0 ? 0xffffffffu : 0u) : pair_mask(valid, i);
-      }
-    };
-    auto read_t = [&](int j, int h) {
-      uint4 v;
-      if constexpr (kTRows) {
-        v = *reinterpret_cast<const uint4*>(st + (16 * (t0 + j) + l) * 128 + (((g + 4 * h) ^ swz_t(l)) * 16));
-      } else {
-        v = read_tr<C::BM>(st, t0 + j, h, lane);
-      }
-      clear(v, h);
-      return v;
-    };
-    auto read_c = [&](int i, int h) {
-      uint4 v;
-      if constexpr (kCRows) {
-        // tiles 2 p and 2 p + 1 share 32 columns: row 4 a + b of them is column 8 a + b and 8 a + 4 + b, so a
-        // lane's results are eight consecutive columns
-        const int row = 16 * (c0 + (i & ~1)) + 8 * (l >> 2) + (l & 3) + 4 * (i & 1);
-        v = *reinterpret_cast<const uint4*>(st + kTBytes + row * 128 + (((g + 4 * h) ^ swz_c(row)) * 16));
-      } else {
-        v = read_tr<C::BN>(st + kTBytes, c0 + i, h, lane);
-      }
-      clear(v, h);
-      return v;
-    };
+    const int l = lane & 15;
+    const int t0 = wm * C::TT, c0 = wn * C::CT;
     if constexpr (kF8) {
-      const float* sc = reinterpret_cast<const float*>(st + kTBytes + kCBytes);
-      float ts[C::TT];
-      uint4 cv[C::CT][2];
-      float cs[C::CT];
+      const float* sc = scales(st);
+      float ts[C::TT], cs[C::CT];
+      i32x8 cv[C::CT];
 #pragma unroll
       for (int i = 0; i < C::CT; ++i) {
-        cv[i][0] = read_c(i, 0);
-        cv[i][1] = read_c(i, 1);
-        cs[i] = sc[(C::BM + 63) / 64 * 64 + (c0 + i) / 8];
+        cv[i] = join(read_c<TAIL>(st, c0 + i, 0, lane, left), read_c<TAIL>(st, c0 + i, 1, lane, left));
+        cs[i] = sc[64 * kTW + (c0 + i) / 8];
       }
 #pragma unroll
       for (int j = 0; j < C::TT; ++j) ts[j] = sc[16 * (t0 + j) + l];
+      // multiply-adds two MFMAs behind, as in phase_mul
+      constexpr int kN = C::TT * C::CT, kBehind = kX ? 0 : 2;
+      f32x4 p[kN];
+      i32x8 tv;
 #pragma unroll
-      for (int j = 0; j < C::TT; ++j) {
-        const uint4 lo = read_t(j, 0), hi = read_t(j, 1);
-        const i32x8 tv = {(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
-#pragma unroll
-        for (int i = 0; i < C::CT; ++i) {
-          const i32x8 v = {(int)cv[i][0].x, (int)cv[i][0].y, (int)cv[i][0].z, (int)cv[i][0].w,
-                           (int)cv[i][1].x, (int)cv[i][1].y, (int)cv[i][1].z, (int)cv[i][1].w};
-          f32x4 p = {0.0f, 0.0f, 0.0f, 0.0f};
+      for (int q = 0; q < kN + kBehind; ++q) {
+        if (q < kN) {
+          const int j = q / C::CT, i = q % C::CT;
+          if (i == 0) tv = join(read_t<TAIL>(st, t0 + j, 0, lane, left), read_t<TAIL>(st, t0 + j, 1, lane, left));
+          p[q] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
           if constexpr (kX) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-              p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fp8x8_to_bf16x8(v[2 * q], v[2 * q + 1]),
-                                                          fp8x8_to_bf16x8(tv[2 * q], tv[2 * q + 1]), p, 0, 0, 0);
+            for (int h = 0; h < 4; ++h)
+              p[q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fp8x8_to_bf16x8(cv[i][2 * h], cv[i][2 * h + 1]),
+                                                             fp8x8_to_bf16x8(tv[2 * h], tv[2 * h + 1]), p[q], 0, 0, 0);
           } else {
-            p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(v, tv, p, 0, 0, 0, 0, 0, 0);
+            p[q] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(cv[i], tv, p[q], 0, 0, 0, 0, 0, 0);
+            __builtin_amdgcn_sched_barrier(0);
           }
+        }
+        if (q >= kBehind) {
+          const int r = q - kBehind, j = r / C::CT, i = r % C::CT;
           const float s = ts[j] * cs[i];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) acc[i][j][k] = fmaf(p[k], s, acc[i][j][k]);
+          for (int k = 0; k < 4; ++k) acc[i][j][k] = fmaf(p[r][k], s, acc[i][j][k]);
+          if constexpr (!kX) __builtin_amdgcn_sched_barrier(0);
         }
       }
     } else {
@@ -301,16 +371,120 @@ struct Kernel {
       for (int h = 0; h < 2; ++h) {
         bf16x8 cv[C::CT];
 #pragma unroll
-        for (int i = 0; i < C::CT; ++i) cv[i] = __builtin_bit_cast(bf16x8, read_c(i, h));
+        for (int i = 0; i < C::CT; ++i) cv[i] = __builtin_bit_cast(bf16x8, read_c<TAIL>(st, c0 + i, h, lane, left));
 #pragma unroll
         for (int j = 0; j < C::TT; ++j) {
-          const bf16x8 tv = __builtin_bit_cast(bf16x8, read_t(j, h));
+          const bf16x8 tv = __builtin_bit_cast(bf16x8, read_t<TAIL>(st, t0 + j, h, lane, left));
 #pragma unroll
           for (int i = 0; i < C::CT; ++i)
             acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(cv[i], tv, acc[i][j], 0, 0, 0);
         }
       }
     }
+  }
+
+  // The same step in four phases for two groups of waves taking turns (see
+  // grouped_pair_kernel).  The column fragments of a half of the step stay in
+  // registers until their second phase; row fragments are read for each.
+  //   E4M3             phase p: quarter p of the rows, all of the step
+  //   T rows along q   phase p: half p / 2 of the rows, half p % 2 of the step
+  //   T rows along t   phase p: half p % 2 of the rows, half p / 2 of the step
+  static constexpr int kRowsOf(int p) { return kTRows ? p / 2 : p % 2; }
+  static constexpr int kHalfOf(int p) { return kTRows ? p % 2 : p / 2; }
+  struct Phase {
+    uint4 c[C::CT][2], t[C::TT / 2];
+    float ts[C::TT / 4 + 1], cs;
+  };
+  template <int P, bool TAIL>
+  static __device__ __forceinline__ void phase_read(const uint8_t* st, int wm, int wn, int lane, int left, Phase& f) {
+    const int t0 = wm * C::TT, c0 = wn * C::CT;
+    if constexpr (kF8) {
+      if constexpr (P == 0) {
+#pragma unroll
+        for (int i = 0; i < C::CT; ++i) {
+          f.c[i][0] = read_c<TAIL>(st, c0 + i, 0, lane, left);
+          f.c[i][1] = read_c<TAIL>(st, c0 + i, 1, lane, left);
+        }
+        f.cs = scales(st)[64 * kTW + c0 / 8];
+      }
+#pragma unroll
+      for (int j = 0; j < C::TT / 4; ++j) {
+        f.t[2 * j] = read_t<TAIL>(st, t0 + P * (C::TT / 4) + j, 0, lane, left);
+        f.t[2 * j + 1] = read_t<TAIL>(st, t0 + P * (C::TT / 4) + j, 1, lane, left);
+        f.ts[j] = scales(st)[16 * (t0 + P * (C::TT / 4) + j) + (lane & 15)];
+      }
+    } else {
+      constexpr int H = kHalfOf(P);
+      if constexpr (P == 0 || H != kHalfOf(P - 1)) {
+        if constexpr (kTRows ? P < 2 : true) {
+#pragma unroll
+          for (int i = 0; i < C::CT; ++i) f.c[i][kTRows ? H : 0] = read_c<TAIL>(st, c0 + i, H, lane, left);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < C::TT / 2; ++j)
+        f.t[j] = read_t<TAIL>(st, t0 + kRowsOf(P) * (C::TT / 2) + j, H, lane, left);
+    }
+  }
+  template <int P>
+  static __device__ __forceinline__ void phase_mul(const Phase& f, f32x4 (&acc)[C::CT][C::TT]) {
+    if constexpr (kF8) {
+      // an MFMA takes 32 cycles, its four multiply-adds 16 and must wait for it: they are held two MFMAs behind
+      constexpr int kN = C::TT / 4 * C::CT, kBehind = 2;
+      f32x4 p[kN];
+      float s[C::TT / 4];
+#pragma unroll
+      for (int j = 0; j < C::TT / 4; ++j) s[j] = f.ts[j] * f.cs;
+#pragma unroll
+      for (int q = 0; q < kN + kBehind; ++q) {
+        if (q < kN) {
+          const int j = q / C::CT, i = q % C::CT;
+          const f32x4 z = {0.0f, 0.0f, 0.0f, 0.0f};
+          p[q] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(join(f.c[i][0], f.c[i][1]),
+                                                                  join(f.t[2 * j], f.t[2 * j + 1]), z, 0, 0, 0, 0, 0, 0);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        if (q >= kBehind) {
+          const int r = q - kBehind, j = r / C::CT, i = r % C::CT;
+          f32x4& d = acc[i][P * (C::TT / 4) + j];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) d[k] = fmaf(p[r][k], s[j], d[k]);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < C::TT / 2; ++j)
+#pragma unroll
+        for (int i = 0; i < C::CT; ++i) {
+          f32x4& d = acc[i][kRowsOf(P) * (C::TT / 2) + j];
+          d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, f.c[i][kTRows ? kHalfOf(P) : 0]),
+                                                      __builtin_bit_cast(bf16x8, f.t[j]), d, 0, 0, 0);
+        }
+    }
+  }
+
+  // The requests of a step, in four groups of two or three per wave, in the
+  // order they are made and needed (grouped_pair_kernel):
+  //   T rows along q: C (0, 1), C (2, 3), T of the first half of the rows with
+  //     the scales, T of the second;
+  //   T rows along t: T and C of the first half of the step, T and C of the second.
+  static constexpr int kGroup[4] = {2, 2, 2 + kSD, 2};
+  template <int G, bool IDX>
+  static __device__ __forceinline__ void issue_group(const GroupedArgs& a, const Tile& x, const Geo& g, uint32_t lds0,
+                                                     const uint8_t* ids, int j, int wave, int lane) {
+    const uint32_t st = lds0 + (j & 1) * kStage;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if constexpr (kTRows) {
+        if constexpr (G < 2) issue_c<IDX>(a, x, g, st, ids, j, 2 * G + i, wave, lane);
+        else issue_t<IDX>(a, x, g, st, ids, j, (G - 2) + 2 * i, wave, lane);
+      } else {
+        if constexpr (G % 2 == 0) issue_t<IDX>(a, x, g, st, ids, j, G + i, wave, lane);
+        else issue_c<IDX>(a, x, g, st, ids, j, G - 1 + i, wave, lane);
+      }
+    }
+    if constexpr (G == 2) issue_s(g, st, j, wave);
   }
 
   static __device__ __forceinline__ void epilogue(const GroupedArgs& a, const Tile& x, int wm, int wn, int lane,
@@ -376,35 +550,64 @@ __device__ __forceinline__ int find_group(const int* pre, int experts, int m, in
   return 16 * chunk + (__popcll(__ballot(e < experts && v <= m)) >> 2) - 1;
 }
 
-template <class C, int MODE, bool IDX>
-__global__ __launch_bounds__(C::W * 64, C::MINB) void grouped_kernel(GroupedArgs a) {
-  using K = Kernel<C, MODE>;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[C::ST * K::kStage + K::kIds + (kMaxE + 1 + 16) * 4];
-  uint8_t* ids = lds + C::ST * K::kStage;
-  int* pre = reinterpret_cast<int*>(lds + C::ST * K::kStage + K::kIds);
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = wave / C::WN, wn = wave % C::WN;
-  const uint32_t lds0 = lds_addr_of(lds);
+// A workgroup barrier that neither waits for memory nor lets anything move
+// across it.
+__device__ __forceinline__ void part_barrier() {
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_barrier" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+// Wait until this wave's requests but the last N have landed.
+template <int N>
+__device__ __forceinline__ void land() {
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+template <class K, int P, class A>
+__device__ __forceinline__ void phase_mul_fenced(const typename K::Phase& f, A& acc) {
+  __builtin_amdgcn_s_setprio(1);
+  K::template phase_mul<P>(f, acc);
+  __builtin_amdgcn_s_setprio(0);
+  part_barrier();
+}
 
-  int m_tiles;
-  if constexpr (K::kWg) {
-    m_tiles = a.experts * a.m_bound;
-  } else {
-    if (a.offsets) {
+// The tiles of one workgroup, in order.
+template <class K>
+struct Walk {
+  using C = typename K::Config;
+  int m_tiles, slots;
+  int64_t it, last;
+
+  __device__ __forceinline__ Walk(const GroupedArgs& a, int* pre, int tid) {
+    if constexpr (K::kWg) {
+      m_tiles = a.experts * a.m_bound;
+    } else if (a.offsets) {
       tile_prefix<K::kThreads>(a, C::BM, pre, pre + kMaxE + 1, tid);
       m_tiles = min(pre[a.experts], a.m_bound);   // ascending offsets never exceed the bound
     } else {
       m_tiles = a.m_bound;
     }
+    // each XCD (workgroups b, b + 8, ...) walks a contiguous share of the tiles
+    const int64_t total = (int64_t)m_tiles * a.n_tiles;
+    const int xcds = min((int)gridDim.x, 8), xcd = blockIdx.x % xcds;
+    slots = gridDim.x / xcds;
+    it = total * xcd / xcds + blockIdx.x / xcds;
+    last = total * (xcd + 1) / xcds;
   }
-  const int64_t total = (int64_t)m_tiles * a.n_tiles;
 
-  // each XCD (workgroups b, b + 8, ...) walks a contiguous share of the tiles
-  const int xcds = min((int)gridDim.x, 8), xcd = blockIdx.x % xcds, slots = gridDim.x / xcds;
-  const int64_t first = total * xcd / xcds, last = total * (xcd + 1) / xcds;
-  for (int64_t it = first + blockIdx.x / xcds; it < last; it += slots) {
-    Tile x;
-    int steps, left;
+  // Moves on to the next tile that holds something; false if there is none.
+  __device__ __forceinline__ bool next(const GroupedArgs& a, const int* pre, int lane, Tile& x, int& steps, int& left) {
+    for (; it < last; it += slots) {
+      if (tile(a, pre, lane, x, steps, left)) {
+        it += slots;
+        return true;
+      }
+    }
+    return false;
+  }
+
+  // The tile `it`; false if it holds nothing (only with offsets that do not ascend).
+  __device__ __forceinline__ bool tile(const GroupedArgs& a, const int* pre, int lane, Tile& x, int& steps, int& left) {
     if constexpr (K::kWg) {
       const int per = a.m_bound * a.n_tiles;
       x.e = (int)(it / per);
@@ -414,12 +617,12 @@ __global__ __launch_bounds__(C::W * 64, C::MINB) void grouped_kernel(GroupedArgs
       group_rows(a, x.e, x.lo, x.hi);
       steps = (x.hi - x.lo + 63) / 64;
       left = x.hi - x.lo - 64 * (steps - 1);
+      return true;
     } else {
       // within a group: eight row tiles by all column tiles, rows fastest
       int local, m_l;
       if (a.offsets) {
-        x.e = find_group(pre, a.experts, (int)(it / a.n_tiles), lane);
-        x.e = __builtin_amdgcn_readfirstlane(x.e);
+        x.e = __builtin_amdgcn_readfirstlane(find_group(pre, a.experts, (int)(it / a.n_tiles), lane));
         local = (int)(it - (int64_t)pre[x.e] * a.n_tiles);
         m_l = pre[x.e + 1] - pre[x.e];
       } else {
@@ -432,13 +635,138 @@ __global__ __launch_bounds__(C::W * 64, C::MINB) void grouped_kernel(GroupedArgs
       const int high = min(8, m_l - 8 * block);
       x.m0 = x.lo + (8 * block + in % high) * C::BM;
       x.n0 = (in / high) * C::BN;
-      if (x.m0 >= x.hi || x.n0 >= a.N) continue;   // only with offsets that do not ascend
       constexpr int kQ = K::kF8 ? 128 : 64;
       steps = (a.K + kQ - 1) / kQ;
       left = a.K - kQ * (steps - 1);
+      return x.m0 < x.hi && x.n0 < a.N;
     }
-    const bool tail = left < (K::kF8 ? 128 : 64);
+  }
+};
 
+template <class C, int MODE, bool IDX>
+__global__ __launch_bounds__(C::W * 64, C::MINB) void grouped_kernel(GroupedArgs a) {
+  using K = Kernel<C, MODE, true>;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[C::ST * K::kStage + K::kIds + (kMaxE + 1 + 16) * 4];
+  uint8_t* ids = lds + C::ST * K::kStage;
+  int* pre = reinterpret_cast<int*>(lds + C::ST * K::kStage + K::kIds);
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / C::WN, wn = wave % C::WN;
+  const uint32_t lds0 = lds_addr_of(lds);
+
+  Walk<K> w(a, pre, tid);
+  Tile x;
+  int steps, left;
+  typename K::Geo g;
+  // go on to the next tile that holds something and request its first steps
+  auto start = [&]() {
+    if (!w.next(a, pre, lane, x, steps, left)) return false;
+    if (steps == 0) return true;
+    g = K::geometry(a, x, wave, lane);
+    if constexpr (IDX) {
+      K::template first_ids<C::ST - 1>(a, x, ids, wave, lane);
+      __syncthreads();
+    }
+#pragma unroll
+    for (int s = 0; s < C::ST - 1; ++s)
+      if (s < steps) K::template issue<IDX>(a, x, g, lds0 + s * K::kStage, ids, s, wave, lane);
+    return true;
+  };
+
+  bool more = start();
+  while (more) {
+    const bool tail = left < (K::kF8 ? 128 : 64);
+    f32x4 acc[C::CT][C::TT];
+#pragma unroll
+    for (int i = 0; i < C::CT; ++i)
+#pragma unroll
+      for (int j = 0; j < C::TT; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+    int stage = 0;
+    for (int j = 0; j < steps; ++j) {
+      constexpr int kD = K::dmas(IDX);
+      const int after = min(C::ST - 2, steps - 1 - j);
+      if (after >= 2) dma_barrier<2 * kD>();
+      else if (after == 1) dma_barrier<kD>();
+      else dma_barrier<0>();
+      const int ahead = stage == 0 ? C::ST - 1 : stage - 1;
+      if (j + C::ST - 1 < steps)
+        K::template issue<IDX>(a, x, g, lds0 + ahead * K::kStage, ids, j + C::ST - 1, wave, lane);
+      const uint8_t* st = lds + stage * K::kStage;
+      if (tail && j == steps - 1) K::template compute<true>(st, wm, wn, lane, left, acc);
+      else K::template compute<false>(st, wm, wn, lane, left, acc);
+      stage = stage + 1 == C::ST ? 0 : stage + 1;
+    }
+    lds_barrier();                                           // all fragments of the tile have been read
+    const Tile done = x;
+    more = start();                                          // under way while the results are stored
+    K::epilogue(a, done, wm, wn, lane, acc);
+  }
+}
+
+// Large tiles: two groups of four waves, one wave of each on every SIMD, take
+// turns.  A step has four phases, each a reading part R (fragments from LDS,
+// requests for later steps) and a multiplying part M (1/4 of the step's
+// MFMAs), with a workgroup barrier after every part; the second group runs
+// one part behind, so that while one group multiplies the other reads.
+//
+// Two stages hold steps j and j + 1, and a region is requested again as soon
+// as its step has been read, so that requests have about a step to land
+// (issue_group's groups 0 .. 3):
+//   R3(j): group 0 of step j + 2     R1(j): group 2 of step j + 1
+//   R0(j): group 1 of step j + 1     R2(j): group 3 of step j + 1
+// Regions: groups 0 and 1 are last read in R1, group 2 in R1 (T rows along q)
+// or R2 to R3, group 3 in R3, and the scales in R3.  A fragment read in Rk
+// is in its register by the end of Mk.  The first group issues one part ahead
+// of the second: its R(k + 2) begins when the second group's M(k) has ended.
+// Group 0 in R3 overwrites what R1 read, group 1 in R0 and group 2 in R1 of the
+// next step what R1 and R3 read: two parts R on, or more.  Group 3 in R2 is
+// three parts R after R3.
+// Landing: R0 of a step needs its groups 0 to 2 (T rows along t: 0 and 1), R2 the
+// rest.  Each wave waits for its own requests before the barrier that ends R3
+// (or R1); the first group begins R0 (R2) at the barrier that ends the second
+// group's R3 (R1), so by then every wave has waited.
+template <class C, int MODE, bool IDX>
+__global__ __launch_bounds__(512, 2) void grouped_pair_kernel(GroupedArgs a) {
+  using K = Kernel<C, MODE, false>;
+  static_assert(C::W == 8 && C::ST == 2 && C::TT % 4 == 0 && K::kTD == 4 && K::kCD == 4,
+                "two groups of four waves, two stages, four phases, groups of two requests");
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * K::kStage + K::kIds + (kMaxE + 1 + 16) * 4];
+  uint8_t* ids = lds + 2 * K::kStage;
+  int* pre = reinterpret_cast<int*>(lds + 2 * K::kStage + K::kIds);
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / C::WN, wn = wave % C::WN;
+  const uint32_t lds0 = lds_addr_of(lds);
+  // requests made after those waited for, up to the wait (the row indices of
+  // step j + 3 go with R1): in R3 for groups 0 .. 2 (0 .. 1) of the next step,
+  // in R1 for the rest of this one
+  constexpr int kI = IDX ? 1 : 0;
+  constexpr int kAfterR3 = K::kTRows ? K::kGroup[3] + K::kGroup[0]
+                                     : K::kGroup[2] + kI + K::kGroup[3] + K::kGroup[0];
+  constexpr int kAfterR1 = K::kGroup[0] + K::kGroup[1] + K::kGroup[2] + kI;
+
+  Walk<K> w(a, pre, tid);
+  Tile x;
+  int steps, left;
+  typename K::Geo g;
+  // go on to the next tile that holds something and request its first step
+  auto start = [&]() {
+    if (!w.next(a, pre, lane, x, steps, left)) return false;
+    if (steps == 0) return true;
+    g = K::geometry(a, x, wave, lane);
+    if constexpr (IDX) {
+      K::template first_ids<3>(a, x, ids, wave, lane);
+      __syncthreads();
+    }
+    K::template issue_group<0, IDX>(a, x, g, lds0, ids, 0, wave, lane);
+    K::template issue_group<1, IDX>(a, x, g, lds0, ids, 0, wave, lane);
+    K::template issue_group<2, IDX>(a, x, g, lds0, ids, 0, wave, lane);
+    K::template issue_group<3, IDX>(a, x, g, lds0, ids, 0, wave, lane);
+    if (steps > 1) K::template issue_group<0, IDX>(a, x, g, lds0, ids, 1, wave, lane);
+    return true;
+  };
+
+  bool more = start();
+  while (more) {
     f32x4 acc[C::CT][C::TT];
 #pragma unroll
     for (int i = 0; i < C::CT; ++i)
@@ -446,37 +774,54 @@ __global__ __launch_bounds__(C::W * 64, C::MINB) void grouped_kernel(GroupedArgs
       for (int j = 0; j < C::TT; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
     if (steps > 0) {
-      const typename K::Geo g = K::geometry(a, x, wave, lane);
-      __syncthreads();                             // the last tile's stages have been read
-      if constexpr (IDX) {
-        for (int s = wave; s < C::ST - 1; s += C::W)
-          reinterpret_cast<int32_t*>(ids)[s * 64 + lane] = a.pairs[min(x.lo + 64 * s + lane, x.hi - 1)];
-        __syncthreads();
-      }
-#pragma unroll
-      for (int s = 0; s < C::ST - 1; ++s)
-        if (s < steps) K::template issue<IDX>(a, x, g, lds0 + s * K::kStage, ids, s, wave, lane);
-      int stage = 0;
-      for (int j = 0; j < steps; ++j) {
-        constexpr int kD = K::dmas(IDX);
-        const int after = min(C::ST - 2, steps - 1 - j);
-        if (after >= 2) dma_barrier<2 * kD>();
-        else if (after == 1) dma_barrier<kD>();
-        else dma_barrier<0>();
-        const int ahead = stage == 0 ? C::ST - 1 : stage - 1;
-        if (j + C::ST - 1 < steps)
-          K::template issue<IDX>(a, x, g, lds0 + ahead * K::kStage, ids, j + C::ST - 1, wave, lane);
-        const uint8_t* st = lds + stage * K::kStage;
-        if (tail && j == steps - 1) K::template compute<true>(st, wm, wn, lane, left, acc);
-        else K::template compute<false>(st, wm, wn, lane, left, acc);
-        stage = stage + 1 == C::ST ? 0 : stage + 1;
-      }
+      dma_barrier<0>();
+      if (wave >= 4) part_barrier();
+      typename K::Phase f;
+      // AHEAD: steps that follow, 2 for two or more; the last step may end inside
+      auto step = [&](auto ahead, int j) {
+        constexpr int kA = decltype(ahead)::value;
+        constexpr bool kT = kA == 0;
+        const uint8_t* st = lds + (j & 1) * K::kStage;
+        K::template phase_read<0, kT>(st, wm, wn, lane, left, f);
+        if constexpr (kA > 0) K::template issue_group<1, IDX>(a, x, g, lds0, ids, j + 1, wave, lane);
+        part_barrier();
+        phase_mul_fenced<K, 0>(f, acc);
+        K::template phase_read<1, kT>(st, wm, wn, lane, left, f);
+        if constexpr (kA > 0) {
+          if constexpr (IDX) K::issue_ids(a, x, ids, j + 3, lane);
+          K::template issue_group<2, IDX>(a, x, g, lds0, ids, j + 1, wave, lane);
+          land<kAfterR1>();
+        } else {
+          land<0>();
+        }
+        part_barrier();
+        phase_mul_fenced<K, 1>(f, acc);
+        K::template phase_read<2, kT>(st, wm, wn, lane, left, f);
+        if constexpr (kA > 0) K::template issue_group<3, IDX>(a, x, g, lds0, ids, j + 1, wave, lane);
+        part_barrier();
+        phase_mul_fenced<K, 2>(f, acc);
+        K::template phase_read<3, kT>(st, wm, wn, lane, left, f);
+        if constexpr (kA > 1) {
+          K::template issue_group<0, IDX>(a, x, g, lds0, ids, j + 2, wave, lane);
+          land<kAfterR3>();
+        } else {
+          land<0>();
+        }
+        part_barrier();
+        phase_mul_fenced<K, 3>(f, acc);
+      };
+      for (int j = 0; j < steps - 2; ++j) step(std::integral_constant<int, 2>{}, j);
+      if (steps > 1) step(std::integral_constant<int, 1>{}, steps - 2);
+      step(std::integral_constant<int, 0>{}, steps - 1);
+      if (wave < 4) part_barrier();                          // all fragments of the tile have been read
     }
-    K::epilogue(a, x, wm, wn, lane, acc);
+    const Tile done = x;
+    more = start();                                          // under way while the results are stored
+    K::epilogue(a, done, wm, wn, lane, acc);
   }
 }
 
-template <class C, int MODE, bool IDX>
+template <class C, int MODE, bool IDX, bool PAIR = false>
 hipError_t launch_as(GroupedArgs& a, int cus, hipStream_t s) {
   a.n_tiles = (a.N + C::BN - 1) / C::BN;
   int64_t tiles;
@@ -490,11 +835,86 @@ hipError_t launch_as(GroupedArgs& a, int cus, hipStream_t s) {
   const int64_t most = (int64_t)C::MINB * 4 / C::W * cus;    // resident workgroups
   int64_t grid = tiles < most ? tiles : most;
   if (grid > 8) grid = (grid + 7) / 8 * 8;
-  hipLaunchKernelGGL((grouped_kernel<C, MODE, IDX>), dim3((unsigned)grid), dim3(C::W * 64), 0, s, a);
+  if constexpr (PAIR) hipLaunchKernelGGL((grouped_pair_kernel<C, MODE, IDX>), dim3((unsigned)grid), dim3(512), 0, s, a);
+  else hipLaunchKernelGGL((grouped_kernel<C, MODE, IDX>), dim3((unsigned)grid), dim3(C::W * 64), 0, s, a);
   return hipGetLastError();
 }
 
+// Tile shapes.  With their stages two workgroups of the first two and three
+// of the third fit a CU, one of the last.
+using Small = Cfg<64, 64, 2, 2, 3, 2>;
 using Mid = Cfg<64, 128, 2, 2, 3, 2>;
+using Short = Cfg<64, 128, 2, 2, 2, 3>;
+using Large = Cfg<128, 128, 2, 2, 2, 2>;
+using Pair = Cfg<256, 256, 2, 4, 2, 2>;      // grouped_pair_kernel
+
+// Whether 32-bit offsets reach every row a tile of grouped_pair_kernel reads
+// (Kernel's WIDE): gathered rows from the start of their array, others from the
+// tile's first row (a step's 64, or the tile's 256).
+bool narrow_ok(GroupedMode mode, const GroupedArgs& a) {
+  const int64_t lim = (int64_t)1 << 32;
+  const auto fits = [&](const RowDiv& d, int64_t stride, int32_t rows) {
+    return (d.div && a.pairs ? (int64_t)rows : 256) * stride < lim;
+  };
+  if (!fits(a.t_div, a.t_stride, a.t_rows)) return false;
+  if (mode == kGWgrad && !fits(a.c_div, a.c_stride, a.c_rows)) return false;
+  return 256 * a.c_stride < lim && 256 * a.ts_stride * 4 < lim;
+}
+
+// The tile shape: the one whose rounds over the chip cost least, a round being
+// steps * (time of a step) + (first requests and last stores).  Times in us of
+// bf16 products on an MI355X (E4M3 ones are 1.35 times these for every shape),
+// with one workgroup a CU and with all that fit:
+//          one    all    fixed
+//   Small  0.45   0.46   3       Mid  0.53   0.72   3
+//   Large  0.80   1.20   4       Pair 1.35   1.75   8
+// So measured (Small / Mid / Large / Pair, k 3584 bf16, 3584 columns): 64 rows
+// 28 / 32 / 44 / 68 us, 1024 rows 63 / 45 / 50 / 77, 2048 rows 113 / 80 / 66 /
+// 81, 4096 rows 208 / 147 / 133 / 96.
+// Up to two steps the fixed part is all and three workgroups of Short beside
+// each other hide it best: 16384 rows in 112 groups, 768 columns, k 32: 20 us
+// against 24 of Mid.
+// Groups are taken to hold rows / experts each and to end inside a tile.
+enum Shape { kSmall, kMid, kShort, kLarge, kPair };
+Shape choose(GroupedMode mode, const GroupedArgs& a, int cus) {
+  const bool wg = mode == kGWgrad;
+  const int q = mode == kGFwd8 || mode == kGFwd8x ? 128 : 64;
+  const double mean = (double)a.rows / a.experts;
+  const double steps = wg ? mean / 64 + 0.5 : (double)((a.K + q - 1) / q);
+  if (steps <= 2) return kShort;
+  struct Cost { Shape shape; int bm, bn, per_cu; double one, all, fixed; };
+  constexpr Cost kCosts[] = {{kSmall, 64, 64, 2, 0.45, 0.46, 3}, {kMid, 64, 128, 2, 0.53, 0.72, 3},
+                             {kLarge, 128, 128, 2, 0.80, 1.20, 4}, {kPair, 256, 256, 1, 1.35, 1.75, 8}};
+  Shape best = kSmall;
+  double least = 1e30;
+  for (const Cost& c : kCosts) {
+    if (c.shape == kPair && (mode == kGFwd8x || !narrow_ok(mode, a))) continue;
+    double m;
+    if (wg) m = (double)((a.M + c.bm - 1) / c.bm) * a.experts;
+    else if (!a.offsets) m = (a.rows + c.bm - 1) / c.bm;
+    else m = a.experts * std::max(1.0, mean / c.bm + 0.5);
+    const double tiles = m * ((a.N + c.bn - 1) / c.bn), slots = (double)cus * c.per_cu;
+    const double cost = std::ceil(tiles / slots) * (steps * (tiles <= cus ? c.one : c.all) + c.fixed);
+    if (cost < least) {
+      least = cost;
+      best = c.shape;
+    }
+  }
+  return best;
+}
+
+template <int MODE, bool IDX>
+hipError_t launch_mode(GroupedArgs& a, int cus, hipStream_t s) {
+  switch (choose((GroupedMode)MODE, a, cus)) {
+    case kSmall: return launch_as<Small, MODE, IDX>(a, cus, s);
+    case kMid: return launch_as<Mid, MODE, IDX>(a, cus, s);
+    case kShort: return launch_as<Short, MODE, IDX>(a, cus, s);
+    case kLarge: return launch_as<Large, MODE, IDX>(a, cus, s);
+    case kPair:
+      if constexpr (MODE != kGFwd8x) return launch_as<Pair, MODE, IDX, true>(a, cus, s);
+  }
+  return hipErrorInvalidValue;
+}
 
 }  // namespace
 
@@ -502,15 +922,15 @@ hipError_t launch_grouped(GroupedMode mode, GroupedArgs& a, int cus, hipStream_t
   if (mode == kGFwd8 && a.out_f32) mode = kGFwd8x;
   if ((mode == kGFwd || mode == kGFwd8 || mode == kGFwd8x) && few_rows(a)) return launch_grouped_few(mode, a, cus, s);
   switch (mode) {
-    case kGFwd: return launch_as<Mid, kGFwd, false>(a, cus, s);
-    case kGFwd8: return launch_as<Mid, kGFwd8, false>(a, cus, s);
-    case kGFwd8x: return launch_as<Mid, kGFwd8x, false>(a, cus, s);
-    case kGDgrad: return launch_as<Mid, kGDgrad, false>(a, cus, s);
+    case kGFwd: return launch_mode<kGFwd, false>(a, cus, s);
+    case kGFwd8: return launch_mode<kGFwd8, false>(a, cus, s);
+    case kGFwd8x: return launch_mode<kGFwd8x, false>(a, cus, s);
+    case kGDgrad: return launch_mode<kGDgrad, false>(a, cus, s);
     case kGWgrad:
-      if (a.pairs && (a.t_div.div || a.c_div.div)) return launch_as<Mid, kGWgrad, true>(a, cus, s);
-      return launch_as<Mid, kGWgrad, false>(a, cus, s);
-    default: return hipErrorInvalidValue;
+      if (a.pairs && (a.t_div.div || a.c_div.div)) return launch_mode<kGWgrad, true>(a, cus, s);
+      return launch_mode<kGWgrad, false>(a, cus, s);
   }
+  return hipErrorInvalidValue;
 }
 
 }  // namespace situ

@@ -39,15 +39,14 @@ __device__ __forceinline__ void store4(const GroupedArgs& a, uint8_t* row, int c
     }
   } else {
     uint16_t* o = reinterpret_cast<uint16_t*>(row) + col;
-    uint32_t b[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) b[k] = f32_to_bf16_rne(v[k]);
+    const bf16x2 lo = {(__bf16)v[0], (__bf16)v[1]}, hi = {(__bf16)v[2], (__bf16)v[3]};   // nearest even
+    const uint2 b = make_uint2(__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi));
     if (a.vec && col + 4 <= a.N) {
-      *reinterpret_cast<uint2*>(o) = make_uint2(b[0] | b[1] << 16, b[2] | b[3] << 16);
+      *reinterpret_cast<uint2*>(o) = b;
     } else {
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        if (col + k < a.N) o[k] = (uint16_t)b[k];
+        if (col + k < a.N) o[k] = (uint16_t)((k < 2 ? b.x : b.y) >> (16 * (k & 1)));
     }
   }
 }
