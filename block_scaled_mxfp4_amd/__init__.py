@@ -111,10 +111,10 @@ def load():
         "situ_moe_quantize_mxfp8": (c_int, [vp, c_i64, c_int, vp, vp, vp]),
         "situ_moe_tile_weights": (c_int, [vp, vp, c_int, c_int, c_int, vp, vp, vp]),
         "situ_moe_quantize_fp8_block128": (c_int, [vp, c_i64, c_int, c_i64, vp, vp, vp]),
-        "situ_moe_matmul_fp8_block128": (c_int, [P(SituMoeFp8Matmul), vp]),
-        "situ_moe_grouped_matmul": (c_int, [P(SituMoeGrouped), vp]),
-        "situ_moe_grouped_matmul_dgrad": (c_int, [P(SituMoeGrouped), vp]),
-        "situ_moe_grouped_matmul_wgrad": (c_int, [P(SituMoeGrouped), vp]),
+        "situ_moe_matmul_fp8_block128": (c_int, [vp, vp]),
+        "situ_moe_grouped_matmul": (c_int, [vp, vp]),
+        "situ_moe_grouped_matmul_dgrad": (c_int, [vp, vp]),
+        "situ_moe_grouped_matmul_wgrad": (c_int, [vp, vp]),
         "situ_moe_measure_mfma_peak": (c_int, [c_int, P(ctypes.c_double)]),
         "situ_moe_status_string": (ctypes.c_char_p, [c_int]),
         "situ_moe_last_error": (ctypes.c_char_p, []),

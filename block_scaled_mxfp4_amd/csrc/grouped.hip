@@ -881,7 +881,7 @@ Shape choose(GroupedMode mode, const GroupedArgs& a, int cus) {
   const int q = mode == kGFwd8 || mode == kGFwd8x ? 128 : 64;
   const double mean = (double)a.rows / a.experts;
   const double steps = wg ? mean / 64 + 0.5 : (double)((a.K + q - 1) / q);
-  if (steps <= 2) return kShort;
+  if (steps <= 2 && !wg) return kShort;
   struct Cost { Shape shape; int bm, bn, per_cu; double one, all, fixed; };
   constexpr Cost kCosts[] = {{kSmall, 64, 64, 2, 0.45, 0.46, 3}, {kMid, 64, 128, 2, 0.53, 0.72, 3},
                              {kLarge, 128, 128, 2, 0.80, 1.20, 4}, {kPair, 256, 256, 1, 1.35, 1.75, 8}};
