@@ -134,6 +134,11 @@ struct Kernel {
     else gdma16s(base, off, lds);
   }
 
+  // The swizzle of C changes with every other eight rows: only a wave alone has both kinds.
+  static __device__ __forceinline__ int c_chunk_of(const Geo& g, int i) {
+    return C::W % 2 && i % 2 ? g.c_chunk ^ 64 : g.c_chunk;
+  }
+
   static __device__ __forceinline__ Geo geometry(const GroupedArgs& a, const Tile& x, int wave, int lane) {
     Geo g{};
     if constexpr (kTRows) {
@@ -157,11 +162,11 @@ struct Kernel {
     }
     if constexpr (kCRows) {
       g.cb = a.c + (int64_t)x.e * a.c_expert + (int64_t)x.n0 * a.c_stride;
-      g.c_chunk = ((lane & 7) ^ swz_c(8 * wave + (lane >> 3))) * 16;   // W is even: the same for every i
+      g.c_chunk = ((lane & 7) ^ swz_c(8 * wave + (lane >> 3))) * 16;   // of block 0: c_chunk_of
 #pragma unroll
       for (int i = 0; i < kCD; ++i) {
         const int n = min((wave + C::W * i) * 8 + (lane >> 3), a.N - 1 - x.n0);
-        g.c[i] = (Off)n * (Off)a.c_stride + g.c_chunk;
+        g.c[i] = (Off)n * (Off)a.c_stride + c_chunk_of(g, i);
       }
     } else {
       g.cb = a.c + (kWg ? 0 : (int64_t)x.e * a.c_expert);
@@ -218,7 +223,7 @@ struct Kernel {
                                                  const uint8_t* ids, int j, int i, int wave, int lane) {
     const uint32_t to = st + kTBytes + (wave + C::W * i) * 1024;
     const int r = ((wave + C::W * i) * 64 + lane) / (C::BN / 8);
-    if constexpr (kCRows) request(g.cb, chunk_at(a, j, g.c_chunk, g.c[i]), to);
+    if constexpr (kCRows) request(g.cb, chunk_at(a, j, c_chunk_of(g, i), g.c[i]), to);
     else if constexpr (kWg) request_q<IDX>(a, x, a.c_div, g.cb, a.c_stride, a.c_rows, ids, j, r, g.c[i], to);
     else request(g.cb + (int64_t)(64 * j) * a.c_stride, (Off)min(r, a.K - 1 - 64 * j) * (Off)a.c_stride + g.c[i], to);
   }
@@ -487,22 +492,27 @@ struct Kernel {
     if constexpr (G == 2) issue_s(g, st, j, wave);
   }
 
+  // Where row tile j (of the workgroup's tile) goes in this lane; null if nowhere.
+  static __device__ __forceinline__ uint8_t* out_row(const GroupedArgs& a, const Tile& x, int j, int lane) {
+    const int t = x.m0 + 16 * j + (lane & 15);
+    if (t >= (kWg ? a.M : x.hi)) return nullptr;
+    const int row = kWg ? t : index_row(a.o_div, a.pairs, t, a.o_rows);
+    if (row < 0) return nullptr;
+    return static_cast<uint8_t*>(a.out) + (kWg ? (int64_t)x.e * a.out_expert : 0) + (int64_t)row * a.out_stride;
+  }
+  // The first of the four columns of column tile i that this lane holds.
+  static __device__ __forceinline__ int out_col(const Tile& x, int i, int lane) {
+    const int g = lane >> 4;
+    return x.n0 + (kCRows ? 16 * (i & ~1) + 8 * g + 4 * (i & 1) : 16 * i + 4 * g);
+  }
   static __device__ __forceinline__ void epilogue(const GroupedArgs& a, const Tile& x, int wm, int wn, int lane,
                                                   f32x4 (&acc)[C::CT][C::TT]) {
-    const int l = lane & 15, g = lane >> 4;
 #pragma unroll
     for (int j = 0; j < C::TT; ++j) {
-      const int t = x.m0 + 16 * (wm * C::TT + j) + l;
-      if (t >= (kWg ? a.M : x.hi)) continue;
-      const int row = kWg ? t : index_row(a.o_div, a.pairs, t, a.o_rows);
-      if (row < 0) continue;
-      uint8_t* o = static_cast<uint8_t*>(a.out) + (kWg ? (int64_t)x.e * a.out_expert : 0) + (int64_t)row * a.out_stride;
-      const int n0 = x.n0 + 16 * wn * C::CT;
+      uint8_t* o = out_row(a, x, wm * C::TT + j, lane);
+      if (!o) continue;
 #pragma unroll
-      for (int i = 0; i < C::CT; ++i) {
-        const int col = n0 + (kCRows ? 16 * (i & ~1) + 8 * g + 4 * (i & 1) : 16 * i + 4 * g);
-        store4(a, o, col, acc[i][j]);
-      }
+      for (int i = 0; i < C::CT; ++i) store4(a, o, out_col(x, wn * C::CT + i, lane), acc[i][j]);
     }
   }
 };
@@ -578,11 +588,12 @@ struct Walk {
   int m_tiles, slots;
   int64_t it, last;
 
-  __device__ __forceinline__ Walk(const GroupedArgs& a, int* pre, int tid) {
+  template <int NT>
+  __device__ __forceinline__ Walk(const GroupedArgs& a, int* pre, int tid, std::integral_constant<int, NT>) {
     if constexpr (K::kWg) {
       m_tiles = a.experts * a.m_bound;
     } else if (a.offsets) {
-      tile_prefix<K::kThreads>(a, C::BM, pre, pre + kMaxE + 1, tid);
+      tile_prefix<NT>(a, C::BM, pre, pre + kMaxE + 1, tid);
       m_tiles = min(pre[a.experts], a.m_bound);   // ascending offsets never exceed the bound
     } else {
       m_tiles = a.m_bound;
@@ -653,7 +664,7 @@ __global__ __launch_bounds__(C::W * 64, C::MINB) void grouped_kernel(GroupedArgs
   const int wm = wave / C::WN, wn = wave % C::WN;
   const uint32_t lds0 = lds_addr_of(lds);
 
-  Walk<K> w(a, pre, tid);
+  Walk<K> w(a, pre, tid, std::integral_constant<int, K::kThreads>{});
   Tile x;
   int steps, left;
   typename K::Geo g;
@@ -703,6 +714,78 @@ __global__ __launch_bounds__(C::W * 64, C::MINB) void grouped_kernel(GroupedArgs
   }
 }
 
+// Few tiles, long contractions: the waves of a workgroup split q between them,
+// wave w taking steps w, w + KS, ... of the same tile with stages of its own,
+// so there is no barrier in the loop; the partial sums are added in LDS in the
+// waves' order.  With one tile a CU the kernel above spends 0.45 us on a step
+// of 64 x 64 (barrier, requests, LDS and MFMA latency in turn); here KS steps
+// are under way at once.
+template <class C, int MODE, int KS>
+__global__ __launch_bounds__(KS * 64, 1) void grouped_split_kernel(GroupedArgs a) {
+  using K = Kernel<C, MODE, true>;
+  static_assert(C::W == 1, "a wave computes the whole tile");
+  constexpr int kStages = KS * C::ST * K::kStage, kSums = KS * C::CT * C::TT * 1024;
+  static_assert(kSums <= kStages, "the sums fit the stages");
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[kStages + (kMaxE + 1 + 16) * 4];
+  int* pre = reinterpret_cast<int*>(lds + kStages);
+  const int tid = threadIdx.x, lane = tid & 63, wk = __builtin_amdgcn_readfirstlane(tid >> 6);
+  uint8_t* own = lds + wk * C::ST * K::kStage;
+  const uint32_t own0 = lds_addr_of(own);
+  f32x4* sums = reinterpret_cast<f32x4*>(lds);
+  constexpr int kD = K::dmas(false);
+
+  Walk<K> w(a, pre, tid, std::integral_constant<int, KS * 64>{});
+  Tile x;
+  int steps, left;
+  while (w.next(a, pre, lane, x, steps, left)) {
+    f32x4 acc[C::CT][C::TT];
+#pragma unroll
+    for (int i = 0; i < C::CT; ++i)
+#pragma unroll
+      for (int j = 0; j < C::TT; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    const int mine = wk < steps ? (steps - wk + KS - 1) / KS : 0;   // steps of this wave
+    if (mine > 0) {
+      const typename K::Geo g = K::geometry(a, x, 0, lane);
+#pragma unroll
+      for (int s = 0; s < C::ST - 1; ++s)
+        if (s < mine) K::template issue<false>(a, x, g, own0 + s * K::kStage, nullptr, wk + s * KS, 0, lane);
+      int stage = 0;
+      for (int u = 0; u < mine; ++u) {
+        const int j = wk + u * KS;
+        const int ahead = stage == 0 ? C::ST - 1 : stage - 1;
+        // the stage ahead was read a step ago, and its fragments have arrived
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        if (u + C::ST - 1 < mine) {
+          K::template issue<false>(a, x, g, own0 + ahead * K::kStage, nullptr, j + (C::ST - 1) * KS, 0, lane);
+          land<(C::ST - 1) * kD>();
+        } else {
+          land<0>();
+        }
+        const uint8_t* st = own + stage * K::kStage;
+        if (j == steps - 1) K::template compute<true>(st, 0, 0, lane, left, acc);
+        else K::template compute<false>(st, 0, 0, lane, left, acc);
+        stage = stage + 1 == C::ST ? 0 : stage + 1;
+      }
+    }
+    __syncthreads();                               // the stages have been read
+#pragma unroll
+    for (int i = 0; i < C::CT; ++i)
+#pragma unroll
+      for (int j = 0; j < C::TT; ++j) sums[((wk * C::CT + i) * C::TT + j) * 64 + lane] = acc[i][j];
+    __syncthreads();
+    for (int q = wk; q < C::CT * C::TT; q += KS) {
+      const int i = q / C::TT, j = q % C::TT;
+      uint8_t* o = K::out_row(a, x, j, lane);
+      if (!o) continue;
+      f32x4 v = sums[q * 64 + lane];
+#pragma unroll
+      for (int s = 1; s < KS; ++s) v += sums[(s * C::CT * C::TT + q) * 64 + lane];
+      store4(a, o, K::out_col(x, i, lane), v);
+    }
+    __syncthreads();                               // the sums have been read
+  }
+}
+
 // Large tiles: two groups of four waves, one wave of each on every SIMD, take
 // turns.  A step has four phases, each a reading part R (fragments from LDS,
 // requests for later steps) and a multiplying part M (1/4 of the step's
@@ -744,7 +827,7 @@ __global__ __launch_bounds__(512, 2) void grouped_pair_kernel(GroupedArgs a) {
                                      : K::kGroup[2] + kI + K::kGroup[3] + K::kGroup[0];
   constexpr int kAfterR1 = K::kGroup[0] + K::kGroup[1] + K::kGroup[2] + kI;
 
-  Walk<K> w(a, pre, tid);
+  Walk<K> w(a, pre, tid, std::integral_constant<int, K::kThreads>{});
   Tile x;
   int steps, left;
   typename K::Geo g;
@@ -821,7 +904,8 @@ __global__ __launch_bounds__(512, 2) void grouped_pair_kernel(GroupedArgs a) {
   }
 }
 
-template <class C, int MODE, bool IDX, bool PAIR = false>
+// KS: waves that split q (grouped_split_kernel); 0: grouped_kernel, -1: grouped_pair_kernel.
+template <class C, int MODE, bool IDX, int KS = 0>
 hipError_t launch_as(GroupedArgs& a, int cus, hipStream_t s) {
   a.n_tiles = (a.N + C::BN - 1) / C::BN;
   int64_t tiles;
@@ -832,10 +916,11 @@ hipError_t launch_as(GroupedArgs& a, int cus, hipStream_t s) {
     a.m_bound = a.offsets ? a.rows / C::BM + a.experts : (a.rows + C::BM - 1) / C::BM;
     tiles = (int64_t)a.m_bound * a.n_tiles;
   }
-  const int64_t most = (int64_t)C::MINB * 4 / C::W * cus;    // resident workgroups
+  const int64_t most = KS > 0 ? cus : (int64_t)C::MINB * 4 / C::W * cus;   // resident workgroups
   int64_t grid = tiles < most ? tiles : most;
   if (grid > 8) grid = (grid + 7) / 8 * 8;
-  if constexpr (PAIR) hipLaunchKernelGGL((grouped_pair_kernel<C, MODE, IDX>), dim3((unsigned)grid), dim3(512), 0, s, a);
+  if constexpr (KS > 0) hipLaunchKernelGGL((grouped_split_kernel<C, MODE, KS>), dim3((unsigned)grid), dim3(KS * 64), 0, s, a);
+  else if constexpr (KS < 0) hipLaunchKernelGGL((grouped_pair_kernel<C, MODE, IDX>), dim3((unsigned)grid), dim3(512), 0, s, a);
   else hipLaunchKernelGGL((grouped_kernel<C, MODE, IDX>), dim3((unsigned)grid), dim3(C::W * 64), 0, s, a);
   return hipGetLastError();
 }
@@ -847,6 +932,8 @@ using Mid = Cfg<64, 128, 2, 2, 3, 2>;
 using Short = Cfg<64, 128, 2, 2, 2, 3>;
 using Large = Cfg<128, 128, 2, 2, 2, 2>;
 using Pair = Cfg<256, 256, 2, 4, 2, 2>;      // grouped_pair_kernel
+using Split = Cfg<64, 32, 1, 1, 3, 1>;       // grouped_split_kernel, four waves
+using Split2 = Cfg<64, 64, 1, 1, 2, 1>;
 
 // Whether 32-bit offsets reach every row a tile of grouped_pair_kernel reads
 // (Kernel's WIDE): gathered rows from the start of their array, others from the
@@ -868,6 +955,10 @@ bool narrow_ok(GroupedMode mode, const GroupedArgs& a) {
 //          one    all    fixed
 //   Small  0.45   0.46   3       Mid  0.53   0.72   3
 //   Large  0.80   1.20   4       Pair 1.35   1.75   8
+//   Split  0.14          8       Split2 0.20        9
+// Split pays where its tiles are no more than the CUs: 64 rows, k 3584 bf16,
+// 3584 columns 17 us against 27 of Small; with 8192 columns and 128 rows
+// Split2 24, Small 31, Split 31.
 // So measured (Small / Mid / Large / Pair, k 3584 bf16, 3584 columns): 64 rows
 // 28 / 32 / 44 / 68 us, 1024 rows 63 / 45 / 50 / 77, 2048 rows 113 / 80 / 66 /
 // 81, 4096 rows 208 / 147 / 133 / 96.
@@ -875,7 +966,7 @@ bool narrow_ok(GroupedMode mode, const GroupedArgs& a) {
 // each other hide it best: 16384 rows in 112 groups, 768 columns, k 32: 20 us
 // against 24 of Mid.
 // Groups are taken to hold rows / experts each and to end inside a tile.
-enum Shape { kSmall, kMid, kShort, kLarge, kPair };
+enum Shape { kSmall, kMid, kShort, kLarge, kPair, kSplit, kSplit2 };
 Shape choose(GroupedMode mode, const GroupedArgs& a, int cus) {
   const bool wg = mode == kGWgrad;
   const int q = mode == kGFwd8 || mode == kGFwd8x ? 128 : 64;
@@ -884,11 +975,13 @@ Shape choose(GroupedMode mode, const GroupedArgs& a, int cus) {
   if (steps <= 2 && !wg) return kShort;
   struct Cost { Shape shape; int bm, bn, per_cu; double one, all, fixed; };
   constexpr Cost kCosts[] = {{kSmall, 64, 64, 2, 0.45, 0.46, 3}, {kMid, 64, 128, 2, 0.53, 0.72, 3},
-                             {kLarge, 128, 128, 2, 0.80, 1.20, 4}, {kPair, 256, 256, 1, 1.35, 1.75, 8}};
+                             {kLarge, 128, 128, 2, 0.80, 1.20, 4}, {kPair, 256, 256, 1, 1.35, 1.75, 8},
+                             {kSplit, 64, 32, 1, 0.14, 0.14, 8},   {kSplit2, 64, 64, 1, 0.20, 0.20, 9}};
   Shape best = kSmall;
   double least = 1e30;
   for (const Cost& c : kCosts) {
     if (c.shape == kPair && (mode == kGFwd8x || !narrow_ok(mode, a))) continue;
+    if ((c.shape == kSplit || c.shape == kSplit2) && wg && a.pairs) continue;   // row indices are shared by waves
     double m;
     if (wg) m = (double)((a.M + c.bm - 1) / c.bm) * a.experts;
     else if (!a.offsets) m = (a.rows + c.bm - 1) / c.bm;
@@ -910,8 +1003,14 @@ hipError_t launch_mode(GroupedArgs& a, int cus, hipStream_t s) {
     case kMid: return launch_as<Mid, MODE, IDX>(a, cus, s);
     case kShort: return launch_as<Short, MODE, IDX>(a, cus, s);
     case kLarge: return launch_as<Large, MODE, IDX>(a, cus, s);
+    case kSplit:
+      if constexpr (!IDX) return launch_as<Split, MODE, IDX, 4>(a, cus, s);
+      break;
+    case kSplit2:
+      if constexpr (!IDX) return launch_as<Split2, MODE, IDX, 4>(a, cus, s);
+      break;
     case kPair:
-      if constexpr (MODE != kGFwd8x) return launch_as<Pair, MODE, IDX, true>(a, cus, s);
+      if constexpr (MODE != kGFwd8x) return launch_as<Pair, MODE, IDX, -1>(a, cus, s);
   }
   return hipErrorInvalidValue;
 }
