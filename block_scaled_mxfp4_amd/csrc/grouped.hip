@@ -107,7 +107,7 @@ struct Kernel {
   static constexpr int kStage = kTBytes + kCBytes + kSBytes;
   static constexpr int kTD = C::BM / 8 / C::W, kCD = C::BN / 8 / C::W;   // DMAs of a wave and step
   static constexpr int kThreads = C::W * 64;
-  static constexpr int kIds = kWg ? 8 * 64 * 4 : 0;             // ring of row indices, 64 per step
+  static constexpr int kIds = kWg ? 8 * 64 * 4 : 0;             // ring of row indices, 64 per step (IDX)
   static constexpr int kTW = (C::BM + 63) / 64, kSD = kF8 ? (kTW + C::W) / C::W : 0;   // blocks of row scales, scale DMAs of a wave
 
   // Byte offset, within an operand stored as 64 rows of q and R columns, of
@@ -141,6 +141,12 @@ struct Kernel {
 
   static __device__ __forceinline__ Geo geometry(const GroupedArgs& a, const Tile& x, int wave, int lane) {
     Geo g{};
+    geometry_t(a, x, g, wave, lane);
+    geometry_c(a, x, g, wave, lane);
+    geometry_s(a, x, g, wave, lane);
+    return g;
+  }
+  static __device__ __forceinline__ void geometry_t(const GroupedArgs& a, const Tile& x, Geo& g, int wave, int lane) {
     if constexpr (kTRows) {
       const bool near = !WIDE && a.t_div.div == 0;             // rows from the tile's first one
       g.tb = a.t + (near ? (int64_t)x.m0 * a.t_stride : 0);
@@ -160,6 +166,8 @@ struct Kernel {
         g.t[i] = 2 * (col < a.M ? col : 0);
       }
     }
+  }
+  static __device__ __forceinline__ void geometry_c(const GroupedArgs& a, const Tile& x, Geo& g, int wave, int lane) {
     if constexpr (kCRows) {
       g.cb = a.c + (int64_t)x.e * a.c_expert + (int64_t)x.n0 * a.c_stride;
       g.c_chunk = ((lane & 7) ^ swz_c(8 * wave + (lane >> 3))) * 16;   // of block 0: c_chunk_of
@@ -177,6 +185,8 @@ struct Kernel {
         g.c[i] = 2 * (col < a.N ? col : 0);
       }
     }
+  }
+  static __device__ __forceinline__ void geometry_s(const GroupedArgs& a, const Tile& x, Geo& g, int wave, int lane) {
 #pragma unroll
     for (int i = 0; i < kSD; ++i) {
       const int b = wave + C::W * i;
@@ -190,7 +200,6 @@ struct Kernel {
         g.s[i] = (uint32_t)min(lane, nb - 1 - n) * (uint32_t)kb * 4u;
       }
     }
-    return g;
   }
 
   // The row indices of the first N steps (kGWgrad).
@@ -505,29 +514,54 @@ struct Kernel {
     const int g = lane >> 4;
     return x.n0 + (kCRows ? 16 * (i & ~1) + 8 * g + 4 * (i & 1) : 16 * i + 4 * g);
   }
-  static __device__ __forceinline__ void epilogue(const GroupedArgs& a, const Tile& x, int wm, int wn, int lane,
-                                                  f32x4 (&acc)[C::CT][C::TT]) {
+  // Where the wave's row tiles go, all looked up before the first store.
+  static __device__ __forceinline__ void out_rows(const GroupedArgs& a, const Tile& x, int wm, int lane,
+                                                  uint8_t* (&o)[C::TT]) {
+#pragma unroll
+    for (int j = 0; j < C::TT; ++j) o[j] = out_row(a, x, wm * C::TT + j, lane);
+  }
+  static __device__ __forceinline__ void epilogue(const GroupedArgs& a, const Tile& x, int wn, int lane,
+                                                  uint8_t* const (&o)[C::TT], f32x4 (&acc)[C::CT][C::TT]) {
 #pragma unroll
     for (int j = 0; j < C::TT; ++j) {
-      uint8_t* o = out_row(a, x, wm * C::TT + j, lane);
-      if (!o) continue;
+      if (!o[j]) continue;
 #pragma unroll
-      for (int i = 0; i < C::CT; ++i) store4(a, o, out_col(x, wn * C::CT + i, lane), acc[i][j]);
+      for (int i = 0; i < C::CT; i += 2) {
+        if constexpr (kCRows) {
+          store8(a, o[j], out_col(x, wn * C::CT + i, lane), acc[i][j], acc[i + 1][j]);
+        } else {
+          store4(a, o[j], out_col(x, wn * C::CT + i, lane), acc[i][j]);
+          store4(a, o[j], out_col(x, wn * C::CT + i + 1, lane), acc[i + 1][j]);
+        }
+      }
     }
   }
 };
 
-// Exclusive prefix of the groups' row tiles in pre[0 .. E].
-template <int NT>
-__device__ __forceinline__ void tile_prefix(const GroupedArgs& a, int bm, int* pre, int* part, int tid) {
+// The groups of a launch, kept in LDS (a second array would cost Mid and Short
+// a workgroup a CU): the exclusive prefix of their row tiles (of BM rows), or
+// (kGWgrad) where each begins.
+struct Table {
+  int at[kMaxE + 1], part[16];
+};
+
+template <int NT, int BM, bool FIRST>
+__device__ __forceinline__ void make_table(const GroupedArgs& a, Table& t, int tid) {
   constexpr int kPer = kMaxE / NT;
+  int at_e[kPer + 1];
+#pragma unroll
+  for (int i = 0; i <= kPer; ++i) at_e[i] = min(max(a.offsets[min(tid * kPer + i, a.experts)], 0), a.rows);
+  if constexpr (FIRST) {
+#pragma unroll
+    for (int i = 0; i <= kPer; ++i)
+      if (tid * kPer + i <= a.experts) t.at[tid * kPer + i] = at_e[i];
+    __syncthreads();
+    return;
+  }
   int cnt[kPer], sum = 0;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    const int e = tid * kPer + i;
-    int lo = 0, hi = 0;
-    if (e < a.experts) group_rows(a, e, lo, hi);
-    cnt[i] = (hi - lo + bm - 1) / bm;
+    cnt[i] = tid * kPer + i < a.experts ? (max(at_e[i + 1] - at_e[i], 0) + BM - 1) / BM : 0;
     sum += cnt[i];
   }
   int inc = sum;
@@ -536,17 +570,16 @@ __device__ __forceinline__ void tile_prefix(const GroupedArgs& a, int bm, int* p
     const int up = __shfl_up(inc, d, kWave);
     if ((tid & 63) >= d) inc += up;
   }
-  if ((tid & 63) == 63) part[tid >> 6] = inc;
+  if ((tid & 63) == 63) t.part[tid >> 6] = inc;
   __syncthreads();
   int at = inc - sum;
-  for (int w = 0; w < (tid >> 6); ++w) at += part[w];
+  for (int w = 0; w < (tid >> 6); ++w) at += t.part[w];
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    const int e = tid * kPer + i;
-    if (e <= a.experts) pre[e] = at;
+    if (tid * kPer + i <= a.experts) t.at[tid * kPer + i] = at;
     at += cnt[i];
   }
-  if (tid == NT - 1 && a.experts == kMaxE) pre[kMaxE] = at;
+  if (tid == NT - 1 && a.experts == kMaxE) t.at[kMaxE] = at;
   __syncthreads();
 }
 
@@ -589,12 +622,12 @@ struct Walk {
   int64_t it, last;
 
   template <int NT>
-  __device__ __forceinline__ Walk(const GroupedArgs& a, int* pre, int tid, std::integral_constant<int, NT>) {
+  __device__ __forceinline__ Walk(const GroupedArgs& a, Table& t, int tid, std::integral_constant<int, NT>) {
+    if (a.offsets) make_table<NT, C::BM, K::kWg>(a, t, tid);
     if constexpr (K::kWg) {
       m_tiles = a.experts * a.m_bound;
     } else if (a.offsets) {
-      tile_prefix<NT>(a, C::BM, pre, pre + kMaxE + 1, tid);
-      m_tiles = min(pre[a.experts], a.m_bound);   // ascending offsets never exceed the bound
+      m_tiles = min(t.at[a.experts], a.m_bound);   // ascending offsets never exceed the bound
     } else {
       m_tiles = a.m_bound;
     }
@@ -607,9 +640,9 @@ struct Walk {
   }
 
   // Moves on to the next tile that holds something; false if there is none.
-  __device__ __forceinline__ bool next(const GroupedArgs& a, const int* pre, int lane, Tile& x, int& steps, int& left) {
+  __device__ __forceinline__ bool next(const GroupedArgs& a, const Table& t, int lane, Tile& x, int& steps, int& left) {
     for (; it < last; it += slots) {
-      if (tile(a, pre, lane, x, steps, left)) {
+      if (tile(a, t, lane, x, steps, left)) {
         it += slots;
         return true;
       }
@@ -618,14 +651,15 @@ struct Walk {
   }
 
   // The tile `it`; false if it holds nothing (only with offsets that do not ascend).
-  __device__ __forceinline__ bool tile(const GroupedArgs& a, const int* pre, int lane, Tile& x, int& steps, int& left) {
+  __device__ __forceinline__ bool tile(const GroupedArgs& a, const Table& t, int lane, Tile& x, int& steps, int& left) {
     if constexpr (K::kWg) {
       const int per = a.m_bound * a.n_tiles;
       x.e = (int)(it / per);
       const int r = (int)(it % per);
       x.m0 = (r % a.m_bound) * C::BM;
       x.n0 = (r / a.m_bound) * C::BN;
-      group_rows(a, x.e, x.lo, x.hi);
+      x.lo = a.offsets ? t.at[x.e] : 0;
+      x.hi = a.offsets ? max(t.at[x.e + 1], x.lo) : a.rows;
       steps = (x.hi - x.lo + 63) / 64;
       left = x.hi - x.lo - 64 * (steps - 1);
       return true;
@@ -633,9 +667,9 @@ struct Walk {
       // within a group: eight row tiles by all column tiles, rows fastest
       int local, m_l;
       if (a.offsets) {
-        x.e = __builtin_amdgcn_readfirstlane(find_group(pre, a.experts, (int)(it / a.n_tiles), lane));
-        local = (int)(it - (int64_t)pre[x.e] * a.n_tiles);
-        m_l = pre[x.e + 1] - pre[x.e];
+        x.e = __builtin_amdgcn_readfirstlane(find_group(t.at, a.experts, (int)(it / a.n_tiles), lane));
+        local = (int)(it - (int64_t)t.at[x.e] * a.n_tiles);
+        m_l = t.at[x.e + 1] - t.at[x.e];
       } else {
         x.e = 0;
         local = (int)it;
@@ -657,20 +691,20 @@ struct Walk {
 template <class C, int MODE, bool IDX>
 __global__ __launch_bounds__(C::W * 64, C::MINB) void grouped_kernel(GroupedArgs a) {
   using K = Kernel<C, MODE, true>;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[C::ST * K::kStage + K::kIds + (kMaxE + 1 + 16) * 4];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[C::ST * K::kStage + K::kIds + sizeof(Table)];
   uint8_t* ids = lds + C::ST * K::kStage;
-  int* pre = reinterpret_cast<int*>(lds + C::ST * K::kStage + K::kIds);
+  Table& table = *reinterpret_cast<Table*>(lds + C::ST * K::kStage + K::kIds);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / C::WN, wn = wave % C::WN;
   const uint32_t lds0 = lds_addr_of(lds);
 
-  Walk<K> w(a, pre, tid, std::integral_constant<int, K::kThreads>{});
+  Walk<K> w(a, table, tid, std::integral_constant<int, K::kThreads>{});
   Tile x;
   int steps, left;
   typename K::Geo g;
   // go on to the next tile that holds something and request its first steps
   auto start = [&]() {
-    if (!w.next(a, pre, lane, x, steps, left)) return false;
+    if (!w.next(a, table, lane, x, steps, left)) return false;
     if (steps == 0) return true;
     g = K::geometry(a, x, wave, lane);
     if constexpr (IDX) {
@@ -710,7 +744,9 @@ __global__ __launch_bounds__(C::W * 64, C::MINB) void grouped_kernel(GroupedArgs
     lds_barrier();                                           // all fragments of the tile have been read
     const Tile done = x;
     more = start();                                          // under way while the results are stored
-    K::epilogue(a, done, wm, wn, lane, acc);
+    uint8_t* o[C::TT];
+    K::out_rows(a, done, wm, lane, o);
+    K::epilogue(a, done, wn, lane, o, acc);
   }
 }
 
@@ -726,18 +762,18 @@ __global__ __launch_bounds__(KS * 64, 1) void grouped_split_kernel(GroupedArgs a
   static_assert(C::W == 1, "a wave computes the whole tile");
   constexpr int kStages = KS * C::ST * K::kStage, kSums = KS * C::CT * C::TT * 1024;
   static_assert(kSums <= kStages, "the sums fit the stages");
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[kStages + (kMaxE + 1 + 16) * 4];
-  int* pre = reinterpret_cast<int*>(lds + kStages);
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[kStages + sizeof(Table)];
+  Table& table = *reinterpret_cast<Table*>(lds + kStages);
   const int tid = threadIdx.x, lane = tid & 63, wk = __builtin_amdgcn_readfirstlane(tid >> 6);
   uint8_t* own = lds + wk * C::ST * K::kStage;
   const uint32_t own0 = lds_addr_of(own);
   f32x4* sums = reinterpret_cast<f32x4*>(lds);
   constexpr int kD = K::dmas(false);
 
-  Walk<K> w(a, pre, tid, std::integral_constant<int, KS * 64>{});
+  Walk<K> w(a, table, tid, std::integral_constant<int, KS * 64>{});
   Tile x;
   int steps, left;
-  while (w.next(a, pre, lane, x, steps, left)) {
+  while (w.next(a, table, lane, x, steps, left)) {
     f32x4 acc[C::CT][C::TT];
 #pragma unroll
     for (int i = 0; i < C::CT; ++i)
@@ -786,6 +822,78 @@ __global__ __launch_bounds__(KS * 64, 1) void grouped_split_kernel(GroupedArgs a
   }
 }
 
+// Contractions of one step (bf16, 64 elements: adapters' ranks): the time is
+// the output's.  A workgroup owns 128 columns of one group, keeps their
+// fragments in registers and walks every a.m_bound-th tile of 64 rows, three
+// tiles requested ahead of the stores.  The group comes from the block index,
+// so there is no table to build.
+template <class C, int MODE>
+__global__ __launch_bounds__(256, 4) void grouped_thin_kernel(GroupedArgs a) {
+  using K = Kernel<C, MODE, true>;
+  static_assert(C::W == 4 && C::ST == 3 && K::kTRows && !K::kF8, "bf16 rows along q, three row stages");
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[C::ST * K::kTBytes + K::kCBytes];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / C::WN, wn = wave % C::WN;
+  // T stage s lies at s * kTBytes, so C, which issue_c and read_c put kTBytes
+  // behind a stage, behind the last one
+  const uint8_t* last = lds + (C::ST - 1) * K::kTBytes;
+  Tile x;
+  x.e = blockIdx.x / (a.n_tiles * a.m_bound);
+  const int in = blockIdx.x % (a.n_tiles * a.m_bound);
+  x.n0 = (in % a.n_tiles) * C::BN;
+  group_rows(a, x.e, x.lo, x.hi);
+  const int first = x.lo + in / a.n_tiles * C::BM, stride = a.m_bound * C::BM;
+  if (first >= x.hi) return;
+  const int tiles = (x.hi - first + stride - 1) / stride;
+
+  typename K::Geo g{};
+  K::geometry_c(a, x, g, wave, lane);
+#pragma unroll
+  for (int i = 0; i < K::kCD; ++i) K::template issue_c<false>(a, x, g, lds_addr_of(last), nullptr, 0, i, wave, lane);
+  auto request_rows = [&](int u) {
+    Tile y = x;
+    y.m0 = first + u * stride;
+    K::geometry_t(a, y, g, wave, lane);
+#pragma unroll
+    for (int i = 0; i < K::kTD; ++i)
+      K::template issue_t<false>(a, y, g, lds_addr_of(lds) + u % C::ST * K::kTBytes, nullptr, 0, i, wave, lane);
+  };
+  request_rows(0);
+  if (tiles > 1) request_rows(1);
+  if (tiles > 1) dma_barrier<K::kTD>();
+  else dma_barrier<0>();
+  bf16x8 cv[C::CT][2];
+#pragma unroll
+  for (int i = 0; i < C::CT; ++i)
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      cv[i][h] = __builtin_bit_cast(bf16x8, K::template read_c<true>(last, wn * C::CT + i, h, lane, a.K));
+  for (int u = 0; u < tiles; ++u) {
+    if (u > 0) dma_barrier<0>();                   // this tile's rows; the last tile's stores are long under way
+    Tile y = x;
+    y.m0 = first + u * stride;
+    uint8_t* o[C::TT];
+    K::out_rows(a, y, wm, lane, o);
+    if (u + 2 < tiles) request_rows(u + 2);        // into the stage read a tile ago
+    f32x4 acc[C::CT][C::TT];
+    const uint8_t* st = lds + u % C::ST * K::kTBytes;
+#pragma unroll
+    for (int j = 0; j < C::TT; ++j) {
+      bf16x8 tv[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        tv[h] = __builtin_bit_cast(bf16x8, K::template read_t<true>(st, wm * C::TT + j, h, lane, a.K));
+#pragma unroll
+      for (int i = 0; i < C::CT; ++i) {
+        const f32x4 z = {0.0f, 0.0f, 0.0f, 0.0f};
+        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(cv[i][0], tv[0], z, 0, 0, 0);
+        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(cv[i][1], tv[1], acc[i][j], 0, 0, 0);
+      }
+    }
+    K::epilogue(a, x, wn, lane, o, acc);
+  }
+}
+
 // Large tiles: two groups of four waves, one wave of each on every SIMD, take
 // turns.  A step has four phases, each a reading part R (fragments from LDS,
 // requests for later steps) and a multiplying part M (1/4 of the step's
@@ -813,9 +921,9 @@ __global__ __launch_bounds__(512, 2) void grouped_pair_kernel(GroupedArgs a) {
   using K = Kernel<C, MODE, false>;
   static_assert(C::W == 8 && C::ST == 2 && C::TT % 4 == 0 && K::kTD == 4 && K::kCD == 4,
                 "two groups of four waves, two stages, four phases, groups of two requests");
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * K::kStage + K::kIds + (kMaxE + 1 + 16) * 4];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * K::kStage + K::kIds + sizeof(Table)];
   uint8_t* ids = lds + 2 * K::kStage;
-  int* pre = reinterpret_cast<int*>(lds + 2 * K::kStage + K::kIds);
+  Table& table = *reinterpret_cast<Table*>(lds + 2 * K::kStage + K::kIds);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / C::WN, wn = wave % C::WN;
   const uint32_t lds0 = lds_addr_of(lds);
@@ -827,13 +935,13 @@ __global__ __launch_bounds__(512, 2) void grouped_pair_kernel(GroupedArgs a) {
                                      : K::kGroup[2] + kI + K::kGroup[3] + K::kGroup[0];
   constexpr int kAfterR1 = K::kGroup[0] + K::kGroup[1] + K::kGroup[2] + kI;
 
-  Walk<K> w(a, pre, tid, std::integral_constant<int, K::kThreads>{});
+  Walk<K> w(a, table, tid, std::integral_constant<int, K::kThreads>{});
   Tile x;
   int steps, left;
   typename K::Geo g;
   // go on to the next tile that holds something and request its first step
   auto start = [&]() {
-    if (!w.next(a, pre, lane, x, steps, left)) return false;
+    if (!w.next(a, table, lane, x, steps, left)) return false;
     if (steps == 0) return true;
     g = K::geometry(a, x, wave, lane);
     if constexpr (IDX) {
@@ -900,8 +1008,20 @@ __global__ __launch_bounds__(512, 2) void grouped_pair_kernel(GroupedArgs a) {
     }
     const Tile done = x;
     more = start();                                          // under way while the results are stored
-    K::epilogue(a, done, wm, wn, lane, acc);
+    uint8_t* o[C::TT];
+    K::out_rows(a, done, wm, lane, o);
+    K::epilogue(a, done, wn, lane, o, acc);
   }
+}
+
+// As many workgroups as the chip holds, so long as a group's share of the rows has tiles for them.
+template <class C, int MODE>
+hipError_t launch_thin(GroupedArgs& a, int cus, hipStream_t s) {
+  a.n_tiles = (a.N + C::BN - 1) / C::BN;
+  const int64_t columns = (int64_t)a.n_tiles * a.experts, rows = (a.rows / a.experts + C::BM - 1) / C::BM + 1;
+  a.m_bound = (int32_t)std::max<int64_t>(1, std::min((4 * (int64_t)cus + columns - 1) / columns, rows));
+  hipLaunchKernelGGL((grouped_thin_kernel<C, MODE>), dim3((unsigned)(columns * a.m_bound)), dim3(256), 0, s, a);
+  return hipGetLastError();
 }
 
 // KS: waves that split q (grouped_split_kernel); 0: grouped_kernel, -1: grouped_pair_kernel.
@@ -933,6 +1053,7 @@ using Short = Cfg<64, 128, 2, 2, 2, 3>;
 using Large = Cfg<128, 128, 2, 2, 2, 2>;
 using Pair = Cfg<256, 256, 2, 4, 2, 2>;      // grouped_pair_kernel
 using Split = Cfg<64, 32, 1, 1, 3, 1>;       // grouped_split_kernel, four waves
+using Thin = Cfg<64, 128, 2, 2, 3, 4>;        // grouped_thin_kernel
 using Split2 = Cfg<64, 64, 1, 1, 2, 1>;
 
 // Whether 32-bit offsets reach every row a tile of grouped_pair_kernel reads
@@ -966,12 +1087,13 @@ bool narrow_ok(GroupedMode mode, const GroupedArgs& a) {
 // each other hide it best: 16384 rows in 112 groups, 768 columns, k 32: 20 us
 // against 24 of Mid.
 // Groups are taken to hold rows / experts each and to end inside a tile.
-enum Shape { kSmall, kMid, kShort, kLarge, kPair, kSplit, kSplit2 };
+enum Shape { kSmall, kMid, kShort, kLarge, kPair, kSplit, kSplit2, kThin };
 Shape choose(GroupedMode mode, const GroupedArgs& a, int cus) {
   const bool wg = mode == kGWgrad;
   const int q = mode == kGFwd8 || mode == kGFwd8x ? 128 : 64;
   const double mean = (double)a.rows / a.experts;
   const double steps = wg ? mean / 64 + 0.5 : (double)((a.K + q - 1) / q);
+  if (steps <= 1 && (mode == kGFwd || mode == kGDgrad)) return kThin;
   if (steps <= 2 && !wg) return kShort;
   struct Cost { Shape shape; int bm, bn, per_cu; double one, all, fixed; };
   constexpr Cost kCosts[] = {{kSmall, 64, 64, 2, 0.45, 0.46, 3}, {kMid, 64, 128, 2, 0.53, 0.72, 3},
@@ -1003,6 +1125,9 @@ hipError_t launch_mode(GroupedArgs& a, int cus, hipStream_t s) {
     case kMid: return launch_as<Mid, MODE, IDX>(a, cus, s);
     case kShort: return launch_as<Short, MODE, IDX>(a, cus, s);
     case kLarge: return launch_as<Large, MODE, IDX>(a, cus, s);
+    case kThin:
+      if constexpr (MODE == kGFwd || MODE == kGDgrad) return launch_thin<Thin, MODE>(a, cus, s);
+      break;
     case kSplit:
       if constexpr (!IDX) return launch_as<Split, MODE, IDX, 4>(a, cus, s);
       break;

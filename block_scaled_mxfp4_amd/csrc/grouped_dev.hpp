@@ -51,4 +51,16 @@ __device__ __forceinline__ void store4(const GroupedArgs& a, uint8_t* row, int c
   }
 }
 
+// Eight consecutive columns: 16 bytes of bf16 in one store.
+__device__ __forceinline__ void store8(const GroupedArgs& a, uint8_t* row, int col, const f32x4& u, const f32x4& v) {
+  if (!a.out_f32 && a.vec && col + 8 <= a.N) {
+    const bf16x8 b = {(__bf16)u[0], (__bf16)u[1], (__bf16)u[2], (__bf16)u[3],
+                      (__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
+    *reinterpret_cast<bf16x8*>(reinterpret_cast<uint16_t*>(row) + col) = b;
+  } else {
+    store4(a, row, col, u);
+    store4(a, row, col + 4, v);
+  }
+}
+
 }  // namespace situ
