@@ -43,8 +43,11 @@ namespace {
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
-template <int BM_, int BN_, int WM_, int WN_, int ST_, int MINB_>
+// PERM: a lane's results are eight consecutive columns also where C's rows run
+// along q (see read_c).
+template <int BM_, int BN_, int WM_, int WN_, int ST_, int MINB_, bool PERM_ = false>
 struct Cfg {
+  static constexpr bool PERM = PERM_;
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, ST = ST_, MINB = MINB_;
   static constexpr int W = WM * WN, TT = BM / WM / 16, CT = BN / WN / 16;
   static_assert(BM % (8 * W) == 0 && BN % (8 * W) == 0, "whole DMA blocks per wave");
@@ -102,12 +105,13 @@ struct Kernel {
   static constexpr bool kX = MODE == kGFwd8x, kF8 = MODE == kGFwd8 || kX, kWg = MODE == kGWgrad;
   static constexpr bool kTRows = !kWg;                          // T rows run along q
   static constexpr bool kCRows = MODE == kGFwd || kF8;
+  static constexpr bool kPerm = kCRows || C::PERM;              // a lane's results: eight consecutive columns
   static constexpr int kTBytes = C::BM * 128, kCBytes = C::BN * 128;
   static constexpr int kSBytes = kF8 ? (C::BM + 63) / 64 * 256 + 256 : 0;   // scales of a step: rows, then columns / 128
   static constexpr int kStage = kTBytes + kCBytes + kSBytes;
   static constexpr int kTD = C::BM / 8 / C::W, kCD = C::BN / 8 / C::W;   // DMAs of a wave and step
   static constexpr int kThreads = C::W * 64;
-  static constexpr int kIds = kWg ? 8 * 64 * 4 : 0;             // ring of row indices, 64 per step (IDX)
+  static constexpr int kIds = kWg ? 4 * 64 * 4 : 0;             // ring of row indices, 64 per step, at most three steps live
   static constexpr int kTW = (C::BM + 63) / 64, kSD = kF8 ? (kTW + C::W) / C::W : 0;   // blocks of row scales, scale DMAs of a wave
 
   // Byte offset, within an operand stored as 64 rows of q and R columns, of
@@ -243,7 +247,7 @@ struct Kernel {
                                                    const uint8_t* base, int64_t stride, int n_rows, const uint8_t* ids,
                                                    int j, int r, Off col, uint32_t to) {
     if (IDX && d.div != 0) {
-      const int p = max(reinterpret_cast<const int32_t*>(ids)[(j & 7) * 64 + r], 0);
+      const int p = max(reinterpret_cast<const int32_t*>(ids)[(j & 3) * 64 + r], 0);
       request(base, (Off)min(row_of(d, p), n_rows - 1) * (Off)stride + col, to);
     } else {
       const int lo = x.lo + 64 * j;
@@ -256,7 +260,7 @@ struct Kernel {
       gdma4s(g.sb[i] + j, g.s[i], st + kTBytes + kCBytes + min(wave + C::W * i, kTW) * 256);
   }
   static __device__ __forceinline__ void issue_ids(const GroupedArgs& a, const Tile& x, const uint8_t* ids, int s, int lane) {
-    gdma4(a.pairs + min(x.lo + 64 * (int64_t)s + lane, (int64_t)x.hi - 1), lds_addr_of(ids) + (s & 7) * 256);
+    gdma4(a.pairs + min(x.lo + 64 * (int64_t)s + lane, (int64_t)x.hi - 1), lds_addr_of(ids) + (s & 3) * 256);
   }
 
   // Request all of step j.
@@ -274,7 +278,7 @@ struct Kernel {
 
   // Eight consecutive elements of q (half h of a step, group g of lanes) of
   // the 16 columns of unit u, from an operand stored as 64 rows of q.
-  template <int R>
+  template <int R, bool PERM = false>
   static __device__ __forceinline__ uint4 read_tr(const uint8_t* base, int u, int h, int lane) {
     const int l = lane & 15, g = lane >> 4;
     uint4 v;
@@ -282,7 +286,10 @@ struct Kernel {
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
       const int r = 32 * h + 8 * g + 4 * p + (l >> 2);
-      const uint8_t* at = base + r * (2 * R) + unit_slot<R>(r, u) * 32 + (l & 3) * 8;
+      // PERM: units 2 p and 2 p + 1 share 32 columns, four of each eight to either
+      const uint8_t* at = base + r * (2 * R) +
+                          (PERM ? unit_slot<R>(r, (u & ~1) | ((l >> 1) & 1)) * 32 + (l & 1) * 16 + (u & 1) * 8
+                                : unit_slot<R>(r, u) * 32 + (l & 3) * 8);
       const s16x4 w = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
           (__attribute__((address_space(3))) s16x4*)(uintptr_t)lds_addr_of(at));
       const uint2 w2 = __builtin_bit_cast(uint2, w);
@@ -323,7 +330,7 @@ struct Kernel {
       const int row = 16 * (tile & ~1) + 8 * (l >> 2) + (l & 3) + 4 * (tile & 1);
       v = *reinterpret_cast<const uint4*>(st + kTBytes + row * 128 + (((g + 4 * h) ^ swz_c(row)) * 16));
     } else {
-      v = read_tr<C::BN>(st + kTBytes, tile, h, lane);
+      v = read_tr<C::BN, C::PERM>(st + kTBytes, tile, h, lane);
     }
     clear<TAIL>(v, h, g, left);
     return v;
@@ -512,7 +519,7 @@ struct Kernel {
   // The first of the four columns of column tile i that this lane holds.
   static __device__ __forceinline__ int out_col(const Tile& x, int i, int lane) {
     const int g = lane >> 4;
-    return x.n0 + (kCRows ? 16 * (i & ~1) + 8 * g + 4 * (i & 1) : 16 * i + 4 * g);
+    return x.n0 + (kPerm ? 16 * (i & ~1) + 8 * g + 4 * (i & 1) : 16 * i + 4 * g);
   }
   // Where the wave's row tiles go, all looked up before the first store.
   static __device__ __forceinline__ void out_rows(const GroupedArgs& a, const Tile& x, int wm, int lane,
@@ -527,7 +534,7 @@ struct Kernel {
       if (!o[j]) continue;
 #pragma unroll
       for (int i = 0; i < C::CT; i += 2) {
-        if constexpr (kCRows) {
+        if constexpr (kPerm) {
           store8(a, o[j], out_col(x, wn * C::CT + i, lane), acc[i][j], acc[i + 1][j]);
         } else {
           store4(a, o[j], out_col(x, wn * C::CT + i, lane), acc[i][j]);
@@ -618,8 +625,7 @@ __device__ __forceinline__ void phase_mul_fenced(const typename K::Phase& f, A& 
 template <class K>
 struct Walk {
   using C = typename K::Config;
-  int m_tiles, slots;
-  int64_t it, last;
+  int m_tiles, slots, it, last;      // launch_as keeps the number of tiles below 2^31
 
   template <int NT>
   __device__ __forceinline__ Walk(const GroupedArgs& a, Table& t, int tid, std::integral_constant<int, NT>) {
@@ -635,8 +641,8 @@ struct Walk {
     const int64_t total = (int64_t)m_tiles * a.n_tiles;
     const int xcds = min((int)gridDim.x, 8), xcd = blockIdx.x % xcds;
     slots = gridDim.x / xcds;
-    it = total * xcd / xcds + blockIdx.x / xcds;
-    last = total * (xcd + 1) / xcds;
+    it = (int)(total * xcd / xcds) + blockIdx.x / xcds;
+    last = (int)(total * (xcd + 1) / xcds);
   }
 
   // Moves on to the next tile that holds something; false if there is none.
@@ -654,8 +660,8 @@ struct Walk {
   __device__ __forceinline__ bool tile(const GroupedArgs& a, const Table& t, int lane, Tile& x, int& steps, int& left) {
     if constexpr (K::kWg) {
       const int per = a.m_bound * a.n_tiles;
-      x.e = (int)(it / per);
-      const int r = (int)(it % per);
+      x.e = it / per;
+      const int r = it - x.e * per;
       x.m0 = (r % a.m_bound) * C::BM;
       x.n0 = (r / a.m_bound) * C::BN;
       x.lo = a.offsets ? t.at[x.e] : 0;
@@ -667,12 +673,12 @@ struct Walk {
       // within a group: eight row tiles by all column tiles, rows fastest
       int local, m_l;
       if (a.offsets) {
-        x.e = __builtin_amdgcn_readfirstlane(find_group(t.at, a.experts, (int)(it / a.n_tiles), lane));
-        local = (int)(it - (int64_t)t.at[x.e] * a.n_tiles);
+        x.e = __builtin_amdgcn_readfirstlane(find_group(t.at, a.experts, it / a.n_tiles, lane));
+        local = it - t.at[x.e] * a.n_tiles;
         m_l = t.at[x.e + 1] - t.at[x.e];
       } else {
         x.e = 0;
-        local = (int)it;
+        local = it;
         m_l = m_tiles;
       }
       group_rows(a, x.e, x.lo, x.hi);
@@ -1036,6 +1042,7 @@ hipError_t launch_as(GroupedArgs& a, int cus, hipStream_t s) {
     a.m_bound = a.offsets ? a.rows / C::BM + a.experts : (a.rows + C::BM - 1) / C::BM;
     tiles = (int64_t)a.m_bound * a.n_tiles;
   }
+  if (tiles >= (int64_t)1 << 31) return hipErrorInvalidValue;   // beyond any memory: 2^31 tiles of 2^11 results or more
   const int64_t most = KS > 0 ? cus : (int64_t)C::MINB * 4 / C::W * cus;   // resident workgroups
   int64_t grid = tiles < most ? tiles : most;
   if (grid > 8) grid = (grid + 7) / 8 * 8;
@@ -1044,17 +1051,6 @@ hipError_t launch_as(GroupedArgs& a, int cus, hipStream_t s) {
   else hipLaunchKernelGGL((grouped_kernel<C, MODE, IDX>), dim3((unsigned)grid), dim3(C::W * 64), 0, s, a);
   return hipGetLastError();
 }
-
-// Tile shapes.  With their stages two workgroups of the first two and three
-// of the third fit a CU, one of the last.
-using Small = Cfg<64, 64, 2, 2, 3, 2>;
-using Mid = Cfg<64, 128, 2, 2, 3, 2>;
-using Short = Cfg<64, 128, 2, 2, 2, 3>;
-using Large = Cfg<128, 128, 2, 2, 2, 2>;
-using Pair = Cfg<256, 256, 2, 4, 2, 2>;      // grouped_pair_kernel
-using Split = Cfg<64, 32, 1, 1, 3, 1>;       // grouped_split_kernel, four waves
-using Thin = Cfg<64, 128, 2, 2, 3, 4>;        // grouped_thin_kernel
-using Split2 = Cfg<64, 64, 1, 1, 2, 1>;
 
 // Whether 32-bit offsets reach every row a tile of grouped_pair_kernel reads
 // (Kernel's WIDE): gathered rows from the start of their array, others from the
@@ -1070,35 +1066,34 @@ bool narrow_ok(GroupedMode mode, const GroupedArgs& a) {
 }
 
 // The tile shape: the one whose rounds over the chip cost least, a round being
-// steps * (time of a step) + (first requests and last stores).  Times in us of
-// bf16 products on an MI355X (E4M3 ones are 1.35 times these for every shape),
-// with one workgroup a CU and with all that fit:
-//          one    all    fixed
-//   Small  0.45   0.46   3       Mid  0.53   0.72   3
-//   Large  0.80   1.20   4       Pair 1.35   1.75   8
-//   Split  0.14          8       Split2 0.20        9
-// Split pays where its tiles are no more than the CUs: 64 rows, k 3584 bf16,
-// 3584 columns 17 us against 27 of Small; with 8192 columns and 128 rows
-// Split2 24, Small 31, Split 31.
-// So measured (Small / Mid / Large / Pair, k 3584 bf16, 3584 columns): 64 rows
-// 28 / 32 / 44 / 68 us, 1024 rows 63 / 45 / 50 / 77, 2048 rows 113 / 80 / 66 /
-// 81, 4096 rows 208 / 147 / 133 / 96.
-// Up to two steps the fixed part is all and three workgroups of Short beside
-// each other hide it best: 16384 rows in 112 groups, 768 columns, k 32: 20 us
-// against 24 of Mid.
-// Groups are taken to hold rows / experts each and to end inside a tile.
+// steps * (time of a step) + (first requests and last stores).  Times in us on
+// an MI355X, with one workgroup a CU and with all that fit (kCosts): fitted to
+// single rounds (64 rows) and many (8192 rows), k 3584 to 7168.  So measured,
+// with 3584 columns and k 3584 (Small / Mid / Large / Pair):
+//   bf16   64 rows 28 / 32 / 44 / 68 us,  1024 rows 63 / 45 / 50 / 77,
+//          2048 rows 113 / 80 / 66 / 81,  4096 rows 208 / 147 / 133 / 96
+//   E4M3   64 rows 19 / 27 / 32 / 52,     4096 rows 135 / 105 / 93 / 72
+// Split pays where its tiles are no more than the CUs: 64 rows 17 us bf16 and
+// 12 E4M3; with 8192 columns, k 4096 and 128 rows bf16 Split2 24, Small 31,
+// Split 31.
+// One step goes to grouped_thin_kernel; two to Short, three workgroups of which
+// fit a CU and hide their fixed parts best.
+// Groups are taken to hold rows / experts rows and to need 0.6 of a tile more.
+// Where there is more than a round the last one of grouped rows, whose number
+// is only estimated, is taken as 0.3.
 enum Shape { kSmall, kMid, kShort, kLarge, kPair, kSplit, kSplit2, kThin };
 Shape choose(GroupedMode mode, const GroupedArgs& a, int cus) {
-  const bool wg = mode == kGWgrad;
-  const int q = mode == kGFwd8 || mode == kGFwd8x ? 128 : 64;
+  const bool wg = mode == kGWgrad, f8 = mode == kGFwd8 || mode == kGFwd8x;
+  const int q = f8 ? 128 : 64;
   const double mean = (double)a.rows / a.experts;
   const double steps = wg ? mean / 64 + 0.5 : (double)((a.K + q - 1) / q);
   if (steps <= 1 && (mode == kGFwd || mode == kGDgrad)) return kThin;
   if (steps <= 2 && !wg) return kShort;
-  struct Cost { Shape shape; int bm, bn, per_cu; double one, all, fixed; };
-  constexpr Cost kCosts[] = {{kSmall, 64, 64, 2, 0.45, 0.46, 3}, {kMid, 64, 128, 2, 0.53, 0.72, 3},
-                             {kLarge, 128, 128, 2, 0.80, 1.20, 4}, {kPair, 256, 256, 1, 1.35, 1.75, 8},
-                             {kSplit, 64, 32, 1, 0.14, 0.14, 8},   {kSplit2, 64, 64, 1, 0.20, 0.20, 9}};
+  struct Cost { Shape shape; int bm, bn, per_cu; double one, all, one8, all8, fixed; };
+  constexpr Cost kCosts[] = {
+      {kSmall, 64, 64, 2, 0.45, 0.46, 0.57, 0.61, 3},   {kMid, 64, 128, 2, 0.53, 0.72, 0.85, 1.03, 3},
+      {kLarge, 128, 128, 2, 0.80, 1.20, 1.00, 1.62, 4}, {kPair, 256, 256, 1, 1.35, 1.75, 1.60, 2.00, 8},
+      {kSplit, 64, 32, 1, 0.14, 0.14, 0.15, 0.15, 8},   {kSplit2, 64, 64, 1, 0.20, 0.20, 0.27, 0.27, 9}};
   Shape best = kSmall;
   double least = 1e30;
   for (const Cost& c : kCosts) {
@@ -1107,9 +1102,11 @@ Shape choose(GroupedMode mode, const GroupedArgs& a, int cus) {
     double m;
     if (wg) m = (double)((a.M + c.bm - 1) / c.bm) * a.experts;
     else if (!a.offsets) m = (a.rows + c.bm - 1) / c.bm;
-    else m = a.experts * std::max(1.0, mean / c.bm + 0.5);
+    else m = a.experts * std::max(1.0, mean / c.bm + 0.6);
     const double tiles = m * ((a.N + c.bn - 1) / c.bn), slots = (double)cus * c.per_cu;
-    const double cost = std::ceil(tiles / slots) * (steps * (tiles <= cus ? c.one : c.all) + c.fixed);
+    const double rounds = tiles <= slots ? 1 : (wg || !a.offsets ? std::ceil(tiles / slots) : tiles / slots + 0.3);
+    const double step = tiles <= cus ? (f8 ? c.one8 : c.one) : (f8 ? c.all8 : c.all);
+    const double cost = rounds * (steps * step + c.fixed);
     if (cost < least) {
       least = cost;
       best = c.shape;
@@ -1120,22 +1117,28 @@ Shape choose(GroupedMode mode, const GroupedArgs& a, int cus) {
 
 template <int MODE, bool IDX>
 hipError_t launch_mode(GroupedArgs& a, int cus, hipStream_t s) {
+  // bf16 results in 16-byte stores: 8192 rows x 3584 x 32 of dx 24 us, in 8-byte ones 31.  dw is mostly fp32, whose
+  // four columns a lane are 16 bytes already.
+  constexpr bool kP = MODE == kGDgrad;
   switch (choose((GroupedMode)MODE, a, cus)) {
-    case kSmall: return launch_as<Small, MODE, IDX>(a, cus, s);
-    case kMid: return launch_as<Mid, MODE, IDX>(a, cus, s);
-    case kShort: return launch_as<Short, MODE, IDX>(a, cus, s);
-    case kLarge: return launch_as<Large, MODE, IDX>(a, cus, s);
-    case kThin:
-      if constexpr (MODE == kGFwd || MODE == kGDgrad) return launch_thin<Thin, MODE>(a, cus, s);
+    case kSmall: return launch_as<Cfg<64, 64, 2, 2, 3, 2, kP>, MODE, IDX>(a, cus, s);
+    case kMid: return launch_as<Cfg<64, 128, 2, 2, 3, 2, kP>, MODE, IDX>(a, cus, s);
+    case kShort:
+      if constexpr (MODE != kGWgrad) return launch_as<Cfg<64, 128, 2, 2, 2, 3, kP>, MODE, IDX>(a, cus, s);
+      break;
+    case kLarge: return launch_as<Cfg<128, 128, 2, 2, 2, 2, kP>, MODE, IDX>(a, cus, s);
+    case kPair:
+      if constexpr (MODE != kGFwd8x) return launch_as<Cfg<256, 256, 2, 4, 2, 2, kP>, MODE, IDX, -1>(a, cus, s);
       break;
     case kSplit:
-      if constexpr (!IDX) return launch_as<Split, MODE, IDX, 4>(a, cus, s);
+      if constexpr (!IDX) return launch_as<Cfg<64, 32, 1, 1, 3, 1, kP>, MODE, IDX, 4>(a, cus, s);
       break;
     case kSplit2:
-      if constexpr (!IDX) return launch_as<Split2, MODE, IDX, 4>(a, cus, s);
+      if constexpr (!IDX) return launch_as<Cfg<64, 64, 1, 1, 2, 1, kP>, MODE, IDX, 4>(a, cus, s);
       break;
-    case kPair:
-      if constexpr (MODE != kGFwd8x) return launch_as<Pair, MODE, IDX, -1>(a, cus, s);
+    case kThin:
+      if constexpr (MODE == kGFwd || MODE == kGDgrad) return launch_thin<Cfg<64, 128, 2, 2, 3, 4, true>, MODE>(a, cus, s);
+      break;
   }
   return hipErrorInvalidValue;
 }
