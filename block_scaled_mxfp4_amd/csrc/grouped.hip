@@ -527,18 +527,46 @@ struct Kernel {
 #pragma unroll
     for (int j = 0; j < C::TT; ++j) o[j] = out_row(a, x, wm * C::TT + j, lane);
   }
+  // Store the wave's tile.  A lane has 16 bytes of a row at a time (four fp32 or
+  // eight bf16), four lanes 64 bytes in a row; lanes 2 i and 2 i + 1 exchange
+  // halves of two such units so that eight lanes store a row's 128, whole
+  // lines (dw of 8191 rows x 1536 x 3584 in fp32: see launch_mode).
   static __device__ __forceinline__ void epilogue(const GroupedArgs& a, const Tile& x, int wn, int lane,
                                                   uint8_t* const (&o)[C::TT], f32x4 (&acc)[C::CT][C::TT]) {
+    const bool odd = lane & 1;
 #pragma unroll
     for (int j = 0; j < C::TT; ++j) {
-      if (!o[j]) continue;
+      const uint64_t own = (uint64_t)o[j];
+      const uint64_t other = (uint64_t)swap_pair((uint32_t)own) | (uint64_t)swap_pair((uint32_t)(own >> 32)) << 32;
+      uint8_t* even_row = reinterpret_cast<uint8_t*>(odd ? other : own);
+      uint8_t* odd_row = reinterpret_cast<uint8_t*>(odd ? own : other);
+      if (a.out_f32) {
 #pragma unroll
-      for (int i = 0; i < C::CT; i += 2) {
-        if constexpr (kPerm) {
-          store8(a, o[j], out_col(x, wn * C::CT + i, lane), acc[i][j], acc[i + 1][j]);
-        } else {
-          store4(a, o[j], out_col(x, wn * C::CT + i, lane), acc[i][j]);
-          store4(a, o[j], out_col(x, wn * C::CT + i + 1, lane), acc[i + 1][j]);
+        for (int i = 0; i < C::CT; i += 2) {
+          const uint4 u = __builtin_bit_cast(uint4, acc[i][j]), v = __builtin_bit_cast(uint4, acc[i + 1][j]);
+          const uint4 got = swap_pair(pick(odd, u, v));
+          const int col = out_col(x, wn * C::CT + i + (odd ? 1 : 0), lane);
+          if (even_row) store4(a, even_row, col, __builtin_bit_cast(f32x4, pick(odd, got, u)));
+          if (odd_row) store4(a, odd_row, col, __builtin_bit_cast(f32x4, pick(odd, v, got)));
+        }
+      } else if constexpr (kPerm && C::CT % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < C::CT; i += 4) {
+          const uint4 u = pack8(acc[i][j], acc[i + 1][j]), v = pack8(acc[i + 2][j], acc[i + 3][j]);
+          const uint4 got = swap_pair(pick(odd, u, v));
+          const int col = out_col(x, wn * C::CT + i + (odd ? 2 : 0), lane);
+          if (even_row) store8(a, even_row, col, pick(odd, got, u));
+          if (odd_row) store8(a, odd_row, col, pick(odd, v, got));
+        }
+      } else if (o[j]) {
+#pragma unroll
+        for (int i = 0; i < C::CT; i += 2) {
+          if constexpr (kPerm) {
+            store8(a, o[j], out_col(x, wn * C::CT + i, lane), pack8(acc[i][j], acc[i + 1][j]));
+          } else {
+            store4(a, o[j], out_col(x, wn * C::CT + i, lane), acc[i][j]);
+            store4(a, o[j], out_col(x, wn * C::CT + i + 1, lane), acc[i + 1][j]);
+          }
         }
       }
     }

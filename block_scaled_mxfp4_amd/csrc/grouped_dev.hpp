@@ -51,16 +51,33 @@ __device__ __forceinline__ void store4(const GroupedArgs& a, uint8_t* row, int c
   }
 }
 
-// Eight consecutive columns: 16 bytes of bf16 in one store.
-__device__ __forceinline__ void store8(const GroupedArgs& a, uint8_t* row, int col, const f32x4& u, const f32x4& v) {
-  if (!a.out_f32 && a.vec && col + 8 <= a.N) {
-    const bf16x8 b = {(__bf16)u[0], (__bf16)u[1], (__bf16)u[2], (__bf16)u[3],
-                      (__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
-    *reinterpret_cast<bf16x8*>(reinterpret_cast<uint16_t*>(row) + col) = b;
+// Eight consecutive columns of a bf16 row, already rounded.
+__device__ __forceinline__ void store8(const GroupedArgs& a, uint8_t* row, int col, const uint4& b) {
+  uint16_t* o = reinterpret_cast<uint16_t*>(row) + col;
+  if (a.vec && col + 8 <= a.N) {
+    *reinterpret_cast<uint4*>(o) = b;
   } else {
-    store4(a, row, col, u);
-    store4(a, row, col + 4, v);
+    const uint32_t w[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (col + k < a.N) o[k] = (uint16_t)(w[k / 2] >> (16 * (k % 2)));
   }
+}
+__device__ __forceinline__ uint4 pack8(const f32x4& u, const f32x4& v) {
+  const bf16x8 b = {(__bf16)u[0], (__bf16)u[1], (__bf16)u[2], (__bf16)u[3],
+                    (__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};   // nearest even
+  return __builtin_bit_cast(uint4, b);
+}
+
+// The other lane's value of each pair of lanes 2 i, 2 i + 1 (every lane active).
+__device__ __forceinline__ uint32_t swap_pair(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xF, 0xF, true);
+}
+__device__ __forceinline__ uint4 swap_pair(const uint4& v) {
+  return make_uint4(swap_pair(v.x), swap_pair(v.y), swap_pair(v.z), swap_pair(v.w));
+}
+__device__ __forceinline__ uint4 pick(bool c, const uint4& u, const uint4& v) {
+  return make_uint4(c ? u.x : v.x, c ? u.y : v.y, c ? u.z : v.z, c ? u.w : v.w);
 }
 
 }  // namespace situ
