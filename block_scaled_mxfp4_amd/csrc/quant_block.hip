@@ -56,7 +56,8 @@ __global__ __launch_bounds__(256) void quant_block128_kernel(QuantBlockArgs a) {
     d = __builtin_amdgcn_cvt_pk_fp8_f32(quotient(f[4 * i + 2], scale, r), quotient(f[4 * i + 3], scale, r), d, true);
     o[i] = (uint32_t)d;
   }
-  *reinterpret_cast<uint2*>(a.codes + row * a.cols + col) = make_uint2(o[0], o[1]);
+  typedef int i32x2 __attribute__((ext_vector_type(2)));
+  __builtin_nontemporal_store(i32x2{(int)o[0], (int)o[1]}, reinterpret_cast<i32x2*>(a.codes + row * a.cols + col));
   if ((c & 15) == 0) a.scales[rb] = scale;
 }
 
