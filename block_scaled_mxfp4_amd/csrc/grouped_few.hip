@@ -227,7 +227,10 @@ hipError_t launch_type(GroupedArgs& a, int cus, hipStream_t s) {
 // more than eight rows take the 16-row passes, whose x costs as much as w, and
 // the tiles of grouped.hip are as fast or faster (8 groups, 4096 x 4096 bf16:
 // 8 rows each 80 us here, 62 there; 32 groups, 1536 x 2048 E4M3: 27 and 23).
-bool few_rows(const GroupedArgs& a) { return a.rows <= std::max<int64_t>(8, 4 * (int64_t)a.experts); }
+// One workgroup for each group and 16 columns has to fit a grid.
+bool few_rows(const GroupedArgs& a) {
+  return a.rows <= std::max<int64_t>(8, 4 * (int64_t)a.experts) && (int64_t)a.experts * ((a.N + 15) / 16) <= 1 << 22;
+}
 
 hipError_t launch_grouped_few(GroupedMode mode, GroupedArgs& a, int cus, hipStream_t s) {
   return mode == kGFwd ? launch_type<false>(a, cus, s) : launch_type<true>(a, cus, s);

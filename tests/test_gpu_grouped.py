@@ -112,6 +112,15 @@ def test_quantize(rows, cols, pad):
     assert torch.isfinite(v).all()
 
 
+def test_quantize_many_rows():
+    x = torch.randn(1 << 19, 640, device="cuda").to(BF)      # more blocks than the grid has workgroups for at once
+    codes, scales = B.situ_moe_quantize_fp8_block128(x)
+    want = x.view(-1, 5, 128).abs().amax(2).float() / 448
+    assert ((scales - want).abs() <= 2.0 ** -23 * want).all()
+    near = (x.float() / scales.repeat_interleave(128, 1)).to(F8)
+    assert torch.equal(codes, near.view(torch.uint8))
+
+
 def test_quantize_not_finite():
     x = torch.randn(3, 256, device="cuda").to(BF)
     x[0, 5] = float("nan")
@@ -324,6 +333,85 @@ def test_long_contraction_and_many_rows():
     close(B.situ_moe_grouped_matmul(x, w[:1].contiguous()), want, mag, k)
 
 
+# sizes at which each tile shape is taken, with rows, columns and contractions that end inside tiles
+LARGE = {
+    "pair": ([3000, 0, 2500, 1, 3499], 4104, 1096),
+    "large": ([2050], 3592, 520),
+    "split": ([60, 0, 45], 520, 1800),
+    "split2": ([130], 8200, 1032),
+    "short": ([700, 33, 0, 290], 784, 104),
+    "thin": ([700, 33, 0, 290], 784, 40),
+}
+
+
+@pytest.mark.parametrize("shape", LARGE)
+@pytest.mark.parametrize("out", [BF, F32])
+def test_tile_shapes(shape, out):
+    c, n, k = LARGE[shape]
+    g = gen_of(len(shape))
+    rows, off = sum(c), offsets_of(c)
+    x, w = randn(g, rows, k), randn(g, len(c), n, k)
+    want, mag = grouped_ref(x, w, c)
+    close(B.situ_moe_grouped_matmul(x, w, off, out_dtype=out), want, mag, k)
+    # dx of the transposed sizes: contraction k, columns n
+    wt = w.transpose(1, 2).contiguous()
+    close(B.situ_moe_grouped_matmul_dgrad(x, wt, off, out_dtype=out), want, mag, k)
+    if k % 16 == 0 or shape == "pair":
+        k8 = k // 16 * 16
+        a, sa, w8, sw = fp8_inputs(g, rows, len(c), n - 5, k8)
+        want, mag, eights = fp8_ref(a, sa, w8, sw, c)
+        close(B.situ_moe_matmul_fp8_block128(a, sa, w8, sw, offsets=off, out_dtype=out), want, mag, k8, 2.0, eights)
+
+
+@pytest.mark.parametrize("c,n,k", [([900, 1, 0, 1300], 2056, 2056), ([700, 90, 333], 264, 1032), ([5000], 32, 520),
+                                   ([40, 0, 100, 64, 65], 136, 1544)])
+@pytest.mark.parametrize("gather", [False, True])
+def test_wgrad_tile_shapes(c, n, k, gather):
+    g = gen_of(n + k)
+    rows, off = sum(c), offsets_of(c)
+    dy = randn(g, rows, n)
+    pairs, x_div = None, 0
+    x = xs = randn(g, rows, k)
+    if gather:
+        pairs = torch.randperm(2 * rows, generator=g, device="cuda")[:rows].to(torch.int32)
+        x_div, xs = 4, randn(g, -(-2 * rows // 4), k)
+        x = xs[pairs.long() // 4]
+    dw = B.situ_moe_grouped_matmul_wgrad(dy, xs, off, pairs=pairs, x_div=x_div)
+    lo = 0
+    for e, m in enumerate(c):
+        xe, de = x[lo:lo + m].to(D), dy[lo:lo + m].to(D)
+        close(dw[e], de.t() @ xe, de.abs().t() @ xe.abs(), m)
+        lo += m
+
+
+def test_pairs_at_size():
+    """Gathered and scattered rows through the large tiles, more experts than rows, the most experts."""
+    c, n, k = [2100, 0, 1, 1995], 2056, 1032
+    g = gen_of(21)
+    rows, top_k = sum(c), 4
+    tokens = -(-rows * 2 // top_k)
+    pairs = torch.randperm(tokens * top_k, generator=g, device="cuda")[:rows].to(torch.int32)
+    xt, w = randn(g, tokens, k), randn(g, len(c), n, k)
+    got = torch.full((tokens * top_k, n), 3.0, dtype=BF, device="cuda")
+    B.situ_moe_grouped_matmul(xt, w, offsets_of(c), pairs=pairs, x_div=top_k, out_div=1, out=got)
+    want, mag = grouped_ref(xt[pairs.long() // top_k], w, c)
+    close(got[pairs.long()], want, mag, k)
+    rest = torch.ones(tokens * top_k, dtype=torch.bool, device="cuda")
+    rest[pairs.long()] = False
+    assert (got[rest] == 3.0).all()
+    c = [(i * 7919) % 3 // 2 for i in range(1024)]
+    x, w, dy = randn(g, sum(c), 72), randn(g, 1024, 24, 72), randn(g, sum(c), 24)
+    want, mag = grouped_ref(x, w, c)
+    close(B.situ_moe_grouped_matmul(x, w, offsets_of(c)), want, mag, 72)
+    want, mag = grouped_ref(dy, w.transpose(1, 2), c)
+    close(B.situ_moe_grouped_matmul_dgrad(dy, w, offsets_of(c)), want, mag, 24)
+    dw = B.situ_moe_grouped_matmul_wgrad(dy, x, offsets_of(c))
+    expert = torch.repeat_interleave(torch.arange(1024, device="cuda"), torch.tensor(c, device="cuda"))
+    want = torch.zeros(1024, 24, 72, dtype=D, device="cuda")
+    want[expert] = dy.to(D)[:, :, None] * x.to(D)[:, None, :]
+    assert torch.equal(dw.to(D), want)              # one row each: exact
+
+
 def test_no_rows():
     g = gen_of(4)
     w = randn(g, 3, 16, 32)
@@ -389,6 +477,75 @@ def test_arrays_beyond_4_gib():
     assert (dx[1] == 0).all() and (dx[rows_x - 3] == 0).all()
 
 
+def test_gathered_rows_beyond_2_gib():
+    """Offsets with the highest of 32 bits set, through the large tiles."""
+    rows_x, k, n = 500_000, 4096, 2056              # 4.1 GB of x
+    c = [2500, 1500]
+    g = gen_of(22)
+    x = torch.zeros(rows_x, k, dtype=BF, device="cuda")
+    take = (torch.randperm(rows_x // 2, generator=g, device="cuda")[:4000] * 2 + 1).to(torch.int32)   # the last row's parity
+    take[5] = rows_x - 1
+    x[take.long()] = randn(g, 4000, k)
+    w, dy = randn(g, 2, n, k), randn(g, 4000, n)
+    want, mag = grouped_ref(x[take.long()], w, c)
+    close(B.situ_moe_grouped_matmul(x, w, offsets_of(c), pairs=take, x_div=1), want, mag, k)
+    dw = B.situ_moe_grouped_matmul_wgrad(dy, x, offsets_of(c), pairs=take, x_div=1)
+    xe, de = x[take[:2500].long()].to(D), dy[:2500].to(D)
+    close(dw[0], de.t() @ xe, de.abs().t() @ xe.abs(), 2500)
+
+
+# ---------------------------------------------------------------- refusals
+
+def refused(status, f):
+    with pytest.raises(B.SituMoeError) as e:
+        f()
+    assert e.value.status_name == status, e.value
+
+
+def test_refusals():
+    x = torch.zeros(10, 64, dtype=BF, device="cuda")
+    w = torch.zeros(3, 32, 64, dtype=BF, device="cuda")
+    dy = torch.zeros(10, 32, dtype=BF, device="cuda")
+    off = torch.zeros(4, dtype=torch.int32, device="cuda")
+    pairs = torch.zeros(10, dtype=torch.int32, device="cuda")
+    f, d, g = B.situ_moe_grouped_matmul, B.situ_moe_grouped_matmul_dgrad, B.situ_moe_grouped_matmul_wgrad
+    for bad in ("SITU_E_NULL_ARG", None), ("SITU_E_DEVICE", x.cpu()), ("SITU_E_BAD_SHAPE", x.float()), \
+               ("SITU_E_BAD_SHAPE", x[0]), ("SITU_E_BAD_SHAPE", x.t().contiguous().t()), ("SITU_E_BAD_SHAPE", x[:, :56]):
+        refused(bad[0], lambda: f(bad[1], w, off))
+    refused("SITU_E_BAD_SHAPE", lambda: f(x, w, off.long()))
+    refused("SITU_E_BAD_SHAPE", lambda: f(x, w, off[:3]))
+    refused("SITU_E_NULL_ARG", lambda: f(x, w))
+    refused("SITU_E_NULL_ARG", lambda: f(x, w, off, x_div=2))
+    refused("SITU_E_NULL_ARG", lambda: f(x, w, off, pairs=pairs, out_div=1))       # needs out
+    refused("SITU_E_BAD_SHAPE", lambda: f(x, w, off, pairs=pairs, out_div=2, out=dy))
+    refused("SITU_E_BAD_SHAPE", lambda: f(x, w, off, pairs=pairs, x_div=-1))
+    refused("SITU_E_BAD_SHAPE", lambda: f(x, w.transpose(1, 2), off))
+    refused("SITU_E_BAD_SHAPE", lambda: f(x, w, off, pairs=pairs[:5]))            # 5 positions, 10 rows
+    refused("SITU_E_BAD_SHAPE", lambda: f(x, w, off, out=dy[:5]))
+    refused("SITU_E_BAD_SHAPE", lambda: f(x, w, off, out=dy, out_dtype=F32))
+    refused("SITU_E_UNSUPPORTED", lambda: f(x, w, off, out_dtype=torch.float16))
+    refused("SITU_E_BAD_SHAPE", lambda: f(x[:, :60].contiguous(), w[:, :, :60].contiguous(), off))
+    refused("SITU_E_BAD_SHAPE", lambda: f(x.view(-1)[4:4 + 9 * 64].view(9, 64), w, off))   # rows off 16 bytes
+    refused("SITU_E_BAD_SHAPE", lambda: f(x[:1].expand(10, 64), w, off))
+    refused("SITU_E_BAD_SHAPE", lambda: d(dy[:, :28], w[:, :28].contiguous(), off))
+    refused("SITU_E_BAD_SHAPE", lambda: d(x, w, off))
+    refused("SITU_E_BAD_SHAPE", lambda: g(dy[:9], x, off))
+    refused("SITU_E_BAD_SHAPE", lambda: g(dy, x, off, out=torch.zeros(3, 32, 56, device="cuda")))
+    refused("SITU_E_BAD_SHAPE", lambda: B.situ_moe_quantize_fp8_block128(x[:, :40]))
+    refused("SITU_E_BAD_SHAPE", lambda: B.situ_moe_quantize_fp8_block128(x.half()))
+    a, s = B.situ_moe_quantize_fp8_block128(x)
+    w8, ws = torch.zeros(32, 64, dtype=torch.uint8, device="cuda"), torch.ones(1, 1, device="cuda")
+    m = B.situ_moe_matmul_fp8_block128
+    assert m(a.view(F8), s, w8.view(F8), ws).shape == (10, 32)
+    refused("SITU_E_BAD_SHAPE", lambda: m(a, s[:5], w8, ws))
+    refused("SITU_E_BAD_SHAPE", lambda: m(a, s, w8, ws.double()))
+    refused("SITU_E_BAD_SHAPE", lambda: m(a, s, w8, ws, offsets=off))
+    refused("SITU_E_BAD_SHAPE", lambda: m(a, s, w8[None], ws[None]))
+    refused("SITU_E_BAD_SHAPE", lambda: m(a[:, :40], s, w8[:, :40].contiguous(), ws))
+    refused("SITU_E_NULL_ARG", lambda: m(a, None, w8, ws))
+    refused("SITU_E_UNSUPPORTED", lambda: m(a, s, w8, ws, out_dtype=torch.float16))
+
+
 # ------------------------------------------------------------ streams, graphs
 
 def test_deterministic_and_other_stream():
@@ -405,6 +562,24 @@ def test_deterministic_and_other_stream():
     s.synchronize()
     for a, b in zip(first, again):
         assert torch.equal(a, b)
+
+
+def test_two_calls_at_once():
+    """The kernels hold no state: calls on two streams give what they give alone."""
+    g = gen_of(31)
+    c = [1000, 300, 0, 748]
+    x, w = randn(g, 2048, 520), randn(g, 4, 776, 520)
+    y, v = randn(g, 2048, 520), randn(g, 4, 776, 520)
+    off = offsets_of(c)
+    alone = B.situ_moe_grouped_matmul(x, w, off), B.situ_moe_grouped_matmul(y, v, off)
+    s, t = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(4):
+        got.append((B.situ_moe_grouped_matmul(x, w, off, stream=s), B.situ_moe_grouped_matmul(y, v, off, stream=t)))
+    torch.cuda.synchronize()
+    for p in got:
+        assert torch.equal(p[0], alone[0]) and torch.equal(p[1], alone[1])
 
 
 def test_graph_replay():
