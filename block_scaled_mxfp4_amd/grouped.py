@@ -36,6 +36,21 @@ _GROUPED = struct.Struct("=10i2q5Q")
 assert _FP8.size == ctypes.sizeof(SituMoeFp8Matmul) and _GROUPED.size == ctypes.sizeof(SituMoeGrouped)
 
 
+# torch and what the calls use of it, looked up once: importing this package imports neither torch nor the library
+torch = _device = _raw_stream = _empty = _library = None
+_BF16 = _F32 = _EITHER = _CODES = _INT32 = ()
+
+
+def _first():
+    global torch, _device, _raw_stream, _empty, _library, _BF16, _F32, _EITHER, _CODES, _INT32
+    import torch as t
+    _library = _B.load()
+    _device, _raw_stream, _empty = t._C._cuda_getDevice, t._C._cuda_getCurrentRawStream, t.empty
+    _BF16, _F32, _EITHER = (t.bfloat16,), (t.float32,), (t.bfloat16, t.float32)
+    _CODES, _INT32 = (t.uint8, t.float8_e4m3fn), (t.int32,)
+    torch = t
+
+
 def _fail(status, message):
     raise _B.SituMoeError(status, message)
 
@@ -60,35 +75,33 @@ def _dense(t, name, shape, dtypes, dev):
     return t.data_ptr()
 
 
-def _rows(t, name, shape, dtypes, dev):
-    """The address and row stride of a matrix whose rows are dense (of any number of rows where shape says None)."""
-    if t is None or t.dtype not in dtypes or t.get_device() != dev or t.dim() != 2:
-        _bad(t, name, dtypes, dev, f"{shape}, dense rows")
+def _lead(t, name, dtypes):
+    """Device, rows, columns, row stride and address of the matrix that says where a call runs."""
+    if t is None or not t.is_cuda or t.dtype not in dtypes or t.dim() != 2:
+        _bad(t, name, dtypes, None, "a matrix")
     n, w = t.shape
     stride, one = t.stride()
-    if w != shape[1] or (n != shape[0] and shape[0] is not None) or (one != 1 and w > 1):
-        _bad(t, name, dtypes, dev, f"{shape}, dense rows")
-    return t.data_ptr(), stride if n > 1 else -(-w // 16) * 16   # of one row torch says anything
+    if one != 1 and w > 1:
+        _bad(t, name, dtypes, None, "dense rows")
+    return t.get_device(), n, w, stride if n > 1 else -(-w // 16) * 16, t.data_ptr()   # of one row torch says anything
 
 
-def _lead(t, name, dtypes, dim):
-    """The device of the tensor that says where a call runs, and its shape."""
-    if t is None or not t.is_cuda or t.dtype not in dtypes or t.dim() != dim:
-        _bad(t, name, dtypes, None, f"{dim} dimensions")
-    return t.get_device(), t.shape
+def _rows(t, name, n, w, dtypes, dev):
+    """Rows, row stride and address of a matrix [n, w] whose rows are dense (any number of them where n is None)."""
+    if t is None or t.dtype not in dtypes or t.get_device() != dev or t.dim() != 2:
+        _bad(t, name, dtypes, dev, f"({n}, {w}), dense rows")
+    m, v = t.shape
+    stride, one = t.stride()
+    if v != w or (m != n and n is not None) or (one != 1 and w > 1):
+        _bad(t, name, dtypes, dev, f"({n}, {w}), dense rows")
+    return m, stride if m > 1 else -(-w // 16) * 16, t.data_ptr()
 
 
 class _Place:
     """The device and stream of a call: makes both current while outputs are
     allocated and the kernel is enqueued, where they are not already."""
-    __slots__ = ("handle", "entered")
 
     def __init__(self, dev, stream):
-        import torch
-        self.entered = ()
-        if stream is None and dev == torch.cuda.current_device():
-            self.handle = torch._C._cuda_getCurrentRawStream(dev)   # as current_stream(), 2 us sooner
-            return
         device = torch.device("cuda", dev)
         if stream is None:
             stream = torch.cuda.current_stream(device)
@@ -109,13 +122,24 @@ class _Place:
             c.__exit__(*e)
 
 
+def _at(dev, stream, call, *args):
+    """call(handle, *args) on the device and stream."""
+    if stream is None and dev == _device():
+        return call(_raw_stream(dev), *args)
+    with _Place(dev, stream) as handle:
+        return call(handle, *args)
+
+
 def _out_code(dtype):
-    import torch
     if dtype is torch.bfloat16:
         return _B.OUT_BF16
     if dtype is torch.float32:
         return _B.OUT_F32
     _fail(3, f"out_dtype {dtype} (bfloat16 or float32)")
+
+
+def _out_types(out_dtype):
+    return _EITHER if out_dtype is None else (out_dtype,)
 
 
 def situ_moe_quantize_fp8_block128(x, codes=None, scales=None, stream=None):
@@ -124,22 +148,25 @@ def situ_moe_quantize_fp8_block128(x, codes=None, scales=None, stream=None):
     2^-100) / 448 per row and 128 columns, code = E4M3 of x / scale, nearest
     even.  cols a multiple of 16.  Returns (codes, scales), allocated here
     when not given."""
-    import torch
-    dev, (rows, cols) = _lead(x, "x", (torch.bfloat16,), 2)
-    xp, stride = _rows(x, "x", (None, cols), (torch.bfloat16,), dev)
+    if torch is None:
+        _first()
+    dev, rows, cols, stride, xp = _lead(x, "x", _BF16)
+    return _at(dev, stream, _quantize, x.device, dev, rows, cols, stride, xp, codes, scales)
+
+
+def _quantize(handle, device, dev, rows, cols, stride, xp, codes, scales):
     nb = -(-cols // 128)
-    with _Place(dev, stream) as handle:
-        if codes is None:
-            codes = torch.empty(rows, cols, dtype=torch.uint8, device=x.device)
-            cp = codes.data_ptr()
-        else:
-            cp = _dense(codes, "codes", (rows, cols), (torch.uint8, torch.float8_e4m3fn), dev)
-        if scales is None:
-            scales = torch.empty(rows, nb, dtype=torch.float32, device=x.device)
-            sp = scales.data_ptr()
-        else:
-            sp = _dense(scales, "scales", (rows, nb), (torch.float32,), dev)
-        status = _B.load().situ_moe_quantize_fp8_block128(xp, rows, cols, stride, cp, sp, handle)
+    if codes is None:
+        codes = _empty(rows, cols, dtype=torch.uint8, device=device)
+        cp = codes.data_ptr()
+    else:
+        cp = _dense(codes, "codes", (rows, cols), _CODES, dev)
+    if scales is None:
+        scales = _empty(rows, nb, dtype=torch.float32, device=device)
+        sp = scales.data_ptr()
+    else:
+        sp = _dense(scales, "scales", (rows, nb), _F32, dev)
+    status = _library.situ_moe_quantize_fp8_block128(xp, rows, cols, stride, cp, sp, handle)
     if status:
         _B._check(status)
     return codes, scales
@@ -156,83 +183,92 @@ def situ_moe_matmul_fp8_block128(a, a_scale, w, w_scale, *, offsets=None, out=No
     rows offsets[e] .. offsets[e + 1] - 1 belong to expert e.  out: bf16 (the
     default) or fp32 [rows, n]; rows outside every group are left as they are
     (undefined in an output allocated here)."""
-    import torch
-    types = (torch.uint8, torch.float8_e4m3fn)
-    dev, (rows, k) = _lead(a, "a", types, 2)
-    ap, a_stride = _rows(a, "a", (rows, k), types, dev)
+    if torch is None:
+        _first()
+    dev, rows, k, a_stride, ap = _lead(a, "a", _CODES)
     kb = -(-k // 128)
-    sp, s_stride = _rows(a_scale, "a_scale", (rows, kb), (torch.float32,), dev)
+    _, s_stride, sp = _rows(a_scale, "a_scale", rows, kb, _F32, dev)
     if offsets is None:
         if w is None or w.dim() != 2:
-            _bad(w, "w", types, dev, "[n, k] without offsets")
+            _bad(w, "w", _CODES, dev, "[n, k] without offsets")
         n, experts, op = w.shape[0], 1, 0
-        wp = _dense(w, "w", (n, k), types, dev)
-        wsp = _dense(w_scale, "w_scale", (-(-n // 128), kb), (torch.float32,), dev)
+        wp = _dense(w, "w", (n, k), _CODES, dev)
+        wsp = _dense(w_scale, "w_scale", (-(-n // 128), kb), _F32, dev)
     else:
         if w is None or w.dim() != 3:
-            _bad(w, "w", types, dev, "[experts, n, k] with offsets")
-        experts, n = w.shape[0], w.shape[1]
-        op = _dense(offsets, "offsets", (experts + 1,), (torch.int32,), dev)
-        wp = _dense(w, "w", (experts, n, k), types, dev)
-        wsp = _dense(w_scale, "w_scale", (experts, -(-n // 128), kb), (torch.float32,), dev)
-    with _Place(dev, stream) as handle:
-        if out is None:
-            out_dtype = out_dtype or torch.bfloat16
-            code = _out_code(out_dtype)
-            out = torch.empty(rows, n, dtype=out_dtype, device=a.device)
-            outp, out_stride = out.data_ptr(), n
-        else:
-            outp, out_stride = _rows(out, "out", (rows, n), (out_dtype,) if out_dtype else (torch.bfloat16, torch.float32), dev)
-            code = _out_code(out.dtype)
-        status = _B.load().situ_moe_matmul_fp8_block128(
-            _FP8.pack(rows, n, k, experts, code, 0, a_stride, s_stride, out_stride, ap, sp, wp, wsp, op, outp), handle)
+            _bad(w, "w", _CODES, dev, "[experts, n, k] with offsets")
+        experts, n, _ = w.shape
+        op = _dense(offsets, "offsets", (experts + 1,), _INT32, dev)
+        wp = _dense(w, "w", (experts, n, k), _CODES, dev)
+        wsp = _dense(w_scale, "w_scale", (experts, -(-n // 128), kb), _F32, dev)
+    return _at(dev, stream, _matmul, a.device, dev, (rows, n, k, experts), (a_stride, s_stride), (ap, sp, wp, wsp, op),
+               out, out_dtype)
+
+
+def _matmul(handle, device, dev, sizes, strides, pointers, out, out_dtype):
+    rows, n = sizes[:2]
+    if out is None:
+        out_dtype = out_dtype or torch.bfloat16
+        code = _out_code(out_dtype)
+        out = _empty(rows, n, dtype=out_dtype, device=device)
+        stride, outp = n, out.data_ptr()
+    else:
+        _, stride, outp = _rows(out, "out", rows, n, _out_types(out_dtype), dev)
+        code = _out_code(out.dtype)
+    status = _library.situ_moe_matmul_fp8_block128(_FP8.pack(*sizes, code, 0, *strides, stride, *pointers, outp), handle)
     if status:
         _B._check(status)
     return out
 
 
-def _grouped(name, written, lead, dev, sides, offsets, pairs, divs, sizes, out_dtype, stream):
-    """The three grouped products.  sides = (x, y, w) and divs = (x_div,
-    y_div); sides[written] is the kernel's output, allocated here if it is
-    None; lead: the input whose rows are the positions where pairs is None."""
-    import torch
-    experts, n, k = sizes
+def _grouped(handle, name, written, lead, device, dev, sides, offsets, pairs, x_div, y_div, experts, n, k, out_dtype):
+    """The three grouped products.  sides = [x, y, w]; sides[written] is the
+    kernel's output, allocated here if it is None; lead: the input whose rows
+    are the positions where pairs is None."""
     if offsets is None:
         if experts != 1:
             _fail(1, f"offsets is None with {experts} experts")
         op = 0
     else:
-        op = _dense(offsets, "offsets", (experts + 1,), (torch.int32,), dev)
-    x_div, y_div = divs
+        op = _dense(offsets, "offsets", (experts + 1,), _INT32, dev)
     if pairs is None:
         if x_div or y_div:
             _fail(1, "pairs is None")
         rows, pp = sides[lead].shape[0], 0
     else:
         rows = pairs.numel()
-        pp = _dense(pairs, "pairs", (rows,), (torch.int32,), dev)
-    shapes = ((None if x_div else rows, k), (None if y_div else rows, n), (experts, n, k))
+        pp = _dense(pairs, "pairs", (rows,), _INT32, dev)
     names = _NAMES[name]
-    with _Place(dev, stream) as handle:
-        if sides[written] is None:
-            if written < 2 and divs[written]:
-                _fail(1, f"{name} with a div on its written side needs out")
-            out_dtype = out_dtype or (torch.float32 if written == 2 else torch.bfloat16)
-            _out_code(out_dtype)
-            out = torch.empty(*shapes[written], dtype=out_dtype, device=sides[lead].device)
-            sides = sides[:written] + (out,) + sides[written + 1:]
-        either = (out_dtype,) if out_dtype else (torch.bfloat16, torch.float32)
-        bf16 = (torch.bfloat16,)
-        xp, x_stride = _rows(sides[0], names[0], shapes[0], either if written == 0 else bf16, dev)
-        yp, y_stride = _rows(sides[1], names[1], shapes[1], either if written == 1 else bf16, dev)
-        wp = _dense(sides[2], names[2], shapes[2], either if written == 2 else bf16, dev)
-        out = sides[written]
-        status = getattr(_B.load(), name)(
-            _GROUPED.pack(rows, n, k, experts, sides[0].shape[0], sides[1].shape[0], x_div, y_div, _out_code(out.dtype),
-                          0, x_stride, y_stride, op, pp, xp, yp, wp), handle)
+    out = sides[written]
+    types = _out_types(out_dtype)
+    if out is None:
+        if written < 2 and (y_div if written else x_div):
+            _fail(1, f"{name} with a div on its written side needs out")
+        if out_dtype is None:
+            out_dtype = torch.float32 if written == 2 else torch.bfloat16
+        code = _out_code(out_dtype)
+        types = (out_dtype,)
+        if written == 2:
+            out = _empty(experts, n, k, dtype=out_dtype, device=device)
+        else:
+            out = _empty(rows, n if written else k, dtype=out_dtype, device=device)
+        sides[written] = out
+    x, y, w = sides
+    x_rows, x_stride, xp = _rows(x, names[0], None if x_div else rows, k, types if written == 0 else _BF16, dev)
+    y_rows, y_stride, yp = _rows(y, names[1], None if y_div else rows, n, types if written == 1 else _BF16, dev)
+    wp = _dense(w, names[2], (experts, n, k), types if written == 2 else _BF16, dev)
+    status = getattr(_library, name)(
+        _GROUPED.pack(rows, n, k, experts, x_rows, y_rows, x_div, y_div, _out_code(out.dtype), 0, x_stride, y_stride, op,
+                      pp, xp, yp, wp), handle)
     if status:
         _B._check(status)
     return out
+
+
+def _weights(w):
+    if w is None or not w.is_cuda or w.dtype not in _BF16 or w.dim() != 3:
+        _bad(w, "w", _BF16, None, "[experts, n, k]")
+    return w.shape
 
 
 _NAMES = {"situ_moe_grouped_matmul": ("x", "out", "w"), "situ_moe_grouped_matmul_dgrad": ("out", "dy", "w"),
@@ -250,11 +286,13 @@ def situ_moe_grouped_matmul(x, w, offsets=None, *, pairs=None, x_div=0, out_div=
     [positions].  k a multiple of 8.  out: bf16 (the default) or fp32; rows no
     position stands for are left as they are (undefined in an output allocated
     here); with out_div = 1 it has to be given."""
-    import torch
-    dev, _ = _lead(x, "x", (torch.bfloat16,), 2)
-    _, sizes = _lead(w, "w", (torch.bfloat16,), 3)
-    return _grouped("situ_moe_grouped_matmul", 1, 0, dev, (x, out, w), offsets, pairs, (int(x_div), int(out_div)),
-                    sizes, out_dtype, stream)
+    if torch is None:
+        _first()
+    if x is None or not x.is_cuda:
+        _bad(x, "x", _BF16, None, "")
+    dev = x.get_device()
+    return _at(dev, stream, _grouped, "situ_moe_grouped_matmul", 1, 0, x.device, dev, [x, out, w], offsets, pairs,
+               int(x_div), int(out_div), *_weights(w), out_dtype)
 
 
 def situ_moe_grouped_matmul_dgrad(dy, w, offsets=None, *, pairs=None, dy_div=0, out_div=0, out=None, out_dtype=None,
@@ -263,11 +301,13 @@ def situ_moe_grouped_matmul_dgrad(dy, w, offsets=None, *, pairs=None, dy_div=0, 
     out[o(r)] = w[e]^T dy[i(r)], with i(r) by dy_div and o(r) by out_div (0 or
     1).  A token's gradient is the sum of its pairs' rows.  n and k multiples
     of 8."""
-    import torch
-    dev, _ = _lead(dy, "dy", (torch.bfloat16,), 2)
-    _, sizes = _lead(w, "w", (torch.bfloat16,), 3)
-    return _grouped("situ_moe_grouped_matmul_dgrad", 0, 1, dev, (out, dy, w), offsets, pairs,
-                    (int(out_div), int(dy_div)), sizes, out_dtype, stream)
+    if torch is None:
+        _first()
+    if dy is None or not dy.is_cuda:
+        _bad(dy, "dy", _BF16, None, "")
+    dev = dy.get_device()
+    return _at(dev, stream, _grouped, "situ_moe_grouped_matmul_dgrad", 0, 1, dy.device, dev, [out, dy, w], offsets, pairs,
+               int(out_div), int(dy_div), *_weights(w), out_dtype)
 
 
 def situ_moe_grouped_matmul_wgrad(dy, x, offsets=None, *, pairs=None, dy_div=0, x_div=0, out=None, out_dtype=None,
@@ -276,9 +316,10 @@ def situ_moe_grouped_matmul_wgrad(dy, x, offsets=None, *, pairs=None, dy_div=0, 
     positions of e of dy[i(r)] x[j(r)]^T, [experts, n, k] in fp32 (the
     default) or bf16; zero for an empty expert.  i(r) by dy_div, j(r) by
     x_div.  n and k multiples of 8."""
-    import torch
-    dev, (_, n) = _lead(dy, "dy", (torch.bfloat16,), 2)
-    _, (_, k) = _lead(x, "x", (torch.bfloat16,), 2)
+    if torch is None:
+        _first()
+    dev, _, n, _, _ = _lead(dy, "dy", _BF16)
+    _, _, k, _, _ = _lead(x, "x", _BF16)
     experts = 1 if offsets is None else offsets.numel() - 1
-    return _grouped("situ_moe_grouped_matmul_wgrad", 2, 1 if dy_div == 0 else 0, dev, (x, dy, out), offsets, pairs,
-                    (int(x_div), int(dy_div)), (experts, n, k), out_dtype, stream)
+    return _at(dev, stream, _grouped, "situ_moe_grouped_matmul_wgrad", 2, 0 if dy_div else 1, dy.device, dev, [x, dy, out],
+               offsets, pairs, int(x_div), int(dy_div), experts, n, k, out_dtype)
