@@ -13,6 +13,7 @@ using situ::fail_status;
 
 constexpr int32_t kMaxRows = 1 << 24, kMaxSide = 1 << 18, kMaxExperts = 1024;
 constexpr int64_t kMaxStride = (int64_t)1 << 40;
+constexpr int64_t kMaxScaleStride = 1 << 22;   // 64 rows of scales within 32 bits of bytes
 
 bool aligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
@@ -146,6 +147,8 @@ situ_status situ_moe_matmul_fp8_block128(const situ_moe_fp8_matmul_t* p, void* h
   if ((st = check_in("w", p->w, p->k, p->k, 1)) != SITU_OK) return st;
   if ((st = check_out("out", p->out, p->out_stride, p->n, out_size)) != SITU_OK) return st;
   if ((st = check_out("a_scale", p->a_scale, p->a_scale_stride, kb, 4)) != SITU_OK) return st;
+  if (p->a_scale_stride >= kMaxScaleStride)
+    return fail_status(SITU_E_UNSUPPORTED, "a_scale: stride %lld (below 2^22)", (long long)p->a_scale_stride);
   if ((st = check_out("w_scale", p->w_scale, kb, kb, 4)) != SITU_OK) return st;
   int cus = 0;
   if ((st = situ::require_device(&cus)) != SITU_OK) return st;

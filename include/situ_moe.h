@@ -286,7 +286,7 @@ typedef struct situ_moe_fp8_matmul_t {
   int32_t out_dtype;          /* SITU_OUT_F32 or SITU_OUT_BF16 */
   int32_t reserved;           /* 0 */
   int64_t a_stride;           /* elements between rows of a */
-  int64_t a_scale_stride;     /* elements between rows of a_scale */
+  int64_t a_scale_stride;     /* elements between rows of a_scale, below 2^22 */
   int64_t out_stride;         /* elements between rows of out */
   const uint8_t* a;           /* (device) E4M3 [rows, k] */
   const float* a_scale;       /* (device) [rows, ceil(k / 128)] */

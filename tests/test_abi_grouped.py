@@ -60,7 +60,8 @@ def _fp8(**kw):
     (dict(rows=(1 << 24) + 1), 3), (dict(a=None), 1), (dict(a_scale=None), 1), (dict(w=None), 1),
     (dict(w_scale=None), 1), (dict(out=None), 1), (dict(a=FAKE + 8), 2), (dict(w=FAKE + 4), 2), (dict(out=FAKE + 1), 2),
     (dict(a_scale=FAKE + 2), 2), (dict(w_scale=FAKE + 1), 2), (dict(offsets=FAKE + 2), 2), (dict(a_stride=240), 2),
-    (dict(a_stride=264), 2), (dict(a_scale_stride=1), 2), (dict(out_stride=199), 2), (dict(rows=0, a=None), 0)])
+    (dict(a_stride=264), 2), (dict(a_scale_stride=1), 2), (dict(out_stride=199), 2), (dict(rows=0, a=None), 0),
+    (dict(a_scale_stride=1 << 22), 3), (dict(a_scale_stride=1 << 32), 3), (dict(a_scale_stride=1 << 41), 2)])
 def test_fp8_matmul_refusals(kw, want):
     assert _fp8(**kw) == want, B.situ_moe_last_error()
     assert B.load().situ_moe_matmul_fp8_block128(None, None) == 1
