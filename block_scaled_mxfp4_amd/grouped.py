@@ -288,8 +288,8 @@ def situ_moe_grouped_matmul(x, w, offsets=None, *, pairs=None, x_div=0, out_div=
     here); with out_div = 1 it has to be given."""
     if torch is None:
         _first()
-    if x is None or not x.is_cuda:
-        _bad(x, "x", _BF16, None, "")
+    if x is None or not x.is_cuda or x.dim() != 2:
+        _bad(x, "x", _BF16, None, "a matrix")
     dev = x.get_device()
     return _at(dev, stream, _grouped, "situ_moe_grouped_matmul", 1, 0, x.device, dev, [x, out, w], offsets, pairs,
                int(x_div), int(out_div), *_weights(w), out_dtype)
@@ -303,8 +303,8 @@ def situ_moe_grouped_matmul_dgrad(dy, w, offsets=None, *, pairs=None, dy_div=0, 
     of 8."""
     if torch is None:
         _first()
-    if dy is None or not dy.is_cuda:
-        _bad(dy, "dy", _BF16, None, "")
+    if dy is None or not dy.is_cuda or dy.dim() != 2:
+        _bad(dy, "dy", _BF16, None, "a matrix")
     dev = dy.get_device()
     return _at(dev, stream, _grouped, "situ_moe_grouped_matmul_dgrad", 0, 1, dy.device, dev, [out, dy, w], offsets, pairs,
                int(out_div), int(dy_div), *_weights(w), out_dtype)

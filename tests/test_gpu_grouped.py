@@ -546,6 +546,15 @@ def test_refusals():
     refused("SITU_E_UNSUPPORTED", lambda: m(a, s, w8, ws, out_dtype=torch.float16))
 
 
+def test_refusal_of_a_scalar():
+    s = torch.zeros((), dtype=BF, device="cuda")
+    w = torch.zeros(1, 32, 64, dtype=BF, device="cuda")
+    refused("SITU_E_BAD_SHAPE", lambda: B.situ_moe_grouped_matmul(s, w))
+    refused("SITU_E_BAD_SHAPE", lambda: B.situ_moe_grouped_matmul_dgrad(s, w))
+    refused("SITU_E_BAD_SHAPE", lambda: B.situ_moe_grouped_matmul_wgrad(s, s))
+    refused("SITU_E_BAD_SHAPE", lambda: B.situ_moe_quantize_fp8_block128(s))
+
+
 # ------------------------------------------------------------ streams, graphs
 
 def test_deterministic_and_other_stream():
