@@ -320,6 +320,6 @@ def situ_moe_grouped_matmul_wgrad(dy, x, offsets=None, *, pairs=None, dy_div=0, 
         _first()
     dev, _, n, _, _ = _lead(dy, "dy", _BF16)
     _, _, k, _, _ = _lead(x, "x", _BF16)
-    experts = 1 if offsets is None else offsets.numel() - 1
+    experts = 1 if offsets is None else max(offsets.numel() - 1, 0)
     return _at(dev, stream, _grouped, "situ_moe_grouped_matmul_wgrad", 2, 0 if dy_div else 1, dy.device, dev, [x, dy, out],
                offsets, pairs, int(x_div), int(dy_div), experts, n, k, out_dtype)

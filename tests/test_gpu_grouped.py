@@ -555,6 +555,13 @@ def test_refusal_of_a_scalar():
     refused("SITU_E_BAD_SHAPE", lambda: B.situ_moe_quantize_fp8_block128(s))
 
 
+def test_refusal_of_offsets_without_groups():
+    x, dy = torch.zeros(10, 64, dtype=BF, device="cuda"), torch.zeros(10, 32, dtype=BF, device="cuda")
+    off = torch.zeros(4, dtype=torch.int32, device="cuda")
+    for n in (0, 1):
+        refused("SITU_E_BAD_SHAPE", lambda: B.situ_moe_grouped_matmul_wgrad(dy, x, off[:n]))
+
+
 # ------------------------------------------------------------ streams, graphs
 
 def test_deterministic_and_other_stream():
