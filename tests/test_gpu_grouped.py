@@ -363,6 +363,61 @@ def test_tile_shapes(shape, out):
         close(B.situ_moe_matmul_fp8_block128(a, sa, w8, sw, offsets=off, out_dtype=out), want, mag, k8, 2.0, eights)
 
 
+@pytest.mark.parametrize("rows,experts,n,k", [(60, 16, 136, 520), (700, 40, 264, 40), (700, 40, 264, 104),
+                                              (900, 8, 520, 1032), (9000, 6, 2056, 1032)])
+def test_all_rows_in_one_group(rows, experts, n, k):
+    """The shapes are chosen by the mean; a group may hold all rows."""
+    g = gen_of(rows + n)
+    c = [0] * (experts - 2) + [rows, 0]
+    off = offsets_of(c)
+    x, w, dy = randn(g, rows, k), randn(g, experts, n, k), randn(g, rows, n)
+    want, mag = grouped_ref(x, w, c)
+    close(B.situ_moe_grouped_matmul(x, w, off), want, mag, k)
+    want, mag = grouped_ref(dy, w.transpose(1, 2), c)
+    close(B.situ_moe_grouped_matmul_dgrad(dy, w, off), want, mag, n)
+    dw = B.situ_moe_grouped_matmul_wgrad(dy, x, off)
+    close(dw[-2], dy.to(D).t() @ x.to(D), dy.to(D).abs().t() @ x.to(D).abs(), rows)
+    assert (dw[:-2] == 0).all() and (dw[-1] == 0).all()
+    a, sa, w8, sw = fp8_inputs(g, rows, experts, n, k // 16 * 16)
+    want, mag, eights = fp8_ref(a, sa, w8, sw, c)
+    close(B.situ_moe_matmul_fp8_block128(a, sa, w8, sw, offsets=off), want, mag, k, 2.0, eights)
+
+
+@pytest.mark.parametrize("c,n,k", [([3, 5, 2], 72, 264), ([60, 33, 45], 520, 1800), ([301, 77, 200], 264, 40),
+                                   ([3001, 2500, 1], 2056, 1032)])
+def test_not_finite_stays_in_its_row_and_group(c, n, k):
+    """An infinity and a NaN in the last row of the first group: no other row
+    and no other group's weight gradient sees them."""
+    g = gen_of(n + k)
+    rows, off, last = sum(c), offsets_of(c), c[0] - 1
+    x, w, dy = randn(g, rows, k), randn(g, len(c), n, k), randn(g, rows, n)
+    x[last, 0], dy[last, 1] = float("nan"), float("inf")
+    others = torch.arange(rows, device="cuda") != last
+    got = B.situ_moe_grouped_matmul(x, w, off)
+    want, mag = grouped_ref(x, w, c)
+    assert torch.isnan(got[last]).all()
+    close(got[others], want[others], mag[others], k)
+    got = B.situ_moe_grouped_matmul_dgrad(dy, w, off)
+    want, mag = grouped_ref(dy, w.transpose(1, 2), c)
+    assert not torch.isfinite(got[last]).any()
+    close(got[others], want[others], mag[others], n)
+    dw = B.situ_moe_grouped_matmul_wgrad(dy, x, off)
+    assert torch.isnan(dw[0, :, 0]).all() and not torch.isfinite(dw[0, 1]).any()
+    lo = c[0]
+    for e, m in enumerate(c[1:], 1):
+        xe, de = x[lo:lo + m].to(D), dy[lo:lo + m].to(D)
+        close(dw[e], de.t() @ xe, de.abs().t() @ xe.abs(), m)
+        lo += m
+    k8 = k // 16 * 16
+    a, sa, w8, sw = fp8_inputs(g, rows, len(c), n, k8)
+    want, mag, eights = fp8_ref(a, sa, w8, sw, c)
+    a[last, 3] = 0x7f
+    for out in (BF, F32):
+        got = B.situ_moe_matmul_fp8_block128(a, sa, w8, sw, offsets=off, out_dtype=out)
+        assert torch.isnan(got[last]).all()
+        close(got[others], want[others], mag[others], k8, 2.0, eights[others])
+
+
 @pytest.mark.parametrize("c,n,k", [([900, 1, 0, 1300], 2056, 2056), ([700, 90, 333], 264, 1032), ([5000], 32, 520),
                                    ([40, 0, 100, 64, 65], 136, 1544)])
 @pytest.mark.parametrize("gather", [False, True])
