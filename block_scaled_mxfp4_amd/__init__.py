@@ -145,6 +145,19 @@ def _stream(stream):
     return ctypes.c_void_p(int(handle))
 
 
+def _torch_stream(stream, device):
+    """The torch.cuda.Stream of a stream argument.  The raw handle 0 is the
+    default stream: an ExternalStream made of it would be a new stream, which
+    waits for nothing."""
+    import torch
+    if stream is None:
+        return torch.cuda.current_stream(device)
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    handle = int(stream)
+    return torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
+
+
 # ------------------------------------------------------------------ C names
 
 def situ_moe_status_string(status):
@@ -404,12 +417,7 @@ def situ_moe(*, hidden_states, hidden_states_scale=None, topk_ids=None, topk_wei
                         activation=activation, weight_format=weight_format)
     plan = situ_moe_plan(prob)
     dev = hidden_states.device
-    if stream is None:
-        stream_obj = torch.cuda.current_stream(dev)
-    elif isinstance(stream, torch.cuda.Stream):
-        stream_obj = stream
-    else:
-        stream_obj = torch.cuda.ExternalStream(int(stream), device=dev)
+    stream_obj = _torch_stream(stream, dev)
     with torch.cuda.stream(stream_obj):
         if out is None:
             out = torch.empty((T, H), dtype=out_dtype, device=dev)

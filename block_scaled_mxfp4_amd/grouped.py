@@ -103,11 +103,8 @@ class _Place:
 
     def __init__(self, dev, stream):
         device = torch.device("cuda", dev)
-        if stream is None:
-            stream = torch.cuda.current_stream(device)
-        elif not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(int(stream), device=device)
-        elif stream.device != device:
+        stream = _B._torch_stream(stream, device)
+        if stream.device != device:
             _fail(2, f"the stream is of {stream.device}, the tensors are on {device}")
         self.handle = stream.cuda_stream
         self.entered = (torch.cuda.device(device), torch.cuda.stream(stream))
