@@ -36,6 +36,13 @@ _GROUPED = struct.Struct("=10i2q5Q")
 assert _FP8.size == ctypes.sizeof(SituMoeFp8Matmul) and _GROUPED.size == ctypes.sizeof(SituMoeGrouped)
 
 
+def _pack(form, *fields):
+    try:
+        return form.pack(*fields)
+    except struct.error:
+        _fail(3, "a size or div past 32 bits")
+
+
 # torch and what the calls use of it, looked up once: importing this package imports neither torch nor the library
 torch = _device = _raw_stream = _empty = _library = None
 _BF16 = _F32 = _EITHER = _CODES = _INT32 = ()
@@ -152,6 +159,8 @@ def situ_moe_quantize_fp8_block128(x, codes=None, scales=None, stream=None):
 
 
 def _quantize(handle, device, dev, rows, cols, stride, xp, codes, scales):
+    if cols >= 1 << 31:                    # ctypes would pass its low 32 bits
+        _fail(3, f"cols {cols} past 32 bits")
     nb = -(-cols // 128)
     if codes is None:
         codes = _empty(rows, cols, dtype=torch.uint8, device=device)
@@ -212,7 +221,8 @@ def _matmul(handle, device, dev, sizes, strides, pointers, out, out_dtype):
     else:
         _, stride, outp = _rows(out, "out", rows, n, _out_types(out_dtype), dev)
         code = _out_code(out.dtype)
-    status = _library.situ_moe_matmul_fp8_block128(_FP8.pack(*sizes, code, 0, *strides, stride, *pointers, outp), handle)
+    status = _library.situ_moe_matmul_fp8_block128(_pack(_FP8, *sizes, code, 0, *strides, stride, *pointers, outp),
+                                                   handle)
     if status:
         _B._check(status)
     return out
@@ -255,8 +265,8 @@ def _grouped(handle, name, written, lead, device, dev, sides, offsets, pairs, x_
     y_rows, y_stride, yp = _rows(y, names[1], None if y_div else rows, n, types if written == 1 else _BF16, dev)
     wp = _dense(w, names[2], (experts, n, k), types if written == 2 else _BF16, dev)
     status = getattr(_library, name)(
-        _GROUPED.pack(rows, n, k, experts, x_rows, y_rows, x_div, y_div, _out_code(out.dtype), 0, x_stride, y_stride, op,
-                      pp, xp, yp, wp), handle)
+        _pack(_GROUPED, rows, n, k, experts, x_rows, y_rows, x_div, y_div, _out_code(out.dtype), 0, x_stride, y_stride, op,
+              pp, xp, yp, wp), handle)
     if status:
         _B._check(status)
     return out

@@ -126,3 +126,67 @@ def test_row_division():
                   max(((1 << 31) - 1) // d * d - 1, 0)):
             if p < 1 << 31:
                 assert ((p * mul) >> 32) >> (s - 1) == p // d, (p, d)
+
+
+class _Fake:
+    """What the binding asks of a device tensor, of any size (its memory is never reached)."""
+
+    def __init__(self, dtype, *shape):
+        self.dtype, self.shape, self.is_cuda, self.device = dtype, torch.Size(shape), True, torch.device("cuda", 0)
+
+    def dim(self):
+        return len(self.shape)
+
+    def numel(self):
+        return self.shape.numel()
+
+    def stride(self):
+        return tuple(torch.empty(self.shape, device="meta").stride())
+
+    def is_contiguous(self):
+        return True
+
+    def get_device(self):
+        return 0
+
+    def data_ptr(self):
+        return FAKE
+
+
+@pytest.fixture
+def fakes(monkeypatch):
+    if torch.cuda.is_available():
+        pytest.skip("a GPU is present: the addresses of these tensors are not memory")
+    from block_scaled_mxfp4_amd import grouped
+    grouped._first()
+    monkeypatch.setattr(grouped, "_device", lambda: 0)
+    monkeypatch.setattr(grouped, "_raw_stream", lambda dev: 0)
+    return _Fake
+
+
+def _status(call):
+    with pytest.raises(B.SituMoeError) as e:
+        call()
+    return e.value.status_name
+
+
+def test_sizes_past_32_bits(fakes):
+    """No size loses its upper bits on the way to the library: a call of 2^32 + 128 columns is not one of 128."""
+    bf, f32, u8, i32 = torch.bfloat16, torch.float32, torch.uint8, torch.int32
+    big = (1 << 32) + 128
+    assert _status(lambda: B.situ_moe_quantize_fp8_block128(
+        fakes(bf, 1, 128), fakes(u8, 1, 128), fakes(f32, 1, 1))) == "SITU_E_DEVICE"     # the fakes pass where sizes do
+    assert _status(lambda: B.situ_moe_quantize_fp8_block128(
+        fakes(bf, 1, big), fakes(u8, 1, big), fakes(f32, 1, big // 128))) == "SITU_E_UNSUPPORTED"
+    assert _status(lambda: B.situ_moe_matmul_fp8_block128(
+        fakes(u8, 1, big), fakes(f32, 1, big // 128), fakes(u8, 8, big), fakes(f32, 1, big // 128),
+        out=fakes(bf, 1, 8))) == "SITU_E_UNSUPPORTED"
+    x, w, dy = fakes(bf, 4, 128), fakes(bf, 1, 64, 128), fakes(bf, 4, 64)
+    pairs, many = fakes(i32, 4), fakes(bf, (1 << 31) + 4, 128)
+    for call in (lambda: B.situ_moe_grouped_matmul(x, w, pairs=pairs, x_div=1 << 31, out=dy),
+                 lambda: B.situ_moe_grouped_matmul(many, w, pairs=pairs, x_div=1, out=dy),
+                 lambda: B.situ_moe_grouped_matmul_dgrad(dy, w, pairs=pairs, dy_div=1 << 31, out=x),
+                 lambda: B.situ_moe_grouped_matmul_dgrad(dy, w, pairs=pairs, out_div=1, out=many),
+                 lambda: B.situ_moe_grouped_matmul_wgrad(dy, x, pairs=pairs, x_div=1 << 31, out=fakes(f32, 1, 64, 128)),
+                 lambda: B.situ_moe_grouped_matmul_wgrad(dy, many, pairs=pairs, x_div=1, out=fakes(f32, 1, 64, 128))):
+        assert _status(call) == "SITU_E_UNSUPPORTED"
