@@ -180,7 +180,13 @@ def _quantize(handle, device, dev, rows, cols, stride, xp, codes, scales):
 
 def situ_moe_matmul_fp8_block128(a, a_scale, w, w_scale, *, offsets=None, out=None, out_dtype=None, stream=None):
     """out[r, j] = sum over blocks b of 128 along k of a_scale[r, b]
-    w_scale[e, j // 128, b] (a w^T over block b), in fp32.
+    w_scale[e, j // 128, b] (a w^T over block b).  An fp32 output is an fp32
+    sum.  A bf16 output of more than a few rows sums each block by the FP8
+    matrix instruction, which drops from the products of each aligned eight
+    elements of k what lies 13 bits below the largest one's leading bit: off by
+    at most 7 * 2^-13 of the largest scaled product of each eight, summed, and
+    then rounded to bf16.  Where large products cancel that is more than the
+    rounding; out_dtype=torch.float32 has no such loss.
 
     a: E4M3 codes (uint8 or float8_e4m3fn) [rows, k], a_scale fp32 [rows,
     ceil(k / 128)] (both may have a row stride); w: E4M3 [n, k] with scales

@@ -274,8 +274,18 @@ situ_status situ_moe_quantize_fp8_block128(const uint16_t* x_bf16, int64_t rows,
  * cuteDSL MegaMoE SiTU", the FP8 attention weights with 128 x 128 scales):
  *   out[r, j] = sum_b a_scale[r, b] * w_scale[e, j / 128, b] *
  *               sum_{i in block b} a[r, i] * w[e, j, i]
- * in fp32, rounded once to bf16 for SITU_OUT_BF16.  e is the group of row r:
- * group e holds rows offsets[e] .. offsets[e + 1] - 1.  Rows outside every
+ * The scales' products and the sum over blocks are fp32, rounded once to bf16
+ * for SITU_OUT_BF16.  The sum within a block is fp32 for SITU_OUT_F32, and for
+ * SITU_OUT_BF16 where groups hold few rows (about four on average).  Else
+ * SITU_OUT_BF16 takes the FP8 matrix instruction's sum: it adds the products of
+ * each aligned eight elements of k in fixed point and drops what lies 13 bits
+ * below the leading bit of the largest, so that a result may be off by 7 * 2^-13
+ * of the largest scaled product of each eight, summed over k's eights, before it
+ * is rounded.  That is 1.4e-5 of a sum of normal values, but more than the
+ * rounding to bf16 where large products cancel: take SITU_OUT_F32 where they
+ * may.  So a row's last bits depend on the output type and on how many rows
+ * the call has.  e is the group of row r: group e holds rows
+ * offsets[e] .. offsets[e + 1] - 1.  Rows outside every
  * group are not written.  Sizes: rows 0 .. 2^24, n 1 .. 2^18, k a multiple
  * of 16 up to 2^18, experts 1 .. 1024.  a and w 16-byte aligned, a_stride a
  * multiple of 16; out may have any row stride >= n (rows that start on 16
