@@ -13,7 +13,8 @@ situ_moe_run, situ_moe_run_profiled, situ_moe_run_static, situ_moe_route, situ_m
 situ_moe_tile_weights, situ_moe_quantize_fp8_block128, situ_moe_matmul_fp8_block128,
 situ_moe_grouped_matmul, situ_moe_grouped_matmul_dgrad,
 situ_moe_grouped_matmul_wgrad, situ_moe_status_string, situ_moe_last_error, situ_moe_build_info, situ_moe_tactic_name,
-situ_moe_abi_version, and the measurement aid situ_moe_measure_mfma_peak.
+situ_moe_abi_version, and the aids situ_moe_measure_mfma_peak, situ_moe_matmul_fp8_block128_kernel and
+situ_moe_grouped_matmul_kernel.
 situ_moe(...) is the keyword-only one-call form.
 """
 
@@ -29,6 +30,7 @@ __all__ = [
     "situ_moe_build_info", "situ_moe_tactic_name", "situ_moe_abi_version", "situ_moe",
     "SituMoeFp8Matmul", "SituMoeGrouped", "situ_moe_quantize_fp8_block128", "situ_moe_matmul_fp8_block128",
     "situ_moe_grouped_matmul", "situ_moe_grouped_matmul_dgrad", "situ_moe_grouped_matmul_wgrad",
+    "situ_moe_matmul_fp8_block128_kernel", "situ_moe_grouped_matmul_kernel",
     "make_problem", "make_tensors", "new_workspace", "workspace_view", "ACT_W4A16", "ACT_W4A8", "OUT_F32", "OUT_BF16",
 ]
 
@@ -115,6 +117,8 @@ def load():
         "situ_moe_grouped_matmul": (c_int, [vp, vp]),
         "situ_moe_grouped_matmul_dgrad": (c_int, [vp, vp]),
         "situ_moe_grouped_matmul_wgrad": (c_int, [vp, vp]),
+        "situ_moe_matmul_fp8_block128_kernel": (ctypes.c_char_p, [vp, c_int]),
+        "situ_moe_grouped_matmul_kernel": (ctypes.c_char_p, [c_int, vp, c_int]),
         "situ_moe_measure_mfma_peak": (c_int, [c_int, P(ctypes.c_double)]),
         "situ_moe_status_string": (ctypes.c_char_p, [c_int]),
         "situ_moe_last_error": (ctypes.c_char_p, []),
@@ -434,5 +438,6 @@ def situ_moe(*, hidden_states, hidden_states_scale=None, topk_ids=None, topk_wei
 
 
 from .grouped import (SituMoeFp8Matmul, SituMoeGrouped, situ_moe_grouped_matmul,  # noqa: E402
-                      situ_moe_grouped_matmul_dgrad, situ_moe_grouped_matmul_wgrad, situ_moe_matmul_fp8_block128,
+                      situ_moe_grouped_matmul_dgrad, situ_moe_grouped_matmul_kernel, situ_moe_grouped_matmul_wgrad,
+                      situ_moe_matmul_fp8_block128, situ_moe_matmul_fp8_block128_kernel,
                       situ_moe_quantize_fp8_block128)

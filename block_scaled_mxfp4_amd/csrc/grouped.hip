@@ -1134,9 +1134,10 @@ bool narrow_ok(GroupedMode mode, const GroupedArgs& a) {
 // Groups are taken to hold rows / experts rows and to need 0.6 of a tile more.
 // Where there is more than a round the last one of grouped rows, whose number
 // is only estimated, is taken as 0.3.
-enum Shape { kSmall, kMid, kShort, kLarge, kPair, kSplit, kSplit2, kThin };
+enum Shape { kSmall, kMid, kShort, kLarge, kPair, kSplit, kSplit2, kThin, kFew };
 Shape choose(GroupedMode mode, const GroupedArgs& a, int cus) {
   const bool wg = mode == kGWgrad, f8 = mode == kGFwd8 || mode == kGFwd8x;
+  if ((mode == kGFwd || f8) && few_rows(a)) return kFew;
   const int q = f8 ? 128 : 64;
   const double mean = (double)a.rows / a.experts;
   const double steps = wg ? mean / 64 + 0.5 : (double)((a.K + q - 1) / q);
@@ -1192,22 +1193,46 @@ hipError_t launch_mode(GroupedArgs& a, int cus, hipStream_t s) {
     case kThin:
       if constexpr (MODE == kGFwd || MODE == kGDgrad) return launch_thin<Cfg<64, 128, 2, 2, 3, 4, true>, MODE>(a, cus, s);
       break;
+    case kFew:
+      if constexpr (MODE == kGFwd || MODE == kGFwd8 || MODE == kGFwd8x) return launch_grouped_few((GroupedMode)MODE, a, cus, s);
+      break;
   }
   return hipErrorInvalidValue;
 }
 
+GroupedMode with_output(GroupedMode mode, const GroupedArgs& a) {
+  return mode == kGFwd8 && a.out_f32 ? kGFwd8x : mode;
+}
+// Whether a weight gradient looks its rows up (IDX).
+bool indexed(const GroupedArgs& a) { return a.pairs && (a.t_div.div || a.c_div.div); }
+
 }  // namespace
 
+const char* grouped_kernel_name(GroupedMode mode, const GroupedArgs& a, int cus) {
+  const bool idx = mode == kGWgrad && indexed(a);
+  switch (choose(with_output(mode, a), a, cus)) {
+    case kSmall: return idx ? "grouped_kernel 64x64 indexed" : "grouped_kernel 64x64";
+    case kMid: return idx ? "grouped_kernel 64x128 indexed" : "grouped_kernel 64x128";
+    case kShort: return "grouped_kernel 64x128 short";
+    case kLarge: return idx ? "grouped_kernel 128x128 indexed" : "grouped_kernel 128x128";
+    case kPair: return idx ? "grouped_pair_kernel indexed" : "grouped_pair_kernel";
+    case kSplit: return "grouped_split_kernel 64x32";
+    case kSplit2: return "grouped_split_kernel 64x64";
+    case kThin: return "grouped_thin_kernel";
+    case kFew: return few_wide(a, cus) ? "grouped_few_kernel 32" : "grouped_few_kernel 16";
+  }
+  return nullptr;
+}
+
 hipError_t launch_grouped(GroupedMode mode, GroupedArgs& a, int cus, hipStream_t s) {
-  if (mode == kGFwd8 && a.out_f32) mode = kGFwd8x;
-  if ((mode == kGFwd || mode == kGFwd8 || mode == kGFwd8x) && few_rows(a)) return launch_grouped_few(mode, a, cus, s);
+  mode = with_output(mode, a);
   switch (mode) {
     case kGFwd: return launch_mode<kGFwd, false>(a, cus, s);
     case kGFwd8: return launch_mode<kGFwd8, false>(a, cus, s);
     case kGFwd8x: return launch_mode<kGFwd8x, false>(a, cus, s);
     case kGDgrad: return launch_mode<kGDgrad, false>(a, cus, s);
     case kGWgrad:
-      if (a.pairs && (a.t_div.div || a.c_div.div)) return launch_mode<kGWgrad, true>(a, cus, s);
+      if (indexed(a)) return launch_mode<kGWgrad, true>(a, cus, s);
       return launch_mode<kGWgrad, false>(a, cus, s);
   }
   return hipErrorInvalidValue;

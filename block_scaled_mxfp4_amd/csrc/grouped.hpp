@@ -57,9 +57,12 @@ struct GroupedArgs {
 };
 
 hipError_t launch_grouped(GroupedMode mode, GroupedArgs& a, int cus, hipStream_t s);
+// The kernel (and tile) launch_grouped takes.
+const char* grouped_kernel_name(GroupedMode mode, const GroupedArgs& a, int cus);
 
 // The forward products where groups hold few rows (grouped_few.hip).
 bool few_rows(const GroupedArgs& a);
+bool few_wide(const GroupedArgs& a, int cus);
 hipError_t launch_grouped_few(GroupedMode mode, GroupedArgs& a, int cus, hipStream_t s);
 
 struct QuantBlockArgs {

@@ -1,5 +1,6 @@
 // Entry points of the products grouped by expert and of the E4M3 products
-// with scales per 128: argument checks, then one launch each.
+// with scales per 128: argument checks, then one launch each (or the name of
+// the kernel that would be launched).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -54,7 +55,9 @@ situ_status check_out(const char* name, const void* p, int64_t stride, int32_t w
   return SITU_OK;
 }
 
-situ_status grouped(situ::GroupedMode mode, const situ_moe_grouped_t* p, void* hip_stream) {
+// Checks the arguments and fills in the kernels'; `nothing`: there is nothing to compute.
+situ_status grouped_args(situ::GroupedMode mode, const situ_moe_grouped_t* p, situ::GroupedArgs& a, bool& nothing) {
+  nothing = false;
   if (!p) return fail_status(SITU_E_NULL_ARG, "args is NULL");
   situ_status st = check_sizes(p->rows, p->n, p->k, p->experts, p->out_dtype, p->reserved, p->offsets);
   if (st != SITU_OK) return st;
@@ -76,14 +79,13 @@ situ_status grouped(situ::GroupedMode mode, const situ_moe_grouped_t* p, void* h
     st = fwd ? check_out("y", p->y, p->y_stride, n, out_size) : check_in("y", p->y, p->y_stride, n, 2);
     if (st != SITU_OK) return st;
   } else if (!wgrad) {
+    nothing = true;
     return SITU_OK;
   }
   st = wgrad ? check_out("w", p->w, k, k, out_size) : check_in("w", p->w, k, k, 2);
   if (st != SITU_OK) return st;
-  int cus = 0;
-  if ((st = situ::require_device(&cus)) != SITU_OK) return st;
 
-  situ::GroupedArgs a{};
+  a = situ::GroupedArgs{};
   a.offsets = p->offsets;
   a.pairs = indexed ? p->pairs : nullptr;
   a.rows = p->rows;
@@ -110,7 +112,61 @@ situ_status grouped(situ::GroupedMode mode, const situ_moe_grouped_t* p, void* h
   }
   a.out_stride = out_stride * out_size;
   a.vec = aligned(a.out, 16) && a.out_stride % 16 == 0;
-  return launched(situ::launch_grouped(mode, a, cus, static_cast<hipStream_t>(hip_stream)), "grouped matmul");
+  return SITU_OK;
+}
+
+situ_status fp8_args(const situ_moe_fp8_matmul_t* p, situ::GroupedArgs& a, bool& nothing) {
+  nothing = false;
+  if (!p) return fail_status(SITU_E_NULL_ARG, "args is NULL");
+  situ_status st = check_sizes(p->rows, p->n, p->k, p->experts, p->out_dtype, p->reserved, p->offsets);
+  if (st != SITU_OK) return st;
+  if (p->k % 16) return fail_status(SITU_E_BAD_SHAPE, "k %d must be a multiple of 16", p->k);
+  if ((nothing = p->rows == 0)) return SITU_OK;
+  const int out_size = p->out_dtype == SITU_OUT_F32 ? 4 : 2;
+  const int32_t kb = (p->k + 127) / 128;
+  if ((st = check_in("a", p->a, p->a_stride, p->k, 1)) != SITU_OK) return st;
+  if ((st = check_in("w", p->w, p->k, p->k, 1)) != SITU_OK) return st;
+  if ((st = check_out("out", p->out, p->out_stride, p->n, out_size)) != SITU_OK) return st;
+  if ((st = check_out("a_scale", p->a_scale, p->a_scale_stride, kb, 4)) != SITU_OK) return st;
+  if (p->a_scale_stride >= kMaxScaleStride)
+    return fail_status(SITU_E_UNSUPPORTED, "a_scale: stride %lld (below 2^22)", (long long)p->a_scale_stride);
+  if ((st = check_out("w_scale", p->w_scale, kb, kb, 4)) != SITU_OK) return st;
+  a = situ::GroupedArgs{};
+  a.t = p->a; a.t_stride = p->a_stride; a.t_rows = p->rows;
+  a.c = p->w; a.c_stride = p->k; a.c_expert = (int64_t)p->n * p->k;
+  a.t_scale = p->a_scale; a.ts_stride = p->a_scale_stride; a.c_scale = p->w_scale;
+  a.offsets = p->offsets;
+  a.o_rows = p->rows;
+  a.rows = p->rows; a.experts = p->experts;
+  a.N = p->n; a.K = p->k;
+  a.out = p->out; a.out_stride = p->out_stride * out_size; a.out_f32 = p->out_dtype == SITU_OUT_F32;
+  a.vec = aligned(a.out, 16) && a.out_stride % 16 == 0;
+  return SITU_OK;
+}
+
+// One launch of the call described by `a`.
+situ_status launch(situ_status checked, bool nothing, situ::GroupedMode mode, situ::GroupedArgs& a, void* hip_stream,
+                   const char* what) {
+  if (checked != SITU_OK || nothing) return checked;
+  int cus = 0;
+  const situ_status st = situ::require_device(&cus);
+  if (st != SITU_OK) return st;
+  return launched(situ::launch_grouped(mode, a, cus, static_cast<hipStream_t>(hip_stream)), what);
+}
+const char* kernel(situ_status checked, bool nothing, situ::GroupedMode mode, const situ::GroupedArgs& a, int32_t cus) {
+  if (checked != SITU_OK) return nullptr;
+  if (nothing || cus < 1) {
+    fail_status(SITU_E_BAD_SHAPE, nothing ? "a call without rows launches nothing" : "cus %d", cus);
+    return nullptr;
+  }
+  return situ::grouped_kernel_name(mode, a, cus);
+}
+
+situ_status grouped(situ::GroupedMode mode, const situ_moe_grouped_t* p, void* hip_stream) {
+  situ::GroupedArgs a;
+  bool nothing;
+  const situ_status st = grouped_args(mode, p, a, nothing);
+  return launch(st, nothing, mode, a, hip_stream, "grouped matmul");
 }
 
 }  // namespace
@@ -136,33 +192,10 @@ situ_status situ_moe_quantize_fp8_block128(const uint16_t* x, int64_t rows, int3
 }
 
 situ_status situ_moe_matmul_fp8_block128(const situ_moe_fp8_matmul_t* p, void* hip_stream) {
-  if (!p) return fail_status(SITU_E_NULL_ARG, "args is NULL");
-  situ_status st = check_sizes(p->rows, p->n, p->k, p->experts, p->out_dtype, p->reserved, p->offsets);
-  if (st != SITU_OK) return st;
-  if (p->k % 16) return fail_status(SITU_E_BAD_SHAPE, "k %d must be a multiple of 16", p->k);
-  if (p->rows == 0) return SITU_OK;
-  const int out_size = p->out_dtype == SITU_OUT_F32 ? 4 : 2;
-  const int32_t kb = (p->k + 127) / 128;
-  if ((st = check_in("a", p->a, p->a_stride, p->k, 1)) != SITU_OK) return st;
-  if ((st = check_in("w", p->w, p->k, p->k, 1)) != SITU_OK) return st;
-  if ((st = check_out("out", p->out, p->out_stride, p->n, out_size)) != SITU_OK) return st;
-  if ((st = check_out("a_scale", p->a_scale, p->a_scale_stride, kb, 4)) != SITU_OK) return st;
-  if (p->a_scale_stride >= kMaxScaleStride)
-    return fail_status(SITU_E_UNSUPPORTED, "a_scale: stride %lld (below 2^22)", (long long)p->a_scale_stride);
-  if ((st = check_out("w_scale", p->w_scale, kb, kb, 4)) != SITU_OK) return st;
-  int cus = 0;
-  if ((st = situ::require_device(&cus)) != SITU_OK) return st;
-  situ::GroupedArgs a{};
-  a.t = p->a; a.t_stride = p->a_stride; a.t_rows = p->rows;
-  a.c = p->w; a.c_stride = p->k; a.c_expert = (int64_t)p->n * p->k;
-  a.t_scale = p->a_scale; a.ts_stride = p->a_scale_stride; a.c_scale = p->w_scale;
-  a.offsets = p->offsets;
-  a.o_rows = p->rows;
-  a.rows = p->rows; a.experts = p->experts;
-  a.N = p->n; a.K = p->k;
-  a.out = p->out; a.out_stride = p->out_stride * out_size; a.out_f32 = p->out_dtype == SITU_OUT_F32;
-  a.vec = aligned(a.out, 16) && a.out_stride % 16 == 0;
-  return launched(situ::launch_grouped(situ::kGFwd8, a, cus, static_cast<hipStream_t>(hip_stream)), "FP8 matmul");
+  situ::GroupedArgs a;
+  bool nothing;
+  const situ_status st = fp8_args(p, a, nothing);
+  return launch(st, nothing, situ::kGFwd8, a, hip_stream, "FP8 matmul");
 }
 
 situ_status situ_moe_grouped_matmul(const situ_moe_grouped_t* args, void* hip_stream) {
@@ -173,6 +206,24 @@ situ_status situ_moe_grouped_matmul_dgrad(const situ_moe_grouped_t* args, void* 
 }
 situ_status situ_moe_grouped_matmul_wgrad(const situ_moe_grouped_t* args, void* hip_stream) {
   return grouped(situ::kGWgrad, args, hip_stream);
+}
+
+const char* situ_moe_matmul_fp8_block128_kernel(const situ_moe_fp8_matmul_t* p, int32_t cus) {
+  situ::GroupedArgs a;
+  bool nothing;
+  const situ_status st = fp8_args(p, a, nothing);
+  return kernel(st, nothing, situ::kGFwd8, a, cus);
+}
+const char* situ_moe_grouped_matmul_kernel(int32_t direction, const situ_moe_grouped_t* p, int32_t cus) {
+  constexpr situ::GroupedMode kModes[] = {situ::kGFwd, situ::kGDgrad, situ::kGWgrad};
+  if (direction < 0 || direction > 2) {
+    fail_status(SITU_E_UNSUPPORTED, "direction %d (0 the product, 1 dgrad, 2 wgrad)", direction);
+    return nullptr;
+  }
+  situ::GroupedArgs a;
+  bool nothing;
+  const situ_status st = grouped_args(kModes[direction], p, a, nothing);
+  return kernel(st, nothing, kModes[direction], a, cus);
 }
 
 }  // extern "C"

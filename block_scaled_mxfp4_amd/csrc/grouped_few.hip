@@ -212,13 +212,9 @@ hipError_t launch_as(GroupedArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Sixteen columns a workgroup of eight waves where the columns of 32 would
-// leave CUs idle, else 32 columns and four waves.
 template <bool F8>
 hipError_t launch_type(GroupedArgs& a, int cus, hipStream_t s) {
-  const int64_t wide = (int64_t)a.experts * ((a.N + 31) / 32);
-  if (wide < 2 * cus) return launch_as<F8, 8, 2>(a, s);
-  return launch_as<F8, 4, 4>(a, s);
+  return few_wide(a, cus) ? launch_as<F8, 4, 4>(a, s) : launch_as<F8, 8, 2>(a, s);
 }
 
 }  // namespace
@@ -230,6 +226,12 @@ hipError_t launch_type(GroupedArgs& a, int cus, hipStream_t s) {
 // One workgroup for each group and 16 columns has to fit a grid.
 bool few_rows(const GroupedArgs& a) {
   return a.rows <= std::max<int64_t>(8, 4 * (int64_t)a.experts) && (int64_t)a.experts * ((a.N + 15) / 16) <= 1 << 22;
+}
+
+// Sixteen columns a workgroup of eight waves where the columns of 32 would
+// leave CUs idle, else 32 columns and four waves.
+bool few_wide(const GroupedArgs& a, int cus) {
+  return (int64_t)a.experts * ((a.N + 31) / 32) >= 2 * cus;
 }
 
 hipError_t launch_grouped_few(GroupedMode mode, GroupedArgs& a, int cus, hipStream_t s) {

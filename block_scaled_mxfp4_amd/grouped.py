@@ -336,3 +336,20 @@ def situ_moe_grouped_matmul_wgrad(dy, x, offsets=None, *, pairs=None, dy_div=0, 
     experts = 1 if offsets is None else max(offsets.numel() - 1, 0)
     return _at(dev, stream, _grouped, "situ_moe_grouped_matmul_wgrad", 2, 0 if dy_div else 1, dy.device, dev, [x, dy, out],
                offsets, pairs, int(x_div), int(dy_div), experts, n, k, out_dtype)
+
+
+def _name(kernel):
+    if kernel is None:
+        raise _B.SituMoeError(2, _B.situ_moe_last_error())
+    return kernel.decode()
+
+
+def situ_moe_matmul_fp8_block128_kernel(args, cus=256):
+    """The kernel that a SituMoeFp8Matmul is given to on a device of `cus`
+    compute units; nothing is launched and its addresses are not followed."""
+    return _name(_B.load().situ_moe_matmul_fp8_block128_kernel(ctypes.byref(args), cus))
+
+
+def situ_moe_grouped_matmul_kernel(direction, args, cus=256):
+    """The same of a SituMoeGrouped.  direction: 0 the product, 1 dgrad, 2 wgrad."""
+    return _name(_B.load().situ_moe_grouped_matmul_kernel(direction, ctypes.byref(args), cus))

@@ -349,6 +349,15 @@ situ_status situ_moe_grouped_matmul(const situ_moe_grouped_t* args, void* hip_st
 situ_status situ_moe_grouped_matmul_dgrad(const situ_moe_grouped_t* args, void* hip_stream);
 situ_status situ_moe_grouped_matmul_wgrad(const situ_moe_grouped_t* args, void* hip_stream);
 
+/* The kernel (and tile) that such a call is given to on a device of `cus`
+ * compute units, for tests and profiles: the arguments are checked as the call
+ * checks them, no pointer is followed, nothing is launched and no device is
+ * needed.  NULL if the call would be refused or has no rows to compute
+ * (situ_moe_last_error says which).  direction: 0 the product, 1 dgrad,
+ * 2 wgrad.  The names are not part of the interface. */
+const char* situ_moe_matmul_fp8_block128_kernel(const situ_moe_fp8_matmul_t* args, int32_t cus);
+const char* situ_moe_grouped_matmul_kernel(int32_t direction, const situ_moe_grouped_t* args, int32_t cus);
+
 /* Measurement aid for the roofline of the w4a8 GEMMs (not part of the
  * layer): the sustained rate of v_mfma_scale_f32_16x16x128_f8f6f4 with E2M1 x
  * E4M3 operands (the instruction the w4a8 FC1 kernels issue; 65536 flops

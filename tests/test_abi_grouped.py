@@ -190,3 +190,29 @@ def test_sizes_past_32_bits(fakes):
                  lambda: B.situ_moe_grouped_matmul_wgrad(dy, x, pairs=pairs, x_div=1 << 31, out=fakes(f32, 1, 64, 128)),
                  lambda: B.situ_moe_grouped_matmul_wgrad(dy, many, pairs=pairs, x_div=1, out=fakes(f32, 1, 64, 128))):
         assert _status(call) == "SITU_E_UNSUPPORTED"
+
+
+def test_kernel_of_a_call():
+    """The calls of grouped_kernels.py reach the kernels they name on 256 compute units, and all kernels are named."""
+    import grouped_kernels as G
+    for c in G.CASES:
+        product, f32, kernel, counts, n, k, sides = c
+        rows, experts = G.rows_of(counts)
+        for out in (False, True) if f32 is None else (f32,):
+            assert G.kernel_of(product, rows, experts, n, k, f32=out, offsets=not isinstance(counts, int),
+                               sides=sides) == kernel, G.case_id(c)
+    for product, kernels in G.KERNELS.items():
+        assert {c[2] for c in G.CASES if c[0] == product} == {"grouped_" + name for name in kernels}
+
+
+def test_kernel_of_a_refused_call():
+    import grouped_kernels as G
+    for args, kw in ((("fwd", 4, 3, 64, 12), {}), (("dgrad", 4, 3, 60, 64), {}), (("fp8", 4, 1, 64, 24), {}),
+                     (("fwd", 0, 3, 64, 64), {}), (("fwd", 4, 3, 64, 64), dict(cus=0)),
+                     (("fwd", 4, 3, 64, 64), dict(offsets=False)), (("fp8", 0, 1, 64, 64), {})):
+        with pytest.raises(B.SituMoeError):
+            G.kernel_of(*args, **kw)
+    with pytest.raises(B.SituMoeError):
+        B.situ_moe_grouped_matmul_kernel(3, B.SituMoeGrouped())
+    assert B.load().situ_moe_matmul_fp8_block128_kernel(None, 256) is None
+    assert B.load().situ_moe_grouped_matmul_kernel(0, None, 256) is None
