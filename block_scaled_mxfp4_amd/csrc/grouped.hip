@@ -91,7 +91,7 @@ struct Tile {
 __device__ __forceinline__ int swz_t(int row) { return row & 7; }
 __device__ __forceinline__ int swz_c(int row) { return (row & 3) | ((row >> 1) & 4); }
 
-// The elements 8 d .. 8 d + 7 of q that lie below `valid`, as masks of bf16 pairs.
+// The elements 2 d and 2 d + 1 of q that lie below `valid`, as a mask of a bf16 pair.
 __device__ __forceinline__ uint32_t pair_mask(int valid, int d) {
   return valid >= 2 * d + 2 ? 0xffffffffu : (valid == 2 * d + 1 ? 0xffffu : 0u);
 }
@@ -512,7 +512,8 @@ struct Kernel {
   // Whether none of the wave's rows or columns are stored: it then makes its
   // requests and keeps the barriers, but leaves the LDS and the matrix cores
   // to the others.  A group's last tile is half empty on average: 16384 rows in
-  // 104 of 112 groups, 1536 x 3584 E4M3, 212 us without this and 196 with it.
+  // 104 of 112 groups, 1536 x 3584 E4M3, 212 us without this and 196 with it, timed
+  // in turn on one card (185 to 190 on others).
   static __device__ __forceinline__ bool idle(const GroupedArgs& a, const Tile& x, int wm, int wn) {
     return x.m0 + 16 * wm * C::TT >= (kWg ? a.M : x.hi) || x.n0 + 16 * wn * C::CT >= a.N;
   }
@@ -644,7 +645,9 @@ __device__ __forceinline__ void part_barrier() {
   asm volatile("s_barrier" ::: "memory");
   __builtin_amdgcn_sched_barrier(0);
 }
-// Wait until this wave's requests but the last N have landed.
+// Wait until this wave's requests but the last N have landed.  They complete in
+// the order issued, so a store or a spilled register among them can only make
+// the wait longer.
 template <int N>
 __device__ __forceinline__ void land() {
   __builtin_amdgcn_sched_barrier(0);
@@ -965,8 +968,12 @@ __global__ __launch_bounds__(256, 4) void grouped_thin_kernel(GroupedArgs a) {
 // A step (256 x 256 x 64 bf16) takes 1.18 us with one tile on the chip, 0.89
 // without its requests, and 1.55 with all of them in R0, waited for in R3 (4096
 // x 4096 x 16384: 455 us against 523).  With all CUs busy it takes 1.75 (E4M3,
-// 128 deep, 2.0), and 1.42 to 1.58 without requests: the matrix cores are the
-// bound.  8192 x 7168 x 3584 E4M3: 217 us, 1.94 PFLOP/s.
+// 128 deep, 2.0), and 1.42 to 1.58 without requests.  The matrix cores are busy
+// 65 % of the forward kernel's time in bf16 and 52 % in E4M3, so no one thing is
+// the bound: requests are a fifth of a step, and the reading parts' barriers and
+// waits, the rounds' last tiles and the stores the rest.  8192 x 7168 x 3584
+// E4M3: 217 and 249 us on two cards (1.94 and 1.69 PFLOP/s), whose clocks under
+// this load differ.
 template <class C, int MODE, bool IDX>
 __global__ __launch_bounds__(512, 2) void grouped_pair_kernel(GroupedArgs a) {
   using K = Kernel<C, MODE, false>;
@@ -1073,7 +1080,9 @@ __global__ __launch_bounds__(512, 2) void grouped_pair_kernel(GroupedArgs a) {
   }
 }
 
-// As many workgroups as the chip holds, so long as a group's share of the rows has tiles for them.
+// As many workgroups as the chip holds, so long as a group's share of the rows
+// has tiles for them.  The share is the mean: 16384 rows x 768 x 32 in 112 groups
+// take 10 us, with half of the rows in one group 62, with all in one 120.
 template <class C, int MODE>
 hipError_t launch_thin(GroupedArgs& a, int cus, hipStream_t s) {
   a.n_tiles = (a.N + C::BN - 1) / C::BN;
@@ -1132,6 +1141,9 @@ bool narrow_ok(GroupedMode mode, const GroupedArgs& a) {
 // One step goes to grouped_thin_kernel; two to Short, three workgroups of which
 // fit a CU and hide their fixed parts best.
 // Groups are taken to hold rows / experts rows and to need 0.6 of a tile more.
+// Where many rows belong to no group (the layer's whole routing table on an EP
+// shard) that is too many: 128 pairs in 76 of 112 groups, 16 x 3584, 8.4 us as
+// 128 rows and 14.7 as the first 128 of 1024.
 // Where there is more than a round the last one of grouped rows, whose number
 // is only estimated, is taken as 0.3.
 enum Shape { kSmall, kMid, kShort, kLarge, kPair, kSplit, kSplit2, kThin, kFew };

@@ -19,10 +19,12 @@ namespace situ {
 
 namespace {
 
-// x / s correctly rounded for the values met here: q = x * rcp(s) is within
-// two ulp, and one correction by the exact remainder x - q s lands on the
-// nearest fp32 (s >= 2^-109 and |q| <= 448 (1 + 2^-23) keep every step in the
-// normal range or exact).  A block with an infinity has scale inf and codes
+// x / s correctly rounded where it counts: q = x * rcp(s) is within two ulp, and
+// one correction by the remainder x - q s lands on the nearest fp32.  Only in
+// blocks with a maximum below 2^-98 can the remainder of an element 2^13 or more
+// below it leave the normal range, and the quotient be an ulp off; its E4M3 code
+// is the same (every pair of bf16 mantissas at 22 exponent distances, in
+// rational arithmetic).  A block with an infinity has scale inf and codes
 // of NaN; a NaN element gives NaN and leaves the block's scale to the others.
 __device__ __forceinline__ float quotient(float x, float s, float r) {
   const float q = x * r;

@@ -5,7 +5,9 @@ As in the rest of the binding nothing here computes on tensor values: the
 arguments are checked, outputs that are not given are allocated, and each call
 enqueues one kernel on the stream (a torch.cuda.Stream, a raw handle, or None
 for the current stream of the tensors' device).  Calls run on the tensors'
-device whichever device is current.
+device whichever device is current.  An output carries no autograd graph,
+whether or not an input requires grad: a caller who trains calls the _dgrad and
+_wgrad products.
 
 A decode-sized call costs more on the host than on the GPU, so the checks test
 what a right argument has in one expression and look for the reason only when
