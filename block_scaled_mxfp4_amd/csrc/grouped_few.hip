@@ -231,7 +231,7 @@ bool few_rows(const GroupedArgs& a) {
 // Sixteen columns a workgroup of eight waves where the columns of 32 would
 // leave CUs idle, else 32 columns and four waves.
 bool few_wide(const GroupedArgs& a, int cus) {
-  return (int64_t)a.experts * ((a.N + 31) / 32) >= 2 * cus;
+  return (int64_t)a.experts * ((a.N + 31) / 32) >= 2 * (int64_t)cus;
 }
 
 hipError_t launch_grouped_few(GroupedMode mode, GroupedArgs& a, int cus, hipStream_t s) {

@@ -216,3 +216,12 @@ def test_kernel_of_a_refused_call():
         B.situ_moe_grouped_matmul_kernel(3, B.SituMoeGrouped())
     assert B.load().situ_moe_matmul_fp8_block128_kernel(None, 256) is None
     assert B.load().situ_moe_grouped_matmul_kernel(0, None, 256) is None
+
+
+def test_kernel_on_any_number_of_units():
+    import grouped_kernels as G
+    names = {"grouped_" + k for k in G.KERNELS["fwd"]}
+    for cus in (1, 8, 304, (1 << 31) - 1):
+        for rows, experts, n, k in ((2, 3, 64, 64), (700, 16, 1032, 520), (1 << 24, 1024, 1 << 18, 1 << 18)):
+            assert G.kernel_of("fwd", rows, experts, n, k, cus=cus) in names
+    assert G.kernel_of("fwd", 2, 3, 64, 64, cus=(1 << 31) - 1) == "grouped_few_kernel 16"   # never enough columns for them
