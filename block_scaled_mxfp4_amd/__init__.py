@@ -12,7 +12,8 @@ Names mirror the C entry points: situ_moe_plan, situ_moe_valid_tactics,
 situ_moe_run, situ_moe_run_profiled, situ_moe_run_static, situ_moe_route, situ_moe_quantize_mxfp8,
 situ_moe_tile_weights, situ_moe_quantize_fp8_block128, situ_moe_matmul_fp8_block128,
 situ_moe_grouped_matmul, situ_moe_grouped_matmul_dgrad,
-situ_moe_grouped_matmul_wgrad, situ_moe_status_string, situ_moe_last_error, situ_moe_build_info, situ_moe_tactic_name,
+situ_moe_grouped_matmul_wgrad, situ_moe_router, situ_moe_router_backward, situ_moe_activation,
+situ_moe_activation_backward, situ_moe_combine, situ_moe_combine_backward, situ_moe_adapters, situ_moe_status_string, situ_moe_last_error, situ_moe_build_info, situ_moe_tactic_name,
 situ_moe_abi_version, and the aids situ_moe_measure_mfma_peak, situ_moe_matmul_fp8_block128_kernel and
 situ_moe_grouped_matmul_kernel.
 situ_moe(...) is the keyword-only one-call form.
@@ -31,6 +32,9 @@ __all__ = [
     "SituMoeFp8Matmul", "SituMoeGrouped", "situ_moe_quantize_fp8_block128", "situ_moe_matmul_fp8_block128",
     "situ_moe_grouped_matmul", "situ_moe_grouped_matmul_dgrad", "situ_moe_grouped_matmul_wgrad",
     "situ_moe_matmul_fp8_block128_kernel", "situ_moe_grouped_matmul_kernel",
+    "SituMoeRouter", "SituMoeRouterBackward", "SituMoeActivation", "SituMoeCombine", "SituMoeAdapters",
+    "situ_moe_router", "situ_moe_router_backward", "situ_moe_activation", "situ_moe_activation_backward",
+    "situ_moe_combine", "situ_moe_combine_backward", "situ_moe_adapters",
     "make_problem", "make_tensors", "new_workspace", "workspace_view", "ACT_W4A16", "ACT_W4A8", "OUT_F32", "OUT_BF16",
 ]
 
@@ -119,6 +123,15 @@ def load():
         "situ_moe_grouped_matmul_wgrad": (c_int, [vp, vp]),
         "situ_moe_matmul_fp8_block128_kernel": (ctypes.c_char_p, [vp, c_int]),
         "situ_moe_grouped_matmul_kernel": (ctypes.c_char_p, [c_int, vp, c_int]),
+        "situ_moe_router": (c_int, [vp, vp]),
+        "situ_moe_router_backward": (c_int, [vp, vp]),
+        "situ_moe_activation": (c_int, [vp, vp]),
+        "situ_moe_activation_backward": (c_int, [vp, vp]),
+        "situ_moe_combine": (c_int, [vp, vp]),
+        "situ_moe_combine_backward": (c_int, [vp, vp]),
+        "situ_moe_adapters": (c_int, [vp, vp]),
+        "situ_moe_router_workspace": (c_int, [vp, vp]),
+        "situ_moe_adapters_workspace": (c_int, [vp, vp]),
         "situ_moe_measure_mfma_peak": (c_int, [c_int, P(ctypes.c_double)]),
         "situ_moe_status_string": (ctypes.c_char_p, [c_int]),
         "situ_moe_last_error": (ctypes.c_char_p, []),
@@ -441,3 +454,6 @@ from .grouped import (SituMoeFp8Matmul, SituMoeGrouped, situ_moe_grouped_matmul,
                       situ_moe_grouped_matmul_dgrad, situ_moe_grouped_matmul_kernel, situ_moe_grouped_matmul_wgrad,
                       situ_moe_matmul_fp8_block128, situ_moe_matmul_fp8_block128_kernel,
                       situ_moe_quantize_fp8_block128)
+from .routed import (SituMoeActivation, SituMoeAdapters, SituMoeCombine, SituMoeRouter,  # noqa: E402
+                     SituMoeRouterBackward, situ_moe_activation, situ_moe_activation_backward, situ_moe_adapters,
+                     situ_moe_combine, situ_moe_combine_backward, situ_moe_router, situ_moe_router_backward)

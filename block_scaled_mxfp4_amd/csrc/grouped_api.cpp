@@ -5,23 +5,20 @@
 #include <stdint.h>
 
 #include "../../include/situ_moe.h"
+#include "checks.hpp"
 #include "grouped.hpp"
 #include "internal.hpp"
 
 namespace {
 
+using situ::aligned;
+using situ::check_in;
+using situ::check_out;
 using situ::fail_status;
+using situ::launched;
 
 constexpr int32_t kMaxRows = 1 << 24, kMaxSide = 1 << 18, kMaxExperts = 1024;
-constexpr int64_t kMaxStride = (int64_t)1 << 40;
 constexpr int64_t kMaxScaleStride = 1 << 22;   // 64 rows of scales within 32 bits of bytes
-
-bool aligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
-
-situ_status launched(hipError_t e, const char* what) {
-  if (e == hipSuccess) return SITU_OK;
-  return fail_status(SITU_E_LAUNCH, "%s launch failed: %s", what, hipGetErrorString(e));
-}
 
 situ_status check_sizes(int32_t rows, int32_t n, int32_t k, int32_t experts, int32_t out_dtype, int32_t reserved,
                         const int32_t* offsets) {
@@ -35,23 +32,6 @@ situ_status check_sizes(int32_t rows, int32_t n, int32_t k, int32_t experts, int
   if (reserved != 0) return fail_status(SITU_E_BAD_SHAPE, "reserved is %d, not 0", reserved);
   if (!offsets && experts != 1) return fail_status(SITU_E_NULL_ARG, "offsets is NULL with %d experts", experts);
   if (!aligned(offsets, 4)) return fail_status(SITU_E_BAD_SHAPE, "offsets must be 4-byte aligned");
-  return SITU_OK;
-}
-
-// An input (bf16 or E4M3 rows of `width` elements of `size` bytes).
-situ_status check_in(const char* name, const void* p, int64_t stride, int32_t width, int size) {
-  if (!p) return fail_status(SITU_E_NULL_ARG, "%s is NULL", name);
-  if (!aligned(p, 16)) return fail_status(SITU_E_BAD_SHAPE, "%s must be 16-byte aligned", name);
-  if (stride < width || stride > kMaxStride || stride * size % 16)
-    return fail_status(SITU_E_BAD_SHAPE, "%s: stride %lld (at least %d, a multiple of %d)", name, (long long)stride,
-                       width, 16 / size);
-  return SITU_OK;
-}
-situ_status check_out(const char* name, const void* p, int64_t stride, int32_t width, int size) {
-  if (!p) return fail_status(SITU_E_NULL_ARG, "%s is NULL", name);
-  if (!aligned(p, (uintptr_t)size)) return fail_status(SITU_E_BAD_SHAPE, "%s must be %d-byte aligned", name, size);
-  if (stride < width || stride > kMaxStride)
-    return fail_status(SITU_E_BAD_SHAPE, "%s: stride %lld (at least %d)", name, (long long)stride, width);
   return SITU_OK;
 }
 

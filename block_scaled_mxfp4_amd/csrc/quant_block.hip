@@ -14,22 +14,11 @@
 
 #include "common.hpp"
 #include "grouped.hpp"
+#include "quant_block.hpp"
 
 namespace situ {
 
 namespace {
-
-// x / s correctly rounded where it counts: q = x * rcp(s) is within two ulp, and
-// one correction by the remainder x - q s lands on the nearest fp32.  Only in
-// blocks with a maximum below 2^-98 can the remainder of an element 2^13 or more
-// below it leave the normal range, and the quotient be an ulp off; its E4M3 code
-// is the same (every pair of bf16 mantissas at 22 exponent distances, in
-// rational arithmetic).  A block with an infinity has scale inf and codes
-// of NaN; a NaN element gives NaN and leaves the block's scale to the others.
-__device__ __forceinline__ float quotient(float x, float s, float r) {
-  const float q = x * r;
-  return fmaf(fmaf(-q, s, x), r, q);
-}
 
 constexpr int kAtOnce = 4;   // pieces a thread requests before it computes
 
@@ -67,18 +56,10 @@ __global__ __launch_bounds__(256) void quant_block128_kernel(QuantBlockArgs a, i
 #pragma unroll
       for (int m = 1; m < 16; m *= 2) amax = fmaxf(amax, __shfl_xor(amax, m, kWave));
       if (!in[p]) continue;
-      const float scale = fmaxf(amax, 0x1p-100f) / 448.0f;
-      const float r = 1.0f / scale;
-      uint32_t o[2] = {0, 0};
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        int d = 0;
-        d = __builtin_amdgcn_cvt_pk_fp8_f32(quotient(f[4 * i], scale, r), quotient(f[4 * i + 1], scale, r), d, false);
-        d = __builtin_amdgcn_cvt_pk_fp8_f32(quotient(f[4 * i + 2], scale, r), quotient(f[4 * i + 3], scale, r), d, true);
-        o[i] = (uint32_t)d;
-      }
+      const float scale = block_scale(amax);
+      const uint2 o = block_codes(f, scale);
       typedef int i32x2 __attribute__((ext_vector_type(2)));
-      __builtin_nontemporal_store(i32x2{(int)o[0], (int)o[1]}, reinterpret_cast<i32x2*>(a.codes + at[p]));
+      __builtin_nontemporal_store(i32x2{(int)o.x, (int)o.y}, reinterpret_cast<i32x2*>(a.codes + at[p]));
       const int64_t c = c0 + p * all;
       if ((c & 15) == 0) a.scales[c >> 4] = scale;
     }

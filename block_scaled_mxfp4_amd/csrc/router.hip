@@ -1,0 +1,583 @@
+// The gate: expert ids and weights of each token, the balance loss, and the
+// logits' gradient (situ_moe_router, situ_moe_router_backward).
+//
+// A wave takes a token at a time and holds its logits in registers, V J of them
+// a lane: expert e = 64 V j + V lane + v.
+//
+// Choice without sorting.  Logits map to ascending unsigned keys; at least top_k
+// of the 64 lanes' largest keys reach a threshold, so the top_k largest keys of
+// all do, and a bisection on the lanes' largest finds one that few more do.  What
+// reaches it (some 1.3 top_k) is packed into LDS, one candidate a lane, and a
+// candidate's place is the number of candidates before it.  Where more than 64
+// reach it (many equals; top_k near 64), the wave takes its largest remaining
+// key top_k times instead.
+//
+// A selection by sigmoid + bias is compared in 64 bits, since the neighbours of
+// 900 experts lie as near as fp32 rounds.  Only the candidates are: the threshold
+// is taken on fp32 keys and lowered by more than twice their error.
+//
+// Sigmoid scores are held divided by e^min(zmax, 0), which leaves their shares as
+// they are: a row whose scores all underflow keeps its weights.
+//
+// Balance loss: a wave sums its tokens' shares in registers, the workgroup's
+// waves add up in LDS in turn, and each workgroup writes partial sums and counts;
+// a second launch adds them in a fixed order, and its last workgroup (by a
+// ticket) takes the loss.  One workgroup finishes by itself.
+#include <algorithm>
+
+#include "common.hpp"
+#include "routed.hpp"
+#include "wave.hpp"
+
+namespace situ {
+
+namespace {
+
+constexpr float kL2e = 1.44269502162933349609375f;   // log2(e) rounded to fp32
+constexpr int kRouterWaves = 8;                       // of a workgroup
+constexpr int kRouterBlocks = 1024;                   // workgroups at most
+constexpr int kOneBlockTokens = 32;                   // up to here one workgroup finishes the loss by itself
+
+// Keys ascend with the values; 0 is an expert that cannot be chosen (-inf, NaN).
+__device__ __forceinline__ uint32_t key_of(float z) {
+  const uint32_t u = __float_as_uint(z + 0.0f);       // -0 as +0
+  const uint32_t k = u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+  return z > -__builtin_inff() ? k : 0u;
+}
+__device__ __forceinline__ float value_of(uint32_t k) {
+  return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+}
+__device__ __forceinline__ uint64_t key_of(double x) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x + 0.0);
+  return u ^ ((uint64_t)((int64_t)u >> 63) | 0x8000000000000000ull);
+}
+
+// LDS that other lanes of the wave read or wrote: in order, once the compiler keeps it so.
+__device__ __forceinline__ void wave_lds() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+__device__ __forceinline__ float e_to(float x) { return __builtin_amdgcn_exp2f(x * kL2e); }
+
+// The logits of a row, NaN-free where there is none to load (-inf).
+template <bool BF, int V, int J>
+__device__ __forceinline__ void load_row(const void* logits, int64_t at, int lane, int experts, bool vec, float z[V * J]) {
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    const int e = 64 * V * j + V * lane;
+    if constexpr (V == 4) {
+      if (vec && e + 4 <= experts) {
+        if constexpr (BF) {
+          const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(logits) + at + e);
+          z[4 * j] = bf16_to_f32(w.x & 0xffffu); z[4 * j + 1] = bf16_to_f32(w.x >> 16);
+          z[4 * j + 2] = bf16_to_f32(w.y & 0xffffu); z[4 * j + 3] = bf16_to_f32(w.y >> 16);
+        } else {
+          const f32x4 w = *reinterpret_cast<const f32x4*>(static_cast<const float*>(logits) + at + e);
+#pragma unroll
+          for (int v = 0; v < 4; ++v) z[4 * j + v] = w[v];
+        }
+        continue;
+      }
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      z[V * j + v] = -__builtin_inff();
+      if (e + v < experts)
+        z[V * j + v] = BF ? bf16_to_f32(static_cast<const uint16_t*>(logits)[at + e + v])
+                          : static_cast<const float*>(logits)[at + e + v];
+    }
+  }
+}
+
+// Scores of a row, up to a factor the whole row shares: e^(z - zmax), or
+// sigmoid(z) e^-min(zmax, 0).
+__device__ __forceinline__ float score(bool sigmoid, float z, float shift) {
+  // the difference first: a row of the type's lowest value has a finite one
+  if (!sigmoid) return e_to(z - shift);
+  return e_to(fminf(z, 0.0f) - shift) * __builtin_amdgcn_rcpf(1.0f + e_to(-fabsf(z)));
+}
+
+struct RouterArgs {
+  situ_moe_router_t p;
+  int32_t vec;
+  float* part_sum;            // [gridDim.x][experts], or null: no balance loss
+  int32_t* part_count;
+  uint32_t* ticket;
+};
+
+// Candidates of a wave, or a row by expert.
+struct Candidates {
+  uint64_t key[64];
+  float z[64];
+  int32_t id[64];
+};
+
+template <bool BF, int V, int J, bool SIG, bool BIAS, bool BAL>
+__global__ __launch_bounds__(64 * kRouterWaves) void router_kernel(RouterArgs a) {
+  constexpr int N = V * J;
+  __shared__ Candidates cands[kRouterWaves];
+  __shared__ float sums[BAL ? 64 * N : 1];
+  __shared__ int32_t hits[BAL ? 64 * N : 1];
+  const situ_moe_router_t& p = a.p;
+  const int lane = lane_id(), wave = threadIdx.x / kWave;
+  const int experts = p.experts, top_k = p.top_k;
+  Candidates& cd = cands[wave];
+  float acc[BAL ? N : 1];
+  if constexpr (BAL) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) acc[i] = 0.0f;
+    for (int i = threadIdx.x; i < 64 * N; i += 64 * kRouterWaves) { sums[i] = 0.0f; hits[i] = 0; }
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0;     // for the launch that follows
+    __syncthreads();
+  }
+  float bias[BIAS ? N : 1];
+  if constexpr (BIAS) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int e = 64 * V * (i / V) + V * lane + i % V;
+      bias[i] = e < experts ? p.bias[e] : 0.0f;
+    }
+  }
+  const int64_t step = (int64_t)gridDim.x * kRouterWaves;
+  for (int64_t t = (int64_t)blockIdx.x * kRouterWaves + wave; t < p.tokens; t += step) {
+    const int64_t row = t * top_k;
+    uint32_t best = 0, k32[N];
+    float z[N];
+    if (!p.mask || p.mask[t]) {
+      load_row<BF, V, J>(p.logits, t * p.logits_stride, lane, experts, a.vec, z);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        k32[i] = key_of(z[i]);
+        best = max(best, k32[i]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) { z[i] = -__builtin_inff(); k32[i] = 0; }
+    }
+    const uint32_t top = wave_max(best);
+    const float zmax = value_of(top);
+    const bool live = top != 0;                      // the row has an expert to choose
+    if constexpr (BIAS) {
+      best = 0;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const float o = __builtin_amdgcn_rcpf(1.0f + e_to(-z[i]));
+        k32[i] = k32[i] ? key_of(o + bias[i]) : 0u;
+        best = max(best, k32[i]);
+      }
+    }
+    // a threshold that top_k of the lanes' largest keys reach, or 1: every expert that can be chosen
+    uint32_t lo = 1, hi = (BIAS ? wave_max(best) : top);
+    while (live && hi > lo + 1) {
+      const uint32_t mid = lo + (hi - lo) / 2;
+      const int n = __popcll(__ballot(best >= mid));
+      if (n >= top_k) {
+        lo = mid;
+        if (n <= top_k + 8) break;
+      } else {
+        hi = mid;
+      }
+    }
+    if constexpr (BIAS) {
+      // the k-th largest fp32 key is lo at least; an fp32 key is off by less than 2^-21 + 2^-23 |key|
+      const float f = value_of(lo);
+      if (lo > 1 && f < __builtin_inff()) lo = max(key_of(f - 0x1p-19f * (1.0f + fabsf(f))), 1u);
+    }
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const uint64_t in = __ballot(k32[i] >= lo);
+      if (in) {
+        const int at = n + (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(in >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)in, 0));
+        if (k32[i] >= lo && at < 64) {
+          const int e = 64 * V * (i / V) + V * lane + i % V;
+          cd.z[at] = z[i];
+          cd.id[at] = e;
+          if constexpr (BIAS)
+            cd.key[at] = __builtin_bit_cast(uint64_t, (double)bias[i]);
+          else
+            cd.key[at] = ((uint64_t)k32[i] << 32) | (uint32_t)(~e);
+        }
+        n += __popcll(in);
+      }
+    }
+    wave_lds();
+    int id = -1, place = lane;                       // a lane's expert and its place in the row
+    float zc = 0.0f;
+    if (n <= 64) {
+      uint64_t key = 0;
+      if (lane < n) {
+        id = cd.id[lane];
+        zc = cd.z[lane];
+        key = cd.key[lane];
+        if constexpr (BIAS) key = key_of(1.0 / (1.0 + exp(-(double)zc)) + __builtin_bit_cast(double, key));
+      }
+      int before = 0;
+      for (int c = 0; c < n; ++c) {
+        const uint64_t other = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(key >> 32), c) << 32 |
+                               (uint32_t)__builtin_amdgcn_readlane((int)key, c);
+        if constexpr (BIAS) {
+          const int oid = __builtin_amdgcn_readlane(id, c);
+          before += other > key || (other == key && oid < id);
+        } else {
+          before += other > key;
+        }
+      }
+      if (lane < n) place = before;
+    } else {
+      // the largest left, top_k times
+      uint64_t k64[N];
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        if constexpr (BIAS)
+          k64[i] = k32[i] ? key_of(1.0 / (1.0 + exp(-(double)z[i])) + (double)bias[i]) : 0;
+        else
+          k64[i] = k32[i];
+      }
+      for (int c = 0; c < top_k; ++c) {
+        uint64_t mine = 0;
+        int which = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i)                  // ascending ids: the first of equals stays
+          if (k64[i] > mine) { mine = k64[i]; which = i; }
+        const uint32_t h = wave_max((uint32_t)(mine >> 32));
+        const uint32_t l = wave_max((uint32_t)(mine >> 32) == h ? (uint32_t)mine : 0u);
+        const uint64_t largest = (uint64_t)h << 32 | l;
+        if (!largest) break;
+        const int e = 64 * V * (which / V) + V * lane + which % V;
+        const uint32_t first = ~wave_max(mine == largest ? ~(uint32_t)e : 0u);
+        if (mine == largest && e == (int)first) {
+#pragma unroll
+          for (int i = 0; i < N; ++i)
+            if (i == which) { k64[i] = 0; cd.z[c] = z[i]; }
+        }
+        wave_lds();
+        if (lane == c) { id = (int)first; zc = cd.z[c]; }
+      }
+    }
+    const bool chosen = id >= 0 && place < top_k;
+    // renormalized weights are shares of the chosen: their own largest is the one to be near
+    float wshift = SIG ? 0.0f : zmax;
+    if (SIG && p.renormalize) wshift = fminf(BIAS ? value_of(wave_max(chosen ? key_of(zc) : 0u)) : zmax, 0.0f);
+    float w = chosen ? score(SIG, zc, wshift) : 0.0f;
+    float all = 0.0f;
+    if (BAL || (!SIG && !p.renormalize)) {
+      float s[N];
+      if (live) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          s[i] = score(SIG, z[i], SIG ? fminf(zmax, 0.0f) : zmax);
+          all += s[i];
+        }
+        all = wave_sum(all);
+        if constexpr (BAL) {
+          const float r = 1.0f / all;
+#pragma unroll
+          for (int i = 0; i < N; ++i) acc[i] = fmaf(s[i], r, acc[i]);
+          if (chosen) atomicAdd(&hits[id], 1);
+        }
+      }
+    }
+    const float total = p.renormalize ? wave_sum(w) : (SIG ? 1.0f : all);
+    w = chosen ? p.scale * (w / total) : 0.0f;
+    if (chosen || (lane >= n && lane < top_k && n <= 64) || (n > 64 && lane < top_k)) {
+      const int64_t at = row + place;
+      if (p.ids) p.ids[at] = id;
+      const uint32_t b = f32_to_bf16_rne(w);
+      if (p.weights) {
+        if (p.weights_dtype == SITU_OUT_F32)
+          static_cast<float*>(p.weights)[at] = w;
+        else
+          static_cast<uint16_t*>(p.weights)[at] = (uint16_t)b;
+      }
+      if (p.packed) p.packed[at] = (int32_t)(b << 16 | ((uint32_t)id & 0xffffu));
+    }
+    wave_lds();
+  }
+  if constexpr (BAL) {
+    for (int w = 0; w < kRouterWaves; ++w) {         // in turn: a fixed order
+      __syncthreads();
+      if (wave == w) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) sums[64 * V * (i / V) + V * lane + i % V] += acc[i];
+      }
+    }
+    __syncthreads();
+    const bool alone = gridDim.x == 1;
+    float* so = alone ? p.prob_sum : a.part_sum + (int64_t)blockIdx.x * experts;
+    int32_t* co = alone ? p.counts : a.part_count + (int64_t)blockIdx.x * experts;
+    for (int e = threadIdx.x; e < experts; e += 64 * kRouterWaves) { so[e] = sums[e]; co[e] = hits[e]; }
+    if (alone && wave == 0) {
+      float c = 0.0f, d = 0.0f;
+      for (int e = lane; e < experts; e += 64) {
+        c += (float)hits[e];
+        d += (float)hits[e] * sums[e];
+      }
+      c = wave_sum(c);
+      d = wave_sum(d);
+      if (lane == 0) *p.loss = c > 0.0f ? (float)experts * (float)top_k * (d / c) / c : 0.0f;
+    }
+  }
+}
+
+// Sums of the workgroups' parts, 64 experts a workgroup; the last one to finish
+// takes the loss.  Its reads of the others' results go past the caches of its
+// die, as their writes do.
+constexpr int kFinishWaves = 16;
+__global__ __launch_bounds__(64 * kFinishWaves) void router_finish_kernel(RouterArgs a, int parts) {
+  __shared__ float s_sum[kFinishWaves][64];
+  __shared__ int32_t s_count[kFinishWaves][64];
+  __shared__ float s_c[kFinishWaves], s_d[kFinishWaves];
+  __shared__ uint32_t place;
+  const situ_moe_router_t& p = a.p;
+  const int lane = lane_id(), wave = threadIdx.x / kWave, e = blockIdx.x * 64 + lane;
+  float sum = 0.0f;
+  int32_t count = 0;
+  if (e < p.experts) {
+#pragma unroll 8
+    for (int i = wave; i < parts; i += kFinishWaves) {
+      sum += a.part_sum[(int64_t)i * p.experts + e];
+      count += a.part_count[(int64_t)i * p.experts + e];
+    }
+  }
+  s_sum[wave][lane] = sum;
+  s_count[wave][lane] = count;
+  __syncthreads();
+  if (wave == 0) {
+    for (int w = 1; w < kFinishWaves; ++w) { sum += s_sum[w][lane]; count += s_count[w][lane]; }
+    if (e < p.experts) {
+      __hip_atomic_store(&p.prob_sum[e], sum, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      __hip_atomic_store(&p.counts[e], count, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    __threadfence();
+    if (lane == 0) place = __hip_atomic_fetch_add(a.ticket, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  __syncthreads();
+  if (place + 1 != gridDim.x) return;
+  __threadfence();
+  float c = 0.0f, d = 0.0f;
+  for (int i = threadIdx.x; i < p.experts; i += 64 * kFinishWaves) {
+    const float n = (float)__hip_atomic_load(&p.counts[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    c += n;
+    d += n * __hip_atomic_load(&p.prob_sum[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  s_c[wave] = wave_sum(c);
+  s_d[wave] = wave_sum(d);
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    c = d = 0.0f;
+    for (int w = 0; w < kFinishWaves; ++w) { c += s_c[w]; d += s_d[w]; }
+    *p.loss = c > 0.0f ? (float)p.experts * (float)p.top_k * (d / c) / c : 0.0f;
+  }
+}
+
+// The gradient.  With a the scores up to the row's factor, P = a / sum a, q =
+// a / (sum of the chosen):
+//   renormalized  x_i = scale q_i (dw_i - sum q dw)     else  x_i = score_i scale dw_i
+//   dz_e = P_e (g_e - sum P g) + x_e     (softmax, not renormalized: - P_e sum x)
+// and for sigmoid the whole times 1 - sigmoid(z_e).  A row of floats by expert
+// in LDS takes the x to the lanes that hold their experts.
+template <bool BF, bool BFO, int V, int J, bool SIG>
+__global__ __launch_bounds__(64 * kRouterWaves) void router_backward_kernel(situ_moe_router_backward_t p, int vec, int vec_out) {
+  constexpr int N = V * J;
+  __shared__ float rows[kRouterWaves][64 * N];
+  const int lane = lane_id(), wave = threadIdx.x / kWave;
+  float* x = rows[wave];
+  float g[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) { g[i] = 0.0f; x[64 * i + lane] = 0.0f; }
+  const bool loss = p.counts != nullptr;
+  if (loss) {
+    float c = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int e = 64 * V * (i / V) + V * lane + i % V;
+      if (e < p.experts) { g[i] = (float)p.counts[e]; c += g[i]; }
+    }
+    c = wave_sum(c);
+    const float f = c > 0.0f ? *p.d_loss * ((float)p.experts * (float)p.top_k) / c / c : 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) g[i] *= f;
+  }
+  const int64_t step = (int64_t)gridDim.x * kRouterWaves;
+  for (int64_t t = (int64_t)blockIdx.x * kRouterWaves + wave; t < p.tokens; t += step) {
+    const int64_t in = t * p.logits_stride, out = t * p.out_stride;
+    float z[N], d[N];
+    uint32_t best = 0;
+    if (!p.mask || p.mask[t]) {
+      load_row<BF, V, J>(p.logits, in, lane, p.experts, vec, z);
+#pragma unroll
+      for (int i = 0; i < N; ++i) best = max(best, key_of(z[i]));
+    }
+    const uint32_t top = wave_max(best);
+#pragma unroll
+    for (int i = 0; i < N; ++i) d[i] = 0.0f;
+    if (top) {
+      const float shift = SIG ? fminf(value_of(top), 0.0f) : value_of(top);
+      int id = -1;
+      float dw = 0.0f, zc = 0.0f;
+      if (p.d_weights && lane < p.top_k) {
+        id = p.ids[t * p.top_k + lane];
+        if (id >= p.experts) id = -1;
+        if (id >= 0) {
+          dw = p.d_weights[t * p.top_k + lane] * p.scale;
+          zc = BF ? bf16_to_f32(static_cast<const uint16_t*>(p.logits)[in + id])
+                  : static_cast<const float*>(p.logits)[in + id];
+        }
+      }
+      float all = 0.0f, pg = 0.0f;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        d[i] = score(SIG, z[i], shift);
+        all += d[i];
+        pg = fmaf(d[i], g[i], pg);
+      }
+      const float r = 1.0f / wave_sum(all);
+      pg = loss ? wave_sum(pg) * r : 0.0f;
+      if (p.d_weights) {
+        float xc;
+        if (p.renormalize) {
+          const uint32_t topc = wave_max(id >= 0 ? key_of(zc) : 0u);     // of the chosen: they need not be the largest
+          const float sc = id >= 0 && topc ? score(SIG, zc, SIG ? fminf(value_of(topc), 0.0f) : value_of(topc)) : 0.0f;
+          const float total = wave_sum(sc);
+          const float q = topc ? sc / total : 0.0f;
+          xc = q * (dw - wave_sum(q * dw));
+        } else {
+          xc = id >= 0 ? (SIG ? score(true, zc, 0.0f) : score(false, zc, shift) * r) * dw : 0.0f;
+          if constexpr (!SIG) pg += wave_sum(xc);
+        }
+        if (id >= 0) atomicAdd(&x[id], xc);
+        wave_lds();
+      }
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int e = 64 * V * (i / V) + V * lane + i % V;
+        d[i] = fmaf(d[i] * r, g[i] - pg, x[e]);
+        if constexpr (SIG) {
+          const float t1 = e_to(-fabsf(z[i])), o = __builtin_amdgcn_rcpf(1.0f + t1);
+          d[i] *= z[i] >= 0.0f ? t1 * o : o;
+        }
+      }
+      wave_lds();
+      if (id >= 0) x[id] = 0.0f;
+      wave_lds();
+    }
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const int e = 64 * V * j + V * lane;
+      if constexpr (V == 4) {
+        if (vec_out && e + 4 <= p.experts) {
+          if constexpr (BFO) {
+            const bf16x2 lo = {(__bf16)d[4 * j], (__bf16)d[4 * j + 1]}, hi = {(__bf16)d[4 * j + 2], (__bf16)d[4 * j + 3]};
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.d_logits) + out + e) =
+                make_uint2(__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi));
+          } else {
+            *reinterpret_cast<f32x4*>(static_cast<float*>(p.d_logits) + out + e) =
+                f32x4{d[4 * j], d[4 * j + 1], d[4 * j + 2], d[4 * j + 3]};
+          }
+          continue;
+        }
+      }
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        if (e + v < p.experts) {
+          if constexpr (BFO)
+            static_cast<uint16_t*>(p.d_logits)[out + e + v] = (uint16_t)f32_to_bf16_rne(d[V * j + v]);
+          else
+            static_cast<float*>(p.d_logits)[out + e + v] = d[V * j + v];
+        }
+      }
+    }
+  }
+}
+
+template <bool BF, int V, int J, bool SIG, bool BIAS>
+void router_go(const RouterArgs& a, int blocks, hipStream_t s) {
+  if (a.part_sum)
+    hipLaunchKernelGGL((router_kernel<BF, V, J, SIG, BIAS, true>), dim3(blocks), dim3(64 * kRouterWaves), 0, s, a);
+  else
+    hipLaunchKernelGGL((router_kernel<BF, V, J, SIG, BIAS, false>), dim3(blocks), dim3(64 * kRouterWaves), 0, s, a);
+}
+template <bool BF, int V, int J>
+void router_scored(const RouterArgs& a, int blocks, hipStream_t s) {
+  if (a.p.scoring == SITU_SCORE_SOFTMAX) router_go<BF, V, J, false, false>(a, blocks, s);
+  else if (!a.p.bias) router_go<BF, V, J, true, false>(a, blocks, s);
+  else router_go<BF, V, J, true, true>(a, blocks, s);
+}
+template <bool BF>
+void router_sized(const RouterArgs& a, int blocks, hipStream_t s) {
+  const int e = a.p.experts;
+  if (e <= 64) router_scored<BF, 1, 1>(a, blocks, s);
+  else if (e <= 128) router_scored<BF, 2, 1>(a, blocks, s);
+  else if (e <= 256) router_scored<BF, 4, 1>(a, blocks, s);
+  else if (e <= 512) router_scored<BF, 4, 2>(a, blocks, s);
+  else router_scored<BF, 4, 4>(a, blocks, s);
+}
+
+template <bool BF, bool BFO, int V, int J>
+void backward_scored(const situ_moe_router_backward_t& p, int vec, int vec_out, int blocks, hipStream_t s) {
+  if (p.scoring == SITU_SCORE_SOFTMAX)
+    hipLaunchKernelGGL((router_backward_kernel<BF, BFO, V, J, false>), dim3(blocks), dim3(64 * kRouterWaves), 0, s, p, vec, vec_out);
+  else
+    hipLaunchKernelGGL((router_backward_kernel<BF, BFO, V, J, true>), dim3(blocks), dim3(64 * kRouterWaves), 0, s, p, vec, vec_out);
+}
+template <bool BF, bool BFO>
+void backward_sized(const situ_moe_router_backward_t& p, int vec, int vec_out, int blocks, hipStream_t s) {
+  const int e = p.experts;
+  if (e <= 64) backward_scored<BF, BFO, 1, 1>(p, vec, vec_out, blocks, s);
+  else if (e <= 128) backward_scored<BF, BFO, 2, 1>(p, vec, vec_out, blocks, s);
+  else if (e <= 256) backward_scored<BF, BFO, 4, 1>(p, vec, vec_out, blocks, s);
+  else if (e <= 512) backward_scored<BF, BFO, 4, 2>(p, vec, vec_out, blocks, s);
+  else backward_scored<BF, BFO, 4, 4>(p, vec, vec_out, blocks, s);
+}
+
+// Rows of four experts start on 16 bytes (8 in bf16).
+int four_at_once(const void* p, int64_t stride, bool bf) {
+  return reinterpret_cast<uintptr_t>(p) % (bf ? 8 : 16) == 0 && stride % 4 == 0;
+}
+
+}  // namespace
+
+int router_blocks(int32_t tokens) {
+  return tokens <= kOneBlockTokens ? 1 : std::min(kRouterBlocks, (tokens + kRouterWaves - 1) / kRouterWaves);
+}
+
+hipError_t launch_router(const situ_moe_router_t& p, hipStream_t s) {
+  RouterArgs a{};
+  a.p = p;
+  const bool bf = p.logits_dtype == SITU_OUT_BF16;
+  a.vec = four_at_once(p.logits, p.logits_stride, bf);
+  const bool balance = p.counts != nullptr;
+  // without the loss nothing is shared: as many workgroups as there are tokens for
+  const int blocks = balance ? router_blocks(p.tokens)
+                             : (int)std::min<int64_t>(((int64_t)p.tokens + kRouterWaves - 1) / kRouterWaves, 4 * kRouterBlocks);
+  if (balance) {
+    const int64_t part = (int64_t)router_blocks(p.tokens) * p.experts;
+    a.part_sum = static_cast<float*>(p.workspace);
+    a.part_count = reinterpret_cast<int32_t*>(a.part_sum + part);
+    a.ticket = reinterpret_cast<uint32_t*>(a.part_count + part);
+  }
+  if (bf) router_sized<true>(a, blocks, s);
+  else router_sized<false>(a, blocks, s);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || !balance || blocks == 1) return e;
+  hipLaunchKernelGGL(router_finish_kernel, dim3((p.experts + 63) / 64), dim3(64 * kFinishWaves), 0, s, a, blocks);
+  return hipGetLastError();
+}
+
+hipError_t launch_router_backward(const situ_moe_router_backward_t& p, hipStream_t s) {
+  const bool bf = p.logits_dtype == SITU_OUT_BF16, bfo = p.out_dtype == SITU_OUT_BF16;
+  const int vec = four_at_once(p.logits, p.logits_stride, bf), vec_out = four_at_once(p.d_logits, p.out_stride, bfo);
+  const int blocks = (int)std::min<int64_t>(((int64_t)p.tokens + kRouterWaves - 1) / kRouterWaves, kRouterBlocks);
+  if (bf) {
+    if (bfo) backward_sized<true, true>(p, vec, vec_out, blocks, s);
+    else backward_sized<true, false>(p, vec, vec_out, blocks, s);
+  } else {
+    if (bfo) backward_sized<false, true>(p, vec, vec_out, blocks, s);
+    else backward_sized<false, false>(p, vec, vec_out, blocks, s);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace situ

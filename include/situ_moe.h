@@ -358,6 +358,190 @@ situ_status situ_moe_grouped_matmul_wgrad(const situ_moe_grouped_t* args, void* 
 const char* situ_moe_matmul_fp8_block128_kernel(const situ_moe_fp8_matmul_t* args, int32_t cus);
 const char* situ_moe_grouped_matmul_kernel(int32_t direction, const situ_moe_grouped_t* args, int32_t cus);
 
+/* The steps around the routed products, with their gradients, so that a whole
+ * routed layer runs and trains on this library: the gate, the gated activation
+ * between the two expert products, the combine; and low-rank adapters of many
+ * requests beside a shared projection.  None of them uses atomics whose order
+ * changes a result: a repeated call gives the same bits. */
+
+/* The gate: expert ids and weights of each token from its logits z.
+ *   score   softmax(z) over the experts, or sigmoid(z)
+ *   chosen  the top_k largest z; with a bias (SITU_SCORE_SIGMOID only) the top_k
+ *           largest sigmoid(z) + bias, compared in 64 bits.  Equals: the lowest
+ *           id.  In descending order.  An expert whose z (or bias) is -inf or
+ *           NaN is never chosen: where fewer than top_k are left, the rest of
+ *           the row has id -1 and weight 0
+ *   weight  scale * score, with `renormalize` scale * score / (sum of the
+ *           chosen scores), which stays right where every score underflows
+ * The bias takes part in the choice alone.  A token whose mask is 0 is not
+ * routed: ids -1, weights 0, no part in the sums (its logits may be anything).
+ * The balance loss over the batch, if counts, prob_sum and loss are given:
+ *   counts[e]    tokens whose ids hold e
+ *   prob_sum[e]  sum over tokens of P[t, e], the softmax score or the sigmoid
+ *                score divided by its row's sum
+ *   loss         experts * top_k / C^2 * sum_e counts[e] prob_sum[e], C the sum
+ *                of the counts (top_k times the tokens, where none lacks
+ *                experts); 0 if C is 0
+ * Where the batch lies on several ranks, the counts and prob_sums are summed
+ * over them and the loss follows from the sums.
+ * A NaN logit makes its row's softmax, and so the loss, NaN; so does +inf.
+ * ids, packed and weights feed topk_ids, topk_packed and topk_weights of the
+ * layer (an id of -1 is outside every shard; packed, 0xFFFF is).
+ * Sizes: tokens 0 .. 2^24, experts 1 .. 1024, top_k 1 .. min(experts, 64). */
+enum { SITU_SCORE_SOFTMAX = 0, SITU_SCORE_SIGMOID = 1 };
+typedef struct situ_moe_router_t {
+  int32_t tokens, experts, top_k;
+  int32_t scoring;            /* SITU_SCORE_* */
+  int32_t logits_dtype;       /* SITU_OUT_F32 or SITU_OUT_BF16 */
+  int32_t weights_dtype;      /* SITU_OUT_F32 or SITU_OUT_BF16 */
+  int32_t renormalize;        /* 0 or 1 */
+  float scale;
+  int64_t logits_stride;      /* elements between rows */
+  const void* logits;         /* (device) [tokens, experts] (rows that start on 16 bytes, 8 for bf16, are read fastest) */
+  const float* bias;          /* (device) [experts] or NULL */
+  const uint8_t* mask;        /* (device) [tokens] or NULL: every token is routed */
+  int32_t* ids;               /* (device) [tokens, top_k] */
+  void* weights;              /* (device) [tokens, top_k], or NULL */
+  int32_t* packed;            /* (device) [tokens, top_k], or NULL: bf16 weight << 16 | id & 0xFFFF */
+  int32_t* counts;            /* (device) [experts]; counts, prob_sum and loss are all given or all NULL */
+  float* prob_sum;            /* (device) [experts] */
+  float* loss;                /* (device) [1] */
+  void* workspace;            /* (device) 16-byte aligned; calls sharing it must not overlap in time */
+  uint64_t workspace_bytes;
+} situ_moe_router_t;
+/* Bytes of workspace a router call with the balance loss needs (0 without it;
+ * the sizes alone are read); SITU_E_NULL_ARG, SITU_E_BAD_SHAPE or
+ * SITU_E_UNSUPPORTED as the call itself. */
+situ_status situ_moe_router_workspace(const situ_moe_router_t* args, uint64_t* bytes);
+situ_status situ_moe_router(const situ_moe_router_t* args, void* hip_stream);
+
+/* The logits' gradient of a router call,
+ *   d_logits = d_weights through the weights + d_loss[0] through the loss,
+ * from the ids that were chosen (-1, and ids outside the experts, take no part;
+ * an id that a row holds twice counts twice).  counts are those of the loss (of
+ * all ranks, if it was taken over them) and are constants of it, as the choice
+ * is.  d_weights or counts and d_loss may be NULL: that part is 0.  Rows of
+ * masked tokens, and of tokens without a logit above -inf, are 0. */
+typedef struct situ_moe_router_backward_t {
+  int32_t tokens, experts, top_k;
+  int32_t scoring, logits_dtype;
+  int32_t out_dtype;          /* SITU_OUT_F32 or SITU_OUT_BF16 */
+  int32_t renormalize;
+  float scale;
+  int64_t logits_stride, out_stride;
+  const void* logits;         /* (device) [tokens, experts] */
+  const uint8_t* mask;        /* (device) [tokens] or NULL */
+  const int32_t* ids;         /* (device) [tokens, top_k]; may be NULL with d_weights */
+  const float* d_weights;     /* (device) [tokens, top_k] or NULL */
+  const int32_t* counts;      /* (device) [experts] or NULL */
+  const float* d_loss;        /* (device) [1] or NULL */
+  void* d_logits;             /* (device) [tokens, experts] */
+} situ_moe_router_backward_t;
+situ_status situ_moe_router_backward(const situ_moe_router_backward_t* args, void* hip_stream);
+
+/* The gated activation between the expert products, h = act(g, u) of the
+ * gate columns [0, I) and up columns [I, 2I) of gate_up, the rows grouped by
+ * expert as in situ_moe_grouped_matmul; and its gradient.  With codes and scales
+ * the call also keeps g and u in 8 bits for the way back, in half the bytes:
+ * E4M3 with one fp32 scale per row and 128 columns of each half, by the rule of
+ * situ_moe_quantize_fp8_block128 (its very codes, where I is a multiple of 128).
+ *   situ_moe_activation           h, and codes and scales if given
+ *   situ_moe_activation_backward  d_gate_up = (dh d act/d g, dh d act/d u) at the g
+ *                                 and u of gate_up, or of codes and scales if
+ *                                 gate_up is NULL; and, if given, h at them (the
+ *                                 input of the down product, for its wgrad)
+ * beta, alpha and their like are the model's constants: they get no gradient.
+ * The formulas are fp32; h and d_gate_up are rounded once, to bf16.  Rows
+ * outside every group are not written.  I a multiple of 8, up to 2^17;
+ * rows 0 .. 2^24; experts 1 .. 1024.  gate_up, h, dh and d_gate_up 16-byte
+ * aligned with strides of a multiple of 8; codes 8-byte aligned and dense.
+ * d_gate_up may be gate_up itself (the same address and stride), and h may be dh
+ * likewise; otherwise outputs must not overlap inputs. */
+typedef struct situ_moe_activation_t {
+  int32_t rows;
+  int32_t inner;              /* I */
+  int32_t experts;
+  int32_t activation;         /* SITU_ACTIVATION_* */
+  int64_t gate_up_stride, h_stride, dh_stride, d_gate_up_stride;   /* elements between rows */
+  const int32_t* offsets;     /* (device) [experts + 1], as in situ_moe_grouped_t; NULL (experts 1): one group */
+  const float* p0;            /* (device) [experts] SiTU: beta; SwigluBias: alpha; else ignored */
+  const float* p1;            /* (device) [experts] SiTU: linear beta; SwigluBias: beta; else ignored */
+  const uint16_t* gate_up;    /* (device) bf16 [rows, 2I] */
+  uint16_t* h;                /* (device) bf16 [rows, I]; the backward: NULL if not wanted */
+  uint8_t* codes;             /* (device) [rows, 2I], or NULL */
+  float* scales;              /* (device) [rows, 2 ceil(I / 128)]: those of g, then those of u; or NULL */
+  const uint16_t* dh;         /* (device) bf16 [rows, I], the backward only */
+  uint16_t* d_gate_up;        /* (device) bf16 [rows, 2I], the backward only */
+} situ_moe_activation_t;
+situ_status situ_moe_activation(const situ_moe_activation_t* args, void* hip_stream);
+situ_status situ_moe_activation_backward(const situ_moe_activation_t* args, void* hip_stream);
+
+/* The weighted sum of each token's expert rows, and its gradients:
+ *   situ_moe_combine           out[t] = sum_s weights[t, s] y[inv[t, s]], in slot order in
+ *                              fp32; a token without a local pair gets zeros
+ *   situ_moe_combine_backward  dy[inv[t, s]] = weights[t, s] d_out[t]  (in y's type) and
+ *                              d_weights[t, s] = d_out[t] . y[inv[t, s]]  (fp32 sums; 0
+ *                              for a pair that is not local)
+ * inv[t * top_k + s] is the row of pair (t, s), as situ_moe_route leaves it in
+ * the workspace; a value outside [0, rows) is a pair that is not local.  For the
+ * gradient each row belongs to one pair at most; rows of no pair are not written.
+ * hidden a multiple of 8 up to 2^18, rows and tokens 0 .. 2^24, top_k 1 .. 1024.
+ * Arrays 16-byte aligned, strides a multiple of 8 elements.  dy may be y
+ * itself; otherwise outputs must not overlap inputs. */
+typedef struct situ_moe_combine_t {
+  int32_t tokens, top_k, hidden;
+  int32_t rows;               /* rows of y */
+  int32_t y_dtype, weights_dtype;   /* SITU_OUT_F32 or SITU_OUT_BF16 */
+  int32_t out_dtype;          /* of out, and of d_out */
+  int32_t reserved;           /* 0 */
+  int64_t y_stride, out_stride, dy_stride;   /* elements between rows */
+  const void* y;              /* (device) [rows, hidden] */
+  const void* weights;        /* (device) [tokens, top_k] */
+  const int32_t* inv;         /* (device) [tokens, top_k] */
+  void* out;                  /* (device) [tokens, hidden]; the backward reads it as d_out */
+  void* dy;                   /* (device) [rows, hidden], the backward only, or NULL */
+  float* d_weights;           /* (device) [tokens, top_k], the backward only, or NULL */
+} situ_moe_combine_t;
+situ_status situ_moe_combine(const situ_moe_combine_t* args, void* hip_stream);
+situ_status situ_moe_combine_backward(const situ_moe_combine_t* args, void* hip_stream);
+
+/* Low-rank adapters of many requests beside a shared projection (whose output
+ * is base): for the rows r of request q, offsets[q] .. offsets[q + 1] - 1, and
+ * their adapter i = adapter[q],
+ *   out[r] = base[r] + scales[i] * b[i] (a[i] x[r])
+ * A request whose adapter is outside [0, adapters) has none: out[r] = base[r].
+ * base NULL stands for zeros.  out may be base itself (the same address and
+ * stride).  Rows of no request are not written.  ranks[i] is the number of
+ * leading rows of a[i] (and columns of b[i]) that count, NULL: all; scales
+ * NULL: 1.  Sums, and a[i] x[r] between the two products, are held to fp32
+ * accuracy (the second product takes it as two bf16 terms, 2^-16 of it); one
+ * rounding at the end for bf16.  k, n and rank multiples of 8, k and n up to 2^18,
+ * rank up to 256, rows 0 .. 2^24, requests and adapters 1 .. 2^20.  x, a, b, base and out
+ * 16-byte aligned, strides a multiple of 8 elements. */
+typedef struct situ_moe_adapters_t {
+  int32_t rows, n, k;
+  int32_t rank;               /* of a and b */
+  int32_t requests, adapters;
+  int32_t out_dtype;          /* of base and out */
+  int32_t reserved;           /* 0 */
+  int64_t x_stride, base_stride, out_stride;   /* elements between rows */
+  const int32_t* offsets;     /* (device) [requests + 1], ascending within [0, rows].  Other values give unspecified
+                                 outputs, but no access outside the arrays */
+  const int32_t* adapter;     /* (device) [requests] */
+  const int32_t* ranks;       /* (device) [adapters] or NULL */
+  const float* scales;        /* (device) [adapters] or NULL */
+  const uint16_t* x;          /* (device) bf16 [rows, k] */
+  const uint16_t* a;          /* (device) bf16 [adapters, rank, k], dense */
+  const uint16_t* b;          /* (device) bf16 [adapters, n, rank], dense */
+  const void* base;           /* (device) [rows, n] or NULL */
+  void* out;                  /* (device) [rows, n] */
+  void* workspace;            /* (device) 16-byte aligned; calls sharing it must not overlap in time */
+  uint64_t workspace_bytes;
+} situ_moe_adapters_t;
+/* Bytes of workspace an adapters call needs (rows, n, k and rank are read). */
+situ_status situ_moe_adapters_workspace(const situ_moe_adapters_t* args, uint64_t* bytes);
+situ_status situ_moe_adapters(const situ_moe_adapters_t* args, void* hip_stream);
+
 /* Measurement aid for the roofline of the w4a8 GEMMs (not part of the
  * layer): the sustained rate of v_mfma_scale_f32_16x16x128_f8f6f4 with E2M1 x
  * E4M3 operands (the instruction the w4a8 FC1 kernels issue; 65536 flops
