@@ -27,14 +27,14 @@ namespace {
 
 constexpr float kL2e = 1.44269502162933349609375f;   // log2(e) rounded to fp32
 constexpr int kActThreads = 256;
+constexpr int kRows = kActThreads / 16;               // rows a workgroup takes at once
 constexpr int kActExperts = 1024;
 
 struct ActArgs {
   situ_moe_activation_t p;
   int32_t blocks;             // of 128 columns a row
   int32_t run;                // of them that sixteen lanes walk
-  int32_t runs;               // of them a row
-  int64_t items;              // rows * runs
+  int32_t share;              // rows of a workgroup, consecutive
 };
 
 // Constants of a row.
@@ -54,27 +54,44 @@ __device__ __forceinline__ void load_experts(Experts& x, const situ_moe_activati
   if (threadIdx.x == 0) x.offsets[p.experts] = p.offsets ? p.offsets[p.experts] : p.rows;
   __syncthreads();
 }
-// The expert of a row, -1 outside every group: the last one that starts at or before it, where it also ends behind it.
-__device__ __forceinline__ int expert_of(const Experts& x, int experts, int row) {
-  int lo = 0, hi = experts;   // offsets[lo] <= row < offsets[hi], if any
-  if (row < x.offsets[0] || row >= x.offsets[experts]) return -1;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) / 2;
-    if (x.offsets[mid] <= row) lo = mid; else hi = mid;
+// The expert e of a row: the last one that starts at or before it (its group then holds the row, where any does).  The
+// rows of a thread ascend, so that all but the first search (e < 0) go on from the row before.
+__device__ __forceinline__ bool find_expert(const Experts& x, int experts, int row, int& e) {
+  if (row < x.offsets[0] || row >= x.offsets[experts]) return false;
+  if (e < 0) {
+    int hi = experts;
+    e = 0;
+    while (hi - e > 1) {
+      const int mid = (e + hi) / 2;
+      if (x.offsets[mid] <= row) e = mid; else hi = mid;
+    }
   }
-  return lo;
+  while (e + 1 < experts && x.offsets[e + 1] <= row) ++e;
+  return true;
 }
 template <int KIND>
 __device__ __forceinline__ RowK row_k(const Experts& x, int e) {
   if constexpr (KIND == SITU_ACTIVATION_SWIGLU) return RowK{1.0f, 1.0f, 0.0f, 1.0f};
   const float b = x.p0[e], l = x.p1[e];
-  return RowK{b, 1.0f / b, l, 1.0f / l};
+  if constexpr (KIND == SITU_ACTIVATION_SWIGLU_BIAS) return RowK{b, 1.0f, l, 1.0f};
+  return RowK{b, __builtin_amdgcn_rcpf(b), l, __builtin_amdgcn_rcpf(l)};
 }
 
-// tanh_nd (common.hpp) for any x: a NaN stays one.
+// tanh(x) = n / d of fp32 values: x clamped to [-8, 8] (tanh(8) is 1 - 2^-22), n = x P(x^2), d = Q(x^2) with P of
+// degree 3 and Q of 4, fitted on [0, 8] for the smallest largest relative error (reweighted least squares on the
+// linearized residual x P - tanh(x) Q): 1.5e-7, within 6 * 2^-24 as evaluated here.  Both are divided by 64, so that
+// the product of two d and 1 + e^-g overflows no sooner than e^-g does.  A NaN stays one.
 __device__ __forceinline__ void tanh_parts(float x, float& n, float& d) {
-  tanh_nd(x, n, d);
-  n = x != x ? x : n;
+  constexpr float k = 0x1p-6f;
+  const float c = __builtin_elementwise_maximum(__builtin_elementwise_minimum(x, 8.0f), -8.0f);
+  const float s = c * c;
+  float p = 1.1475112e-05f * k, q = 2.4732324e-07f * k;
+  q = fmaf(q, s, 0.000239314897f * k);
+  p = fmaf(p, s, 0.00295580747f * k);  q = fmaf(q, s, 0.0238357844f * k);
+  p = fmaf(p, s, 0.129303546f * k);    q = fmaf(q, s, 0.462636088f * k);
+  p = fmaf(p, s, k);                   q = fmaf(q, s, k);
+  n = c * p;
+  d = q;
 }
 
 template <int KIND>
@@ -83,30 +100,27 @@ __device__ __forceinline__ float act(float g, float u, const RowK& k) {
     float n1, d1, n3, d3;
     tanh_parts(g * k.ib, n1, d1);
     tanh_parts(u * k.il, n3, d3);
-    // sigmoid = 1 / (1 + e), or e / (1 + e) for g < 0: no exponential that overflows
-    const float e = __builtin_amdgcn_exp2f(-fabsf(g) * kL2e), t = d1 * d3;
-    return (n1 * n3) * (g < 0.0f ? e : 1.0f) * __builtin_amdgcn_rcpf(fmaf(t, e, t)) * (k.b * k.l);
+    const float e = __builtin_amdgcn_exp2f(g * -kL2e), t = d1 * d3;
+    return (n1 * n3) * __builtin_amdgcn_rcpf(fmaf(t, e, t)) * (k.b * k.l);
   } else {
-    const float x = k.b * g, e = __builtin_amdgcn_exp2f(-fabsf(x) * kL2e);
-    return g * (u + k.l) * (x < 0.0f ? e : 1.0f) * __builtin_amdgcn_rcpf(1.0f + e);
+    const float e = __builtin_amdgcn_exp2f(k.b * g * -kL2e);
+    return g * (u + k.l) * __builtin_amdgcn_rcpf(1.0f + e);
   }
 }
 
-// tanh(x) and 1 - tanh(x)^2.  Below 1/4 the quotient would be a difference of near numbers: the odd series
-// to x^9, off by less than 2^-24 there.
+// tanh(x) and 1 - tanh(x)^2 = (1 - tanh)(1 + tanh), with e = e^-2|x|: tanh = 1 - e r and 1 + tanh = r, r = 2 / (1 + e).
+// Below 1/16, where 1 - e r is a difference of near numbers, the odd series to x^5, off by less than 2^-27; above it
+// 1 - e r is within 2^-20 of its value.
 __device__ __forceinline__ void tanh_slope(float x, float& t, float& slope) {
   const float e = __builtin_amdgcn_exp2f(fabsf(x) * (-2.0f * kL2e));
-  const float r = __builtin_amdgcn_rcpf(1.0f + e), er = e * r;
-  slope = 4.0f * er * r;
+  const float r = __builtin_amdgcn_rcpf(fmaf(e, 0.5f, 0.5f)), er = e * r;
+  slope = er * r;
   const float x2 = x * x;
-  float q = fmaf(x2, 62.0f / 2835.0f, -17.0f / 315.0f);
-  q = fmaf(x2, q, 2.0f / 15.0f);
-  q = fmaf(x2, q, -1.0f / 3.0f);
-  const float series = fmaf(x2 * x, q, x);
-  t = fabsf(x) < 0.25f ? series : __builtin_copysignf(fmaf(-2.0f, er, 1.0f), x);
+  const float series = fmaf(x2 * x, fmaf(x2, 2.0f / 15.0f, -1.0f / 3.0f), x);
+  t = fabsf(x) < 0.0625f ? series : __builtin_copysignf(1.0f - er, x);
 }
 __device__ __forceinline__ void sigmoid_both(float x, float& s, float& left) {
-  const float e = __builtin_amdgcn_exp2f(-fabsf(x) * kL2e);
+  const float e = __builtin_amdgcn_exp2f(fabsf(x) * -kL2e);
   const float r = __builtin_amdgcn_rcpf(1.0f + e), er = e * r;
   s = x < 0.0f ? er : r;
   left = x < 0.0f ? r : er;
@@ -151,10 +165,11 @@ __device__ __forceinline__ void codes8(const uint2& c, float s, float f[8]) {
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int w = (int)(i ? c.y : c.x);
-    f[4 * i] = __builtin_amdgcn_cvt_f32_fp8(w, 0) * s;
-    f[4 * i + 1] = __builtin_amdgcn_cvt_f32_fp8(w, 1) * s;
-    f[4 * i + 2] = __builtin_amdgcn_cvt_f32_fp8(w, 2) * s;
-    f[4 * i + 3] = __builtin_amdgcn_cvt_f32_fp8(w, 3) * s;
+    const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8(w, false), hi = __builtin_amdgcn_cvt_pk_f32_fp8(w, true);
+    f[4 * i] = lo[0] * s;
+    f[4 * i + 1] = lo[1] * s;
+    f[4 * i + 2] = hi[0] * s;
+    f[4 * i + 3] = hi[1] * s;
   }
 }
 // The largest magnitude of the sixteen lanes' eight (a NaN is passed over).
@@ -165,11 +180,17 @@ __device__ __forceinline__ float row_max(float v) {
 __device__ __forceinline__ float amax16(const float f[8]) {
   float m = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(f[i]));
+  for (int i = 0; i < 8; i += 2) m = fmaxf(fmaxf(fabsf(f[i]), fabsf(f[i + 1])), m);
   m = row_max<0x128>(m);
   m = row_max<0x124>(m);
   m = row_max<0x122>(m);
   return row_max<0x121>(m);
+}
+
+// Codes pass the caches by: they are read on the way back (262144 x 384: 213 us stored as h is, 189 so).
+__device__ __forceinline__ void put(uint8_t* p, const uint2& v) {
+  typedef int i32x2 __attribute__((ext_vector_type(2)));
+  __builtin_nontemporal_store(i32x2{(int)v.x, (int)v.y}, reinterpret_cast<i32x2*>(p));
 }
 
 template <int KIND, bool KEEP>
@@ -178,17 +199,22 @@ __global__ __launch_bounds__(kActThreads) void activation_kernel(ActArgs a) {
   const situ_moe_activation_t& p = a.p;
   load_experts(x, p, KIND != SITU_ACTIVATION_SWIGLU);
   const int at = threadIdx.x & 15;
-  for (int64_t item = (int64_t)blockIdx.x * (kActThreads / 16) + threadIdx.x / 16; item < a.items;
-       item += (int64_t)gridDim.x * (kActThreads / 16)) {
-    const int row = (int)((uint32_t)item / (uint32_t)a.runs), first = (int)((uint32_t)item - (uint32_t)row * a.runs) * a.run;
-    const int e = expert_of(x, p.experts, row);
-    if (e < 0) continue;
+  // this workgroup's rows, sixteen at a time, and columns
+  const int first = blockIdx.y * a.run, last = min(first + a.run, a.blocks);
+  const int end = (int)min((int64_t)(blockIdx.x + 1) * a.share, (int64_t)p.rows);
+  int row = (int)(blockIdx.x * a.share) + (int)(threadIdx.x / 16), e = -1;
+  const uint16_t* gu = p.gate_up + (int64_t)row * p.gate_up_stride + 8 * at;
+  uint16_t* h = p.h + (int64_t)row * p.h_stride + 8 * at;
+  uint8_t* codes = p.codes + (int64_t)row * (2 * p.inner) + 8 * at;
+  float* scales = p.scales + (int64_t)row * (2 * a.blocks);
+  for (; row < end; row += kRows, gu += kRows * p.gate_up_stride, h += kRows * p.h_stride,
+                    codes += (int64_t)kRows * 2 * p.inner, scales += kRows * 2 * a.blocks) {
+    if (!find_expert(x, p.experts, row, e)) continue;
     const RowK k = row_k<KIND>(x, e);
-    const uint16_t* gu = p.gate_up + (int64_t)row * p.gate_up_stride;
-    for (int b = first; b < min(first + a.run, a.blocks); ++b) {
-      const int col = b * 128 + 8 * at;
-      const bool in = col < p.inner;
-      float g[8], u[8];
+    for (int b = first; b < last; ++b) {
+      const int col = b * 128;
+      const bool in = col + 8 * at < p.inner;
+      float g[8], u[8], o[8];
       uint4 vg = make_uint4(0, 0, 0, 0), vu = vg;
       if (in) {
         vg = *reinterpret_cast<const uint4*>(gu + col);
@@ -199,21 +225,18 @@ __global__ __launch_bounds__(kActThreads) void activation_kernel(ActArgs a) {
       if constexpr (KEEP) {
         const float sg = block_scale(amax16(g)), su = block_scale(amax16(u));
         if (in) {
-          uint8_t* c = p.codes + (int64_t)row * (2 * p.inner) + col;
-          *reinterpret_cast<uint2*>(c) = block_codes(g, sg);
-          *reinterpret_cast<uint2*>(c + p.inner) = block_codes(u, su);
+          put(codes + col, block_codes(g, sg));
+          put(codes + p.inner + col, block_codes(u, su));
         }
         if (at == 0) {
-          float* s = p.scales + (int64_t)row * (2 * a.blocks) + b;
-          s[0] = sg;
-          s[a.blocks] = su;
+          scales[b] = sg;
+          scales[a.blocks + b] = su;
         }
       }
       if (in) {
-        float h[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) h[i] = act<KIND>(g[i], u[i], k);
-        *reinterpret_cast<uint4*>(p.h + (int64_t)row * p.h_stride + col) = pack8(h);
+        for (int i = 0; i < 8; ++i) o[i] = act<KIND>(g[i], u[i], k);
+        *reinterpret_cast<uint4*>(h + col) = pack8(o);
       }
     }
   }
@@ -225,72 +248,74 @@ __global__ __launch_bounds__(kActThreads) void activation_backward_kernel(ActArg
   const situ_moe_activation_t& p = a.p;
   load_experts(x, p, KIND != SITU_ACTIVATION_SWIGLU);
   const int at = threadIdx.x & 15;
-  for (int64_t item = (int64_t)blockIdx.x * (kActThreads / 16) + threadIdx.x / 16; item < a.items;
-       item += (int64_t)gridDim.x * (kActThreads / 16)) {
-    const int row = (int)((uint32_t)item / (uint32_t)a.runs), first = (int)((uint32_t)item - (uint32_t)row * a.runs) * a.run;
-    const int e = expert_of(x, p.experts, row);
-    if (e < 0) continue;
+  const int first = blockIdx.y * a.run, last = min(first + a.run, a.blocks);
+  const int end = (int)min((int64_t)(blockIdx.x + 1) * a.share, (int64_t)p.rows);
+  int row = (int)(blockIdx.x * a.share) + (int)(threadIdx.x / 16), e = -1;
+  const uint16_t* gu = p.gate_up + (int64_t)row * p.gate_up_stride + 8 * at;
+  const uint16_t* dhs = p.dh + (int64_t)row * p.dh_stride + 8 * at;
+  const uint8_t* codes = p.codes + (int64_t)row * (2 * p.inner) + 8 * at;
+  const float* scales = p.scales + (int64_t)row * (2 * a.blocks);
+  uint16_t* hs = p.h + (int64_t)row * p.h_stride + 8 * at;
+  uint16_t* ds = p.d_gate_up + (int64_t)row * p.d_gate_up_stride + 8 * at;
+  for (; row < end; row += kRows, gu += kRows * p.gate_up_stride, dhs += kRows * p.dh_stride,
+                    codes += (int64_t)kRows * 2 * p.inner, scales += kRows * 2 * a.blocks, hs += kRows * p.h_stride,
+                    ds += kRows * p.d_gate_up_stride) {
+    if (!find_expert(x, p.experts, row, e)) continue;
     const RowK k = row_k<KIND>(x, e);
-    for (int b = first; b < min(first + a.run, a.blocks); ++b) {
-      const int col = b * 128 + 8 * at;
-      if (col >= p.inner) continue;
+    for (int b = first; b < last; ++b) {
+      const int col = b * 128;
+      if (col + 8 * at >= p.inner) continue;
       float g[8], u[8], dh[8], h[8];
       if constexpr (KEPT) {
-        const uint8_t* c = p.codes + (int64_t)row * (2 * p.inner) + col;
-        const float* s = p.scales + (int64_t)row * (2 * a.blocks) + b;
-        const uint2 cg = *reinterpret_cast<const uint2*>(c), cu = *reinterpret_cast<const uint2*>(c + p.inner);
-        codes8(cg, s[0], g);
-        codes8(cu, s[a.blocks], u);
+        const uint2 cg = *reinterpret_cast<const uint2*>(codes + col), cu = *reinterpret_cast<const uint2*>(codes + p.inner + col);
+        codes8(cg, scales[b], g);
+        codes8(cu, scales[a.blocks + b], u);
       } else {
-        const uint16_t* gu = p.gate_up + (int64_t)row * p.gate_up_stride + col;
-        unpack8(*reinterpret_cast<const uint4*>(gu), g);
-        unpack8(*reinterpret_cast<const uint4*>(gu + p.inner), u);
+        unpack8(*reinterpret_cast<const uint4*>(gu + col), g);
+        unpack8(*reinterpret_cast<const uint4*>(gu + p.inner + col), u);
       }
-      unpack8(*reinterpret_cast<const uint4*>(p.dh + (int64_t)row * p.dh_stride + col), dh);
+      unpack8(*reinterpret_cast<const uint4*>(dhs + col), dh);
 #pragma unroll
       for (int i = 0; i < 8; ++i) act_backward<KIND>(g[i], u[i], dh[i], k, g[i], u[i], h[i]);
-      uint16_t* d = p.d_gate_up + (int64_t)row * p.d_gate_up_stride + col;
-      *reinterpret_cast<uint4*>(d) = pack8(g);
-      *reinterpret_cast<uint4*>(d + p.inner) = pack8(u);
-      if constexpr (AGAIN) *reinterpret_cast<uint4*>(p.h + (int64_t)row * p.h_stride + col) = pack8(h);
+      *reinterpret_cast<uint4*>(ds + col) = pack8(g);
+      *reinterpret_cast<uint4*>(ds + p.inner + col) = pack8(u);
+      if constexpr (AGAIN) *reinterpret_cast<uint4*>(hs + col) = pack8(h);
     }
   }
 }
 
-// Sixteen lanes walk a whole row where there are rows enough for 32 waves a CU,
-// and parts of one where there are not.
-ActArgs act_args(const situ_moe_activation_t& p, int cus) {
+// Sixteen lanes walk a whole row where there are rows enough for 32 waves a CU, and parts of one where there are not.
+ActArgs act_args(const situ_moe_activation_t& p, int cus, dim3& grid) {
   ActArgs a{};
   a.p = p;
   a.blocks = (p.inner + 127) / 128;
-  const int64_t wanted = (int64_t)cus * 32 * 4;
-  const int64_t runs = std::min<int64_t>(a.blocks, std::max<int64_t>(1, wanted / std::max(p.rows, 1)));
-  a.run = (int)((a.blocks + runs - 1) / runs);
-  a.runs = (a.blocks + a.run - 1) / a.run;
-  a.items = (int64_t)p.rows * a.runs;
+  const int wanted = cus * 8;                        // workgroups
+  const int groups = (p.rows + kRows - 1) / kRows;
+  const int runs = std::min(a.blocks, std::max(1, wanted / groups));
+  a.run = (a.blocks + runs - 1) / runs;
+  grid.y = (unsigned)((a.blocks + a.run - 1) / a.run);
+  const int shares = std::min(groups, std::max(1, wanted / (int)grid.y));
+  a.share = (groups + shares - 1) / shares * kRows;
+  grid.x = (unsigned)((p.rows + a.share - 1) / a.share);
   return a;
-}
-int act_grid(const ActArgs& a, int cus) {
-  constexpr int kItems = kActThreads / 16;
-  return (int)std::min<int64_t>((a.items + kItems - 1) / kItems, (int64_t)cus * 8);
 }
 
 template <int KIND>
-void forward_go(const ActArgs& a, int grid, hipStream_t s) {
-  if (a.p.codes) hipLaunchKernelGGL((activation_kernel<KIND, true>), dim3(grid), dim3(kActThreads), 0, s, a);
-  else hipLaunchKernelGGL((activation_kernel<KIND, false>), dim3(grid), dim3(kActThreads), 0, s, a);
+void forward_go(const ActArgs& a, dim3 grid, hipStream_t s) {
+  if (a.p.codes) hipLaunchKernelGGL((activation_kernel<KIND, true>), grid, dim3(kActThreads), 0, s, a);
+  else hipLaunchKernelGGL((activation_kernel<KIND, false>), grid, dim3(kActThreads), 0, s, a);
 }
 template <int KIND, bool KEPT>
-void backward_go(const ActArgs& a, int grid, hipStream_t s) {
-  if (a.p.h) hipLaunchKernelGGL((activation_backward_kernel<KIND, KEPT, true>), dim3(grid), dim3(kActThreads), 0, s, a);
-  else hipLaunchKernelGGL((activation_backward_kernel<KIND, KEPT, false>), dim3(grid), dim3(kActThreads), 0, s, a);
+void backward_go(const ActArgs& a, dim3 grid, hipStream_t s) {
+  if (a.p.h) hipLaunchKernelGGL((activation_backward_kernel<KIND, KEPT, true>), grid, dim3(kActThreads), 0, s, a);
+  else hipLaunchKernelGGL((activation_backward_kernel<KIND, KEPT, false>), grid, dim3(kActThreads), 0, s, a);
 }
 
 }  // namespace
 
 hipError_t launch_activation(const situ_moe_activation_t& p, int cus, hipStream_t s) {
-  const ActArgs a = act_args(p, cus);
-  const int grid = act_grid(a, cus);
+  dim3 grid;
+  const ActArgs a = act_args(p, cus, grid);
   switch (p.activation) {
     case SITU_ACTIVATION_SITU: forward_go<SITU_ACTIVATION_SITU>(a, grid, s); break;
     case SITU_ACTIVATION_SWIGLU: forward_go<SITU_ACTIVATION_SWIGLU>(a, grid, s); break;
@@ -300,8 +325,8 @@ hipError_t launch_activation(const situ_moe_activation_t& p, int cus, hipStream_
 }
 
 hipError_t launch_activation_backward(const situ_moe_activation_t& p, int cus, hipStream_t s) {
-  const ActArgs a = act_args(p, cus);
-  const int grid = act_grid(a, cus);
+  dim3 grid;
+  const ActArgs a = act_args(p, cus, grid);
   const bool kept = !p.gate_up;
   switch (p.activation) {
     case SITU_ACTIVATION_SITU:

@@ -27,39 +27,42 @@ namespace situ {
 
 namespace {
 
-constexpr int kWaves = 4;
+constexpr int kUpWaves = 4;
 
 struct AdapterArgs {
   situ_moe_adapters_t p;
-  float* t;                   // [parts][rows][rank]
-  int32_t tile;               // rows of a tile, 1 .. 16
-  int32_t tiles;
-  int32_t parts;
-  int32_t cols;               // the second product: columns of a wave, a multiple of 64
-  int32_t chunks;             // of them in n
+  uint16_t *high, *low;       // t as two bf16 terms, [rows][rank] each
+  int32_t tile;               // rows of a tile of the first product, 1 .. 32
+  int32_t up_tile;            // of the second, 1 .. 16
+  int32_t up_tiles;
+  int32_t run;                // of them a wave takes in turn (one launch: columns of a workgroup)
+  int32_t chunks;             // of 128 columns in n (one launch: of `run` columns)
 };
 
-// The requests that reach into rows [r0, r1): a wave's lanes hold 64 consecutive ones.
+// Sixty-four consecutive requests, one a lane.
 struct Requests {
-  int32_t first, lo, hi, adapter;   // of lane i: request first + i
-  uint64_t some;                    // the lanes whose request has rows in the tile
-  bool more;                        // the next 64 may reach into the tile too
+  int32_t first, begin, end, adapter;   // of lane i: request first + i
 };
-__device__ __forceinline__ void requests_at(const situ_moe_adapters_t& p, int first, int r0, int r1, int lane, Requests& q) {
-  q.first = first;
-  q.lo = q.hi = 0;
-  q.adapter = -1;
+__device__ __forceinline__ void load_requests(const situ_moe_adapters_t& p, int first, int lane, Requests& q) {
   const int i = first + lane;
+  q.first = first;
+  q.begin = q.end = 0;
+  q.adapter = -1;
   if (i < p.requests) {
-    q.lo = max(p.offsets[i], r0);
-    q.hi = min(p.offsets[i + 1], r1);
+    q.begin = p.offsets[i];
+    q.end = p.offsets[i + 1];
     q.adapter = p.adapter[i];
     if (q.adapter >= p.adapters) q.adapter = -1;
   }
-  q.some = __ballot(q.lo < q.hi);
-  q.more = first + 64 < p.requests && p.offsets[first + 64] < r1;
 }
-// The first request of 64 among which is the first that reaches into a tile from r0.
+// The lanes whose requests have rows in [r0, r1), and whether the next 64 may have some too.
+__device__ __forceinline__ uint64_t in_tile(const Requests& q, int r0, int r1) {
+  return __ballot(max(q.begin, r0) < min(q.end, r1));
+}
+__device__ __forceinline__ bool reaches_on(const situ_moe_adapters_t& p, const Requests& q, int r1) {
+  return q.first + 64 < p.requests && __builtin_amdgcn_readlane(q.end, 63) < r1;
+}
+// The first of 64 requests among which is the first that reaches into a tile from r0.
 __device__ __forceinline__ int first_request(const situ_moe_adapters_t& p, int r0, int lane) {
   int lo = 0, size = p.requests;
   while (size > 64) {
@@ -77,227 +80,418 @@ __device__ __forceinline__ int next_bit(uint64_t& m) {
   return i;
 }
 
-__device__ __forceinline__ uint4 load16(const uint16_t* p, bool in) {
-  return in ? *reinterpret_cast<const uint4*>(p) : make_uint4(0, 0, 0, 0);
+// Sixteen bytes, zeros where there are none: the address is chosen and not the load branched around, since behind
+// branches the compiler cannot count the loads in flight and waits for all of them.
+__device__ const uint4 kZeros[1] = {};
+__device__ __forceinline__ uint4 load16(const void* p, bool in) {
+  typedef const i32x4 __attribute__((address_space(1)))* Global;
+  const Global at = (Global)p, zeros = (Global)kZeros;
+  return __builtin_bit_cast(uint4, *(in ? at : zeros));
 }
 __device__ __forceinline__ f32x4 mfma(const uint4& a, const uint4& b, const f32x4& c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
 
-// t.  Lane l holds ranks 16 i + l % 16 of a (rows of the instruction) and token l % 16 of x (columns), eight of k
-// from 8 (l / 16); a step is 64 of k, whole lines.  RT: tiles of 16 ranks.
-template <int RT>
-__global__ __launch_bounds__(64 * kWaves) void adapters_down_kernel(AdapterArgs a) {
-  __shared__ f32x4 part[kWaves - 1][RT][64];
-  const situ_moe_adapters_t& p = a.p;
-  const int lane = lane_id(), wave = threadIdx.x / kWave, col = lane & 15, group = lane >> 4;
-  const int tile = blockIdx.x % a.tiles, piece = blockIdx.x / a.tiles;
-  const int r0 = tile * a.tile, r1 = min(r0 + a.tile, p.rows);
-  const int units = (p.k + 63) / 64;
-  const int u0 = (int)((int64_t)units * piece / a.parts), u1 = (int)((int64_t)units * (piece + 1) / a.parts);
-  const int row = r0 + col;
-  const uint16_t* x = p.x + (int64_t)min(row, r1 - 1) * p.x_stride;
-  Requests q;
-  q.more = true;
-  for (int first = first_request(p, r0, lane); q.more; first += 64) {
-    requests_at(p, first, r0, r1, lane, q);
-    while (q.some) {
-      const int at = next_bit(q.some);
-      const int i = __builtin_amdgcn_readlane(q.adapter, at);
-      if (i < 0) continue;
-      const int lo = __builtin_amdgcn_readlane(q.lo, at), hi = __builtin_amdgcn_readlane(q.hi, at);
-      const uint16_t* w = p.a + (int64_t)i * p.rank * p.k;
-      f32x4 acc[RT];
+__device__ __forceinline__ void unpack8(const uint4& v, float f[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-      for (int j = 0; j < RT; ++j) acc[j] = f32x4{0, 0, 0, 0};
-      for (int u = u0 + wave; u < u1; u += kWaves) {
-        const int k = u * 64 + 8 * group;
-        const bool in0 = k < p.k, in1 = k + 32 < p.k;
-        const uint4 x0 = load16(x + k, in0), x1 = load16(x + k + 32, in1);
-#pragma unroll
-        for (int j = 0; j < RT; ++j) {
-          const uint16_t* v = w + (int64_t)min(16 * j + col, p.rank - 1) * p.k + k;
-          acc[j] = mfma(load16(v, in0), x0, acc[j]);
-          acc[j] = mfma(load16(v + 32, in1), x1, acc[j]);
-        }
-      }
-      __syncthreads();                                // the last request's sums have been read
-      if (wave > 0) {
-#pragma unroll
-        for (int j = 0; j < RT; ++j) part[wave - 1][j][lane] = acc[j];
-      }
-      __syncthreads();
-      if (wave == 0) {
-        const float c = p.scales ? p.scales[i] : 1.0f;
-        const int rank = p.ranks ? min(max(p.ranks[i], 0), p.rank) : p.rank;
-        float* out = a.t + ((int64_t)piece * p.rows + row) * p.rank;
-#pragma unroll
-        for (int j = 0; j < RT; ++j) {
-          f32x4 v = acc[j];
-#pragma unroll
-          for (int o = 0; o < kWaves - 1; ++o) v += part[o][j][lane];
-          const int r = 16 * j + 4 * group;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) v[e] = r + e < rank ? v[e] * c : 0.0f;
-          if (row >= lo && row < hi && r < p.rank) *reinterpret_cast<f32x4*>(out + r) = v;
-        }
-      }
-    }
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = bf16_to_f32(w[i] & 0xffffu);
+    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
   }
 }
+__device__ __forceinline__ uint4 pack8(const float f[8]) {
+  const bf16x8 b = {(__bf16)f[0], (__bf16)f[1], (__bf16)f[2], (__bf16)f[3],
+                    (__bf16)f[4], (__bf16)f[5], (__bf16)f[6], (__bf16)f[7]};   // nearest even
+  return __builtin_bit_cast(uint4, b);
+}
 
-// Eight ranks of t as two bf16 terms.  A rounded value that is not finite has no second.
-__device__ __forceinline__ void two_terms(const float t[8], uint4& high, uint4& low) {
-  bf16x8 h, l;
+// Four ranks of t as two bf16 terms.  A rounded value that is not finite has no second.
+__device__ __forceinline__ void two_terms(const f32x4& t, uint2& high, uint2& low) {
+  typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+  bf16x4 h, l;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < 4; ++i) {
     h[i] = (__bf16)t[i];
     const float d = t[i] - (float)h[i];
     l[i] = (__bf16)(fabsf(d) < __builtin_inff() ? d : 0.0f);
   }
-  high = __builtin_bit_cast(uint4, h);
-  low = __builtin_bit_cast(uint4, l);
+  high = __builtin_bit_cast(uint2, h);
+  low = __builtin_bit_cast(uint2, l);
 }
 
-// out.  Lane l holds columns of out (rows of b, rows of the instruction) and
-// token l % 16, eight ranks from 8 (l / 16).  Row m of instruction s is column 32
-// (s / 2) + 8 (m / 4) + 4 (s % 2) + m % 4, so that a lane ends with eight
-// consecutive columns of its token from each two: 16 bytes of bf16.
-// KS: steps of 32 ranks; 0: at most 16 ranks, the low term beside the high one.
-template <int KS, bool F32>
-__global__ __launch_bounds__(64 * kWaves) void adapters_up_kernel(AdapterArgs a, int64_t items) {
-  constexpr int S = KS ? KS : 1;
+// t.  A workgroup takes a tile of rows, its waves every W-th unit of 64 of k.  A unit of x and a is requested by whole
+// lines, eight lanes of 16 bytes a row (rows of 64 bytes, as the matrix instruction holds them, go through the address
+// unit at half the rate), put into the wave's own LDS and read back as operands: lane l ranks 16 i + l % 16 of a (rows
+// of the instruction) and tokens 16 j + l % 16 of x (columns), eight of k.  Piece c of row r lies in place c ^ (r % 8).
+// U units are under way while one is multiplied.  RT: tiles of 16 ranks; TG: of 16 tokens.
+template <int RT, int TG, int U, int W>
+__global__ __launch_bounds__(64 * W) void adapters_down_kernel(AdapterArgs a) {
+  constexpr int kParts = 2 * (RT + TG);               // of eight rows in a unit
+  static_assert(RT * TG <= kParts, "the sums take the units' place");
+  __shared__ uint4 lds[W][kParts * 64];
   const situ_moe_adapters_t& p = a.p;
-  const int lane = lane_id(), col = lane & 15, group = lane >> 4;
-  const int64_t item = (int64_t)blockIdx.x * kWaves + threadIdx.x / kWave;
-  if (item >= items) return;
-  const int tile = (int)((uint32_t)item / (uint32_t)a.chunks), chunk = (int)((uint32_t)item - (uint32_t)tile * a.chunks);
-  const int r0 = tile * a.tile, r1 = min(r0 + a.tile, p.rows);
-  const int row = r0 + col;
-  const int first = first_request(p, r0, lane);
+  const int lane = lane_id(), wave = wave_id(), col = lane & 15, group = lane >> 4;
+  const int line = lane >> 3, piece = lane & 7;
+  const int r0 = blockIdx.x * a.tile, r1 = min(r0 + a.tile, p.rows);
+  const int units = (p.k + 63) / 64;
+  uint4* mine = lds[wave];
+  const uint16_t* x[2 * TG];
+#pragma unroll
+  for (int j = 0; j < 2 * TG; ++j) x[j] = p.x + (int64_t)min(r0 + 8 * j + line, r1 - 1) * p.x_stride + 8 * piece;
   Requests q;
-  requests_at(p, first, r0, r1, lane, q);
-  const bool whole = !q.more;                        // these 64 are all
-  // t of the token: rows of requests without an adapter hold anything, and are not used
-  uint4 high[S], low[S];
+  for (int first = first_request(p, r0, lane);; first += 64) {
+    load_requests(p, first, lane, q);
+    uint64_t some = in_tile(q, r0, r1);
+    while (some) {
+      const int at = next_bit(some);
+      const int i = __builtin_amdgcn_readlane(q.adapter, at);
+      if (i < 0) continue;
+      const int lo = max(__builtin_amdgcn_readlane(q.begin, at), r0), hi = min(__builtin_amdgcn_readlane(q.end, at), r1);
+      const uint16_t* w[2 * RT];
 #pragma unroll
-  for (int s = 0; s < S; ++s) {
-    const int r = KS ? 32 * s + 8 * group : 8 * (group & 1);
-    float t[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (r < p.rank && row < r1) {
-      const float* at = a.t + (int64_t)row * p.rank + r;
-      for (int i = 0; i < a.parts; ++i, at += (int64_t)p.rows * p.rank) {
-        const f32x4 u = *reinterpret_cast<const f32x4*>(at), v = *reinterpret_cast<const f32x4*>(at + 4);
+      for (int j = 0; j < 2 * RT; ++j) w[j] = p.a + ((int64_t)i * p.rank + min(8 * j + line, p.rank - 1)) * p.k + 8 * piece;
+      f32x4 acc[RT][TG];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) { t[e] += u[e]; t[4 + e] += v[e]; }
-      }
-    }
-    two_terms(t, high[s], low[s]);
-    if (!KS && group >= 2) high[s] = low[s];
-  }
-  const int c1 = min((chunk + 1) * a.cols, p.n);
-  for (int c0 = chunk * a.cols; c0 < c1; c0 += 64) {
-    f32x4 sum[4];
+      for (int j = 0; j < RT; ++j)
 #pragma unroll
-    for (int s = 0; s < 4; ++s) sum[s] = f32x4{0, 0, 0, 0};
-    bool held = false;                               // the token has a request
-    // base, while the adapters' products run
-    uint4 b0[2], b1[2];
-    const int64_t base = (int64_t)row * p.base_stride;
+        for (int g = 0; g < TG; ++g) acc[j][g] = f32x4{0, 0, 0, 0};
+      struct Unit { uint4 v[kParts]; };
+      auto request = [&](Unit& f, int u) {
+        const bool in = u < units && u * 64 + 8 * piece < p.k;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int c = c0 + 32 * h + 8 * group;
-      b0[h] = b1[h] = make_uint4(0, 0, 0, 0);
-      if (p.base && row < r1 && c < p.n) {
-        if constexpr (F32) {
-          const uint4* v = reinterpret_cast<const uint4*>(static_cast<const float*>(p.base) + base + c);
-          b0[h] = v[0];
-          b1[h] = v[1];
-        } else {
-          b0[h] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.base) + base + c);
+        for (int j = 0; j < 2 * TG; ++j) f.v[j] = load16(x[j] + u * 64, in);
+#pragma unroll
+        for (int j = 0; j < 2 * RT; ++j) f.v[2 * TG + j] = load16(w[j] + u * 64, in);
+      };
+      auto store = [&](const Unit& f) {
+#pragma unroll
+        for (int j = 0; j < kParts; ++j) mine[64 * j + 8 * line + (piece ^ line)] = f.v[j];
+        wave_lds();
+      };
+      auto multiply = [&] {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int c = (4 * h + group) ^ (col & 7);
+          uint4 xt[TG], at_[RT];
+#pragma unroll
+          for (int g = 0; g < TG; ++g) xt[g] = mine[8 * (16 * g + col) + c];
+#pragma unroll
+          for (int j = 0; j < RT; ++j) at_[j] = mine[8 * (16 * (TG + j) + col) + c];
+#pragma unroll
+          for (int j = 0; j < RT; ++j)
+#pragma unroll
+            for (int g = 0; g < TG; ++g) acc[j][g] = mfma(at_[j], xt[g], acc[j][g]);
+        }
+        wave_lds();
+      };
+      Unit f[U];
+#pragma unroll
+      for (int v = 0; v < U; ++v) request(f[v], wave + v * W);
+      for (int u = wave; u < units; u += U * W) {
+#pragma unroll
+        for (int v = 0; v < U; ++v) {
+          store(f[v]);                                // of units past the last: zeros
+          request(f[v], u + (U + v) * W);
+          multiply();
         }
       }
+      // the waves' sums: each adds up every W-th tile of 16 ranks and tokens
+#pragma unroll
+      for (int j = 0; j < RT; ++j)
+#pragma unroll
+        for (int g = 0; g < TG; ++g) mine[64 * (j * TG + g) + lane] = __builtin_bit_cast(uint4, acc[j][g]);
+      __syncthreads();
+      const float c = p.scales ? p.scales[i] : 1.0f;
+      const int rank = p.ranks ? min(max(p.ranks[i], 0), p.rank) : p.rank;
+      for (int o = wave; o < RT * TG; o += W) {
+        f32x4 v = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int e = 0; e < W; ++e) v += __builtin_bit_cast(f32x4, lds[e][64 * o + lane]);
+        const int r = 16 * (o / TG) + 4 * group, row = r0 + 16 * (o % TG) + col;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = r + e < rank ? v[e] * c : 0.0f;
+        if (row >= lo && row < hi && r < p.rank) {
+          uint2 high, low;
+          two_terms(v, high, low);
+          *reinterpret_cast<uint2*>(a.high + (int64_t)row * p.rank + r) = high;
+          *reinterpret_cast<uint2*>(a.low + (int64_t)row * p.rank + r) = low;
+        }
+      }
+      __syncthreads();                                // before the next request's units take their place
     }
-    int start = first;
+    if (!reaches_on(p, q, r1)) break;
+  }
+}
+
+// out.  Tokens are the rows of the instruction and columns of out its columns: lane l holds token l % 16, eight ranks
+// from 8 (l / 16), and of instruction s column 8 (l % 16) + s, so that it ends with eight consecutive columns of the
+// four tokens 4 (l / 16) ..: 16 bytes of bf16, 256 consecutive ones a token.  A wave takes 128 columns of a run of
+// tiles and keeps its columns of b while the adapter stays the same (KEEP: up to 64 ranks).
+// KS: steps of 32 ranks; 0: at most 16 ranks, the low term beside the high one.
+template <int KS, bool F32>
+__global__ __launch_bounds__(64 * kUpWaves) void adapters_up_kernel(AdapterArgs a, int64_t items) {
+  constexpr int S = KS ? KS : 1, NB = F32 ? 2 : 1;
+  constexpr bool KEEP = S <= 2;
+  const situ_moe_adapters_t& p = a.p;
+  const int lane = lane_id(), col = lane & 15, group = lane >> 4;
+  const int64_t item = (int64_t)blockIdx.x * kUpWaves + wave_id();
+  if (item >= items) return;
+  const int run = (int)((uint32_t)item / (uint32_t)a.chunks), chunk = (int)((uint32_t)item - (uint32_t)run * a.chunks);
+  const int c = chunk * 128 + 8 * col;               // the lane's eight columns
+  const bool in = c < p.n;
+  const int r_at = KS ? 8 * group : 8 * (group & 1); // its ranks, of each 32
+  auto load_b = [&](const uint16_t* w, int rank, int s, int ks) {
+    const int r = 32 * ks + r_at;
+    uint4 f = load16(w + s * p.rank + 32 * ks, in && r < rank);
+    if (r + 8 > rank) {                              // columns past the adapter's own rank
+      uint32_t g[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (r + 2 * e >= rank) g[e] = 0;
+        else if (r + 2 * e + 1 >= rank) g[e] &= 0xffffu;
+      }
+      f = make_uint4(g[0], g[1], g[2], g[3]);
+    }
+    return f;
+  };
+  const int tile1 = min((run + 1) * a.run, a.up_tiles);
+  // what a tile needs of base and of t, requested while the one before is computed
+  struct Tile { uint4 base[4][NB], high[S], low[KS ? S : 1]; };
+  auto request = [&](Tile& f, int tile) {
+    const int r0 = tile * a.up_tile, r1 = tile < tile1 ? min(r0 + a.up_tile, p.rows) : 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = r0 + 4 * group + i;
+#pragma unroll
+      for (int h = 0; h < NB; ++h)
+        f.base[i][h] = load16(static_cast<const char*>(p.base) + ((int64_t)row * p.base_stride + c) * (F32 ? 4 : 2) + 16 * h,
+                              p.base && in && row < r1);
+    }
+    // of token l % 16: rows of requests without an adapter hold anything, and are not used
+    const int64_t t = (int64_t)(r0 + col) * p.rank + r_at;
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+      const bool on = 32 * s + r_at < p.rank && r0 + col < r1;
+      if constexpr (KS == 0) {
+        f.high[s] = load16((group < 2 ? a.high : a.low) + t, on);
+      } else {
+        f.high[s] = load16(a.high + t + 32 * s, on);
+        f.low[s] = load16(a.low + t + 32 * s, on);
+      }
+    }
+  };
+  Tile now;
+  request(now, run * a.run);
+  Requests q;
+  load_requests(p, first_request(p, run * a.run * a.up_tile, lane), lane, q);
+  int held = -1;                                     // the adapter whose b is kept
+  uint4 b[KEEP ? S : 1][8];
+  for (int tile = run * a.run; tile < tile1; ++tile) {
+    const int r0 = tile * a.up_tile, r1 = min(r0 + a.up_tile, p.rows);
+    const int mine = r0 + 4 * group;                 // the first of the lane's four rows of out
+    const Tile f = now;
+    request(now, tile + 1);
+    f32x4 sum[8];
+#pragma unroll
+    for (int s = 0; s < 8; ++s) sum[s] = f32x4{0, 0, 0, 0};
+    uint32_t of_request = 0;                         // bit i: row mine + i has a request
     for (;;) {
-      if (!whole) requests_at(p, start, r0, r1, lane, q);
-      uint64_t some = q.some;
+      uint64_t some = in_tile(q, r0, r1);
       while (some) {
         const int at = next_bit(some);
         const int i = __builtin_amdgcn_readlane(q.adapter, at);
-        const bool mine = row >= __builtin_amdgcn_readlane(q.lo, at) && row < __builtin_amdgcn_readlane(q.hi, at);
-        held = held || mine;
+        const int lo = __builtin_amdgcn_readlane(q.begin, at), hi = min(__builtin_amdgcn_readlane(q.end, at), r1);
+        uint32_t own = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) own |= (mine + e >= lo && mine + e < hi ? 1u : 0u) << e;
+        of_request |= own;
         if (i < 0) continue;
         const int rank = p.ranks ? min(max(p.ranks[i], 0), p.rank) : p.rank;
-        const uint16_t* w = p.b + (int64_t)i * p.n * p.rank;
+        const uint16_t* w = p.b + ((int64_t)i * p.n + c) * p.rank + r_at;
+        if (KEEP && i != held) {
+          held = i;
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          const int c = c0 + 32 * (s / 2) + 8 * (col / 4) + 4 * (s % 2) + col % 4;
+          for (int s = 0; s < 8; ++s)
+#pragma unroll
+            for (int ks = 0; ks < S; ++ks) b[KEEP ? ks : 0][s] = load_b(w, rank, s, ks);
+        }
+        const bool all = lo <= r0 && hi >= r1;       // the tile is this request's alone
+#pragma unroll
+        for (int s = 0; s < 8; ++s) {
           f32x4 v = f32x4{0, 0, 0, 0};
 #pragma unroll
           for (int ks = 0; ks < S; ++ks) {
-            const int r = KS ? 32 * ks + 8 * group : 8 * (group & 1);
-            uint4 f = load16(w + (int64_t)min(c, p.n - 1) * p.rank + r, r < rank);
-            if (r + 8 > rank) {                      // columns past the adapter's own rank
-              uint32_t g[4] = {f.x, f.y, f.z, f.w};
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                if (r + 2 * e >= rank) g[e] = 0;
-                else if (r + 2 * e + 1 >= rank) g[e] &= 0xffffu;
-              }
-              f = make_uint4(g[0], g[1], g[2], g[3]);
-            }
-            v = mfma(f, high[ks], v);
-            if constexpr (KS != 0) v = mfma(f, low[ks], v);
+            const uint4 g = KEEP ? b[KEEP ? ks : 0][s] : load_b(w, rank, s, ks);
+            v = mfma(f.high[ks], g, v);
+            if constexpr (KS != 0) v = mfma(f.low[ks], g, v);
           }
+          if (all) {
+            sum[s] = v;
+          } else {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) sum[s][e] = mine ? v[e] : sum[s][e];
+            for (int e = 0; e < 4; ++e) sum[s][e] = own >> e & 1 ? v[e] : sum[s][e];
+          }
         }
       }
-      if (whole || !q.more) break;
-      start += 64;
+      if (!reaches_on(p, q, r1)) break;
+      load_requests(p, q.first + 64, lane, q);
     }
-    if (held && row < r1) {
-      const int64_t out = (int64_t)row * p.out_stride;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int c = c0 + 32 * h + 8 * group;
-        if (c >= p.n) continue;
-        const uint32_t u[4] = {b0[h].x, b0[h].y, b0[h].z, b0[h].w};
-        float f[8];
-        if constexpr (F32) {
-          const uint32_t v[4] = {b1[h].x, b1[h].y, b1[h].z, b1[h].w};
+    for (int i = 0; i < 4; ++i) {
+      if (!in || !(of_request >> i & 1)) continue;
+      float o[8];
+      if constexpr (F32) {
+        const uint32_t u[8] = {f.base[i][0].x, f.base[i][0].y, f.base[i][0].z, f.base[i][0].w,
+                               f.base[i][NB - 1].x, f.base[i][NB - 1].y, f.base[i][NB - 1].z, f.base[i][NB - 1].w};
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            f[e] = __uint_as_float(u[e]) + sum[2 * h][e];
-            f[4 + e] = __uint_as_float(v[e]) + sum[2 * h + 1][e];
-          }
-          float* o = static_cast<float*>(p.out) + out + c;
-          *reinterpret_cast<f32x4*>(o) = f32x4{f[0], f[1], f[2], f[3]};
-          *reinterpret_cast<f32x4*>(o + 4) = f32x4{f[4], f[5], f[6], f[7]};
-        } else {
+        for (int s = 0; s < 8; ++s) o[s] = __uint_as_float(u[s]) + sum[s][i];
+        float* to = static_cast<float*>(p.out) + (int64_t)(mine + i) * p.out_stride + c;
+        *reinterpret_cast<f32x4*>(to) = f32x4{o[0], o[1], o[2], o[3]};
+        *reinterpret_cast<f32x4*>(to + 4) = f32x4{o[4], o[5], o[6], o[7]};
+      } else {
+        unpack8(f.base[i][0], o);
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            f[2 * e] = bf16_to_f32(u[e] & 0xffffu) + sum[2 * h][2 * e];
-            f[2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u) + sum[2 * h][2 * e + 1];
-            f[4 + 2 * e] = bf16_to_f32(u[2 + e] & 0xffffu) + sum[2 * h + 1][2 * e];
-            f[5 + 2 * e] = __uint_as_float(u[2 + e] & 0xffff0000u) + sum[2 * h + 1][2 * e + 1];
-          }
-          const bf16x8 b = {(__bf16)f[0], (__bf16)f[1], (__bf16)f[2], (__bf16)f[3],
-                            (__bf16)f[4], (__bf16)f[5], (__bf16)f[6], (__bf16)f[7]};   // nearest even
-          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + out + c) = __builtin_bit_cast(uint4, b);
-        }
+        for (int s = 0; s < 8; ++s) o[s] += sum[s][i];
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + (int64_t)(mine + i) * p.out_stride + c) = pack8(o);
       }
     }
+  }
+}
+
+// One row, as decode's requests have: both products in one launch.  A workgroup takes a row and a share of out's
+// columns, and computes t for itself: a wave takes every eighth rank, its lanes eight of k at a time.  The row's
+// workgroups lie on one die (workgroups go round the eight dies), so that a is read into one cache.  Of b, as many
+// lanes as a row of it has pieces of eight ranks (the next power of two) share a column; its first pieces and base are
+// requested before t is known.
+constexpr int kRowWaves = 8, kRowCols = 2048, kRowAhead = 8;
+template <bool F32>
+__global__ __launch_bounds__(64 * kRowWaves) void adapters_row_kernel(AdapterArgs a, int log_pieces) {
+  __shared__ float ts[256], sums[kRowCols];
+  const situ_moe_adapters_t& p = a.p;
+  const int lane = lane_id(), wave = wave_id();
+  const int slot = blockIdx.x / 8, row = slot / a.chunks * 8 + blockIdx.x % 8, chunk = slot % a.chunks;
+  if (row >= p.rows) return;
+  const int c0 = chunk * a.run, c1 = min(c0 + a.run, p.n);       // run: columns of a workgroup
+  // base: eight columns a thread
+  const int cb = c0 + 8 * (int)threadIdx.x;
+  constexpr int NB = F32 ? 2 : 1;
+  uint4 base[NB];
+#pragma unroll
+  for (int h = 0; h < NB; ++h)
+    base[h] = load16(static_cast<const char*>(p.base) + ((int64_t)row * p.base_stride + cb) * (F32 ? 4 : 2) + 16 * h, p.base && cb < c1);
+  // x: eight of k a lane and piece
+  const uint16_t* xr = p.x + (int64_t)row * p.x_stride;
+  uint4 x[kRowAhead];
+#pragma unroll
+  for (int o = 0; o < kRowAhead; ++o) x[o] = load16(xr + 8 * (lane + kWave * o), 8 * (lane + kWave * o) < p.k);
+  Requests q;
+  uint64_t some = 0;
+  for (int first = first_request(p, row, lane);; first += 64) {
+    load_requests(p, first, lane, q);
+    some = in_tile(q, row, row + 1);
+    if (some || !reaches_on(p, q, row + 1)) break;
+  }
+  if (!some) return;                                 // of no request
+  const int i = __builtin_amdgcn_readlane(q.adapter, next_bit(some));
+  const bool adapted = i >= 0;
+  const int rank = !adapted ? 0 : p.ranks ? min(max(p.ranks[i], 0), p.rank) : p.rank;
+  if (rank > 0) {
+    const int pieces = 1 << log_pieces, mine = lane & (pieces - 1), cols = kWave >> log_pieces;
+    const uint16_t* b = p.b + (int64_t)i * p.n * p.rank + 8 * mine;
+    const int step = kRowWaves * cols, cw = c0 + wave * cols + (lane >> log_pieces);
+    uint4 ahead[kRowAhead];
+#pragma unroll
+    for (int o = 0; o < kRowAhead; ++o)
+      ahead[o] = load16(b + (int64_t)(cw + o * step) * p.rank, 8 * mine < rank && cw + o * step < c1);
+    __builtin_amdgcn_sched_barrier(0);
+    const float scale = p.scales ? p.scales[i] : 1.0f;
+    const uint16_t* w = p.a + (int64_t)i * p.rank * p.k;
+    for (int r = wave; r < p.rank; r += 2 * kRowWaves) {
+      const bool two = r + kRowWaves < rank;
+      const uint16_t* w0 = w + (int64_t)r * p.k;
+      const uint16_t* w1 = w0 + (two ? (int64_t)kRowWaves * p.k : 0);
+      float s0 = 0.0f, s1 = 0.0f;
+      for (int k0 = 0; k0 < p.k; k0 += 8 * kWave * kRowAhead) {
+        uint4 v0[kRowAhead], v1[kRowAhead];
+#pragma unroll
+        for (int o = 0; o < kRowAhead; ++o) {
+          const int k = k0 + 8 * (lane + kWave * o);
+          v0[o] = load16(w0 + k, k < p.k);
+          v1[o] = load16(w1 + k, k < p.k);
+        }
+#pragma unroll
+        for (int o = 0; o < kRowAhead; ++o) {
+          const int k = k0 + 8 * (lane + kWave * o);
+          float fx[8], f0[8], f1[8];
+          unpack8(k0 == 0 ? x[o] : load16(xr + k, k < p.k), fx);
+          unpack8(v0[o], f0);
+          unpack8(v1[o], f1);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            s0 = fmaf(fx[e], f0[e], s0);
+            s1 = fmaf(fx[e], f1[e], s1);
+          }
+        }
+      }
+      s0 = wave_sum(s0);
+      s1 = wave_sum(s1);
+      if (lane == 0) {
+        ts[r] = r < rank ? s0 * scale : 0.0f;
+        if (r + kRowWaves < p.rank) ts[r + kRowWaves] = two ? s1 * scale : 0.0f;
+      }
+    }
+    __syncthreads();
+    float t[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) t[e] = 8 * mine + e < rank ? ts[8 * mine + e] : 0.0f;
+    auto finish = [&](const uint4& v, int c) {
+      float f[8], s = 0.0f;
+      unpack8(v, f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s = 8 * mine + e < rank ? fmaf(f[e], t[e], s) : s;
+      for (int m = 1; m < pieces; m *= 2) s += __shfl_xor(s, m, kWave);
+      if (mine == 0 && c < c1) sums[c - c0] = s;
+    };
+#pragma unroll
+    for (int o = 0; o < kRowAhead; ++o)
+      if (c0 + wave * cols + o * step < c1) finish(ahead[o], cw + o * step);
+    for (int c = cw + kRowAhead * step; c - (lane >> log_pieces) < c1; c += step)
+      finish(load16(b + (int64_t)c * p.rank, 8 * mine < rank && c < c1), c);
+    __syncthreads();
+  }
+  if (cb >= c1) return;
+  float f[8];
+  if constexpr (F32) {
+    const uint32_t u[8] = {base[0].x, base[0].y, base[0].z, base[0].w, base[NB - 1].x, base[NB - 1].y, base[NB - 1].z, base[NB - 1].w};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(u[e]);
+  } else {
+    unpack8(base[0], f);
+  }
+  if (rank > 0) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] += sums[cb - c0 + e];
+  }
+  if constexpr (F32) {
+    float* o = static_cast<float*>(p.out) + (int64_t)row * p.out_stride + cb;
+    *reinterpret_cast<f32x4*>(o) = f32x4{f[0], f[1], f[2], f[3]};
+    *reinterpret_cast<f32x4*>(o + 4) = f32x4{f[4], f[5], f[6], f[7]};
+  } else {
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + (int64_t)row * p.out_stride + cb) = pack8(f);
   }
 }
 
 // Few rows: a row a tile, as decode's requests have one each; else whole tiles.
-int tile_rows(int32_t rows) { return rows <= 64 ? 1 : rows <= 256 ? 4 : 16; }
+int up_tile_rows(int32_t rows) { return rows <= 64 ? 1 : rows <= 256 ? 4 : 16; }
+int down_tile_rows(int32_t rows, int32_t rank) { return rows <= 2048 || rank > 64 ? up_tile_rows(rows) : 32; }
+
+// The one launch reads an adapter's a for each row and share of its columns, from its die's cache.
+bool row_by_row(int32_t rows, int32_t k, int32_t rank) { return rows <= 64 && (int64_t)rank * k <= 1 << 17; }
 
 template <bool F32>
 void up_go(const AdapterArgs& a, int64_t items, hipStream_t s) {
-  const dim3 grid((unsigned)((items + kWaves - 1) / kWaves)), threads(64 * kWaves);
+  const dim3 grid((unsigned)((items + kUpWaves - 1) / kUpWaves)), threads(64 * kUpWaves);
   const int r = a.p.rank;
   if (r <= 16) hipLaunchKernelGGL((adapters_up_kernel<0, F32>), grid, threads, 0, s, a, items);
   else if (r <= 32) hipLaunchKernelGGL((adapters_up_kernel<1, F32>), grid, threads, 0, s, a, items);
@@ -308,34 +502,51 @@ void up_go(const AdapterArgs& a, int64_t items, hipStream_t s) {
 
 }  // namespace
 
-int adapters_parts(int32_t rows, int32_t k, int32_t rank) {
-  (void)rank;
-  const int tiles = (rows + tile_rows(rows) - 1) / tile_rows(rows), units = (k + 63) / 64;
-  return std::max(1, std::min({512 / std::max(tiles, 1), units / kWaves, 16}));
+uint64_t adapters_workspace_bytes(int32_t rows, int32_t k, int32_t rank) {
+  return row_by_row(rows, k, rank) ? 0 : 4ull * (uint64_t)rows * (uint64_t)rank;
 }
 
 hipError_t launch_adapters(const situ_moe_adapters_t& p, hipStream_t s) {
   AdapterArgs a{};
   a.p = p;
-  a.t = static_cast<float*>(p.workspace);
-  a.tile = tile_rows(p.rows);
-  a.tiles = (p.rows + a.tile - 1) / a.tile;
-  a.parts = adapters_parts(p.rows, p.k, p.rank);
-  const dim3 grid((unsigned)(a.tiles * a.parts)), threads(64 * kWaves);
   const int r = p.rank;
-  if (r <= 16) hipLaunchKernelGGL(adapters_down_kernel<1>, grid, threads, 0, s, a);
-  else if (r <= 32) hipLaunchKernelGGL(adapters_down_kernel<2>, grid, threads, 0, s, a);
-  else if (r <= 64) hipLaunchKernelGGL(adapters_down_kernel<4>, grid, threads, 0, s, a);
-  else if (r <= 128) hipLaunchKernelGGL(adapters_down_kernel<8>, grid, threads, 0, s, a);
-  else hipLaunchKernelGGL(adapters_down_kernel<16>, grid, threads, 0, s, a);
+  if (row_by_row(p.rows, p.k, r)) {
+    // workgroups of a row: 256 in all, each 256 to 2048 columns
+    const int eights = (p.rows + 7) / 8;
+    const int most = (p.n + 255) / 256, least = (p.n + kRowCols - 1) / kRowCols;
+    a.chunks = std::max(least, std::min(most, 32 / eights));
+    a.run = ((p.n + a.chunks - 1) / a.chunks + 7) / 8 * 8;
+    a.chunks = (p.n + a.run - 1) / a.run;
+    int log_pieces = 0;
+    while (8 << log_pieces < r) ++log_pieces;
+    const dim3 grid((unsigned)(eights * 8 * a.chunks)), threads(64 * kRowWaves);
+    if (p.out_dtype == SITU_OUT_F32) hipLaunchKernelGGL(adapters_row_kernel<true>, grid, threads, 0, s, a, log_pieces);
+    else hipLaunchKernelGGL(adapters_row_kernel<false>, grid, threads, 0, s, a, log_pieces);
+    return hipGetLastError();
+  }
+  a.high = static_cast<uint16_t*>(p.workspace);
+  a.low = a.high + (int64_t)p.rows * r;
+  a.up_tile = up_tile_rows(p.rows);
+  a.tile = down_tile_rows(p.rows, r);
+  const dim3 grid((unsigned)((p.rows + a.tile - 1) / a.tile));
+  if (a.tile > 16) {
+    if (r <= 16) hipLaunchKernelGGL((adapters_down_kernel<1, 2, 4, 8>), grid, dim3(512), 0, s, a);
+    else if (r <= 32) hipLaunchKernelGGL((adapters_down_kernel<2, 2, 3, 8>), grid, dim3(512), 0, s, a);
+    else hipLaunchKernelGGL((adapters_down_kernel<4, 2, 1, 8>), grid, dim3(512), 0, s, a);
+  } else {
+    if (r <= 16) hipLaunchKernelGGL((adapters_down_kernel<1, 1, 2, 16>), grid, dim3(1024), 0, s, a);
+    else if (r <= 32) hipLaunchKernelGGL((adapters_down_kernel<2, 1, 3, 8>), grid, dim3(512), 0, s, a);
+    else if (r <= 64) hipLaunchKernelGGL((adapters_down_kernel<4, 1, 2, 8>), grid, dim3(512), 0, s, a);
+    else if (r <= 128) hipLaunchKernelGGL((adapters_down_kernel<8, 1, 1, 8>), grid, dim3(512), 0, s, a);
+    else hipLaunchKernelGGL((adapters_down_kernel<16, 1, 1, 4>), grid, dim3(256), 0, s, a);
+  }
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  // columns of a wave: as many as leave 8192 waves
-  const int blocks = (p.n + 63) / 64;
-  const int64_t per = std::max<int64_t>(1, (int64_t)a.tiles * blocks / 8192);
-  a.cols = (int)std::min<int64_t>(per, blocks) * 64;
-  a.chunks = (p.n + a.cols - 1) / a.cols;
-  const int64_t items = (int64_t)a.tiles * a.chunks;
+  a.up_tiles = (p.rows + a.up_tile - 1) / a.up_tile;
+  a.chunks = (p.n + 127) / 128;
+  // tiles of a wave: as many as leave 3072 waves, three a SIMD
+  a.run = (int)std::min<int64_t>(std::max<int64_t>(1, ((int64_t)a.up_tiles * a.chunks + 3071) / 3072), a.up_tiles);
+  const int64_t items = (int64_t)((a.up_tiles + a.run - 1) / a.run) * a.chunks;
   if (p.out_dtype == SITU_OUT_F32) up_go<true>(a, items, s);
   else up_go<false>(a, items, s);
   return hipGetLastError();

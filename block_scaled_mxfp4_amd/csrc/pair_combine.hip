@@ -78,7 +78,7 @@ __device__ __forceinline__ int next_bit(uint64_t& m) {
 template <bool YF, bool OF>
 __global__ __launch_bounds__(64 * kWaves) void pair_combine_kernel(situ_moe_combine_t p, int parts, int64_t items) {
   const int lane = lane_id();
-  for (int64_t item = (int64_t)blockIdx.x * kWaves + threadIdx.x / kWave; item < items; item += (int64_t)gridDim.x * kWaves) {
+  for (int64_t item = (int64_t)blockIdx.x * kWaves + wave_id(); item < items; item += (int64_t)gridDim.x * kWaves) {
     const int64_t t = (uint32_t)item / (uint32_t)parts;
     const int col = (int)(item - t * parts) * kCols + 8 * lane;
     const bool in = col < p.hidden;
@@ -121,7 +121,7 @@ template <bool YF, bool OF>
 __global__ __launch_bounds__(64 * kWaves) void pair_combine_backward_kernel(situ_moe_combine_t p, int slots, int parts,
                                                                             int64_t items) {
   const int lane = lane_id();
-  for (int64_t item = (int64_t)blockIdx.x * kWaves + threadIdx.x / kWave; item < items; item += (int64_t)gridDim.x * kWaves) {
+  for (int64_t item = (int64_t)blockIdx.x * kWaves + wave_id(); item < items; item += (int64_t)gridDim.x * kWaves) {
     const int64_t t = (uint32_t)item / (uint32_t)parts;
     const int first = (int)(item - t * parts) * slots, end = min(first + slots, p.top_k);
     int row;

@@ -6,23 +6,29 @@
 
 namespace situ {
 
-// x / s correctly rounded where it counts: q = x * rcp(s) is within two ulp, and
-// one correction by the remainder x - q s lands on the nearest fp32.  Only in
-// blocks with a maximum below 2^-98 can the remainder of an element 2^13 or more
-// below it leave the normal range, and the quotient be an ulp off; its E4M3 code
-// is the same (every pair of bf16 mantissas at 22 exponent distances, in
-// rational arithmetic).  A block with an infinity has scale inf and codes
-// of NaN; a NaN element gives NaN and leaves the block's scale to the others.
+// x / s as far as its E4M3 code goes: q = x r with r = rcp(s) within an ulp, and one
+// correction by the remainder x - q s.  The quotient of bf16 values and block
+// maxima lies 2^-13 from every midpoint between two codes unless it is one, and at
+// the midpoints the corrected value rounds as the exactly divided one (all 1449
+// pairs of mantissas and distances, r an ulp off to either side, in rational
+// arithmetic).  A block with an infinity has scale inf and codes of NaN; a NaN
+// element gives NaN and leaves the block's scale to the others.
 __device__ __forceinline__ float quotient(float x, float s, float r) {
   const float q = x * r;
   return fmaf(fmaf(-q, s, x), r, q);
 }
 
-__device__ __forceinline__ float block_scale(float amax) { return fmaxf(amax, 0x1p-100f) / 448.0f; }
+// max(amax, 2^-100) / 448, rounded as a division is (every bf16 mantissa, in rational arithmetic).
+__device__ __forceinline__ float block_scale(float amax) {
+  constexpr float kR = 1.0f / 448.0f;
+  amax = fmaxf(amax, 0x1p-100f);
+  const float q = amax * kR, s = fmaf(fmaf(-q, 448.0f, amax), kR, q);
+  return amax < __builtin_inff() ? s : amax;
+}
 
 // Codes of eight elements of a block with scale s.
 __device__ __forceinline__ uint2 block_codes(const float f[8], float s) {
-  const float r = 1.0f / s;
+  const float r = __builtin_amdgcn_rcpf(s);
   uint32_t o[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {

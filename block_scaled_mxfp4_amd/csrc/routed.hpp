@@ -31,12 +31,8 @@ hipError_t launch_pair_combine(const situ_moe_combine_t& a, hipStream_t s);
 hipError_t launch_pair_combine_backward(const situ_moe_combine_t& a, hipStream_t s);
 
 // ---- the adapters
-// Parts k is split into by the first product, each with partial sums of its own:
-// [parts][rows][rank] floats of workspace.
-int adapters_parts(int32_t rows, int32_t k, int32_t rank);
-inline uint64_t adapters_workspace_bytes(int32_t rows, int32_t k, int32_t rank) {
-  return 4ull * (uint64_t)adapters_parts(rows, k, rank) * (uint64_t)rows * (uint64_t)rank;
-}
+// Workspace: two bf16 terms of t a row and rank; none where one launch does it all.
+uint64_t adapters_workspace_bytes(int32_t rows, int32_t k, int32_t rank);
 hipError_t launch_adapters(const situ_moe_adapters_t& a, hipStream_t s);
 
 }  // namespace situ

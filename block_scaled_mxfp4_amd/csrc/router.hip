@@ -4,17 +4,18 @@
 // A wave takes a token at a time and holds its logits in registers, V J of them
 // a lane: expert e = 64 V j + V lane + v.
 //
-// Choice without sorting.  Logits map to ascending unsigned keys; at least top_k
-// of the 64 lanes' largest keys reach a threshold, so the top_k largest keys of
-// all do, and a bisection on the lanes' largest finds one that few more do.  What
+// Choice without sorting.  Where top_k of the 64 lanes' largest logits reach a
+// threshold, the top_k largest of all do; a bisection on the lanes' largest finds
+// one that few more do.  What
 // reaches it (some 1.3 top_k) is packed into LDS, one candidate a lane, and a
 // candidate's place is the number of candidates before it.  Where more than 64
 // reach it (many equals; top_k near 64), the wave takes its largest remaining
 // key top_k times instead.
 //
 // A selection by sigmoid + bias is compared in 64 bits, since the neighbours of
-// 900 experts lie as near as fp32 rounds.  Only the candidates are: the threshold
-// is taken on fp32 keys and lowered by more than twice their error.
+// 900 experts lie as near as fp32 rounds.  The threshold is taken on fp32 scores and
+// lowered by more than twice their error, and only where two candidates are nearer
+// than that are the candidates' scores computed again in 64 bits.
 //
 // Sigmoid scores are held divided by e^min(zmax, 0), which leaves their shares as
 // they are: a row whose scores all underflow keeps its weights.
@@ -35,7 +36,8 @@ namespace {
 
 constexpr float kL2e = 1.44269502162933349609375f;   // log2(e) rounded to fp32
 constexpr int kRouterWaves = 8;                       // of a workgroup
-constexpr int kRouterBlocks = 1024;                   // workgroups at most
+constexpr int kRouterBlocks = 768;                    // workgroups at most where the loss is taken
+constexpr int kBackWaves = 8;
 constexpr int kOneBlockTokens = 32;                   // up to here one workgroup finishes the loss by itself
 
 // Keys ascend with the values; 0 is an expert that cannot be chosen (-inf, NaN).
@@ -47,20 +49,25 @@ __device__ __forceinline__ uint32_t key_of(float z) {
 __device__ __forceinline__ float value_of(uint32_t k) {
   return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
 }
+// The same order with a place for -inf; NaN must not be given.
+__device__ __forceinline__ uint32_t order_of(float z) {
+  const uint32_t u = __float_as_uint(z);
+  return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float wave_most(float z) { return value_of(wave_max(order_of(z))); }
 __device__ __forceinline__ uint64_t key_of(double x) {
   const uint64_t u = __builtin_bit_cast(uint64_t, x + 0.0);
   return u ^ ((uint64_t)((int64_t)u >> 63) | 0x8000000000000000ull);
 }
 
-// LDS that other lanes of the wave read or wrote: in order, once the compiler keeps it so.
-__device__ __forceinline__ void wave_lds() {
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-}
-
 __device__ __forceinline__ float e_to(float x) { return __builtin_amdgcn_exp2f(x * kL2e); }
 
-// The logits of a row, NaN-free where there is none to load (-inf).
+template <bool BF>
+__device__ __forceinline__ float load_one(const void* logits, int64_t at) {
+  return BF ? bf16_to_f32(static_cast<const uint16_t*>(logits)[at]) : static_cast<const float*>(logits)[at];
+}
+
+// The logits of a row, -inf past the last expert.
 template <bool BF, int V, int J>
 __device__ __forceinline__ void load_row(const void* logits, int64_t at, int lane, int experts, bool vec, float z[V * J]) {
 #pragma unroll
@@ -84,18 +91,34 @@ __device__ __forceinline__ void load_row(const void* logits, int64_t at, int lan
     for (int v = 0; v < V; ++v) {
       z[V * j + v] = -__builtin_inff();
       if (e + v < experts)
-        z[V * j + v] = BF ? bf16_to_f32(static_cast<const uint16_t*>(logits)[at + e + v])
-                          : static_cast<const float*>(logits)[at + e + v];
+        z[V * j + v] = load_one<BF>(logits, at + e + v);
     }
   }
 }
 
 // Scores of a row, up to a factor the whole row shares: e^(z - zmax), or
-// sigmoid(z) e^-min(zmax, 0).
-__device__ __forceinline__ float score(bool sigmoid, float z, float shift) {
-  // the difference first: a row of the type's lowest value has a finite one
-  if (!sigmoid) return e_to(z - shift);
-  return e_to(fminf(z, 0.0f) - shift) * __builtin_amdgcn_rcpf(1.0f + e_to(-fabsf(z)));
+// sigmoid(z) e^-min(zmax, 0).  FAR: the shift is next to the type's lowest value,
+// where its product with log2 e overflows; the difference is taken first.
+template <bool SIG, bool FAR>
+__device__ __forceinline__ float score(float z, float shift) {
+  const float x = SIG ? fminf(z, 0.0f) : z;
+  const float n = FAR ? e_to(x - shift) : __builtin_amdgcn_exp2f(fmaf(x, kL2e, -shift * kL2e));
+  return SIG ? n * __builtin_amdgcn_rcpf(1.0f + e_to(-fabsf(z))) : n;
+}
+__device__ __forceinline__ bool is_far(float shift) { return fabsf(shift) > 0x1p100f; }
+template <bool SIG>
+__device__ __forceinline__ float score(float z, float shift) {
+  return is_far(shift) ? score<SIG, true>(z, shift) : score<SIG, false>(z, shift);
+}
+template <bool SIG, int N>
+__device__ __forceinline__ void scores(const float z[N], float shift, float s[N]) {
+  if (is_far(shift)) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) s[i] = score<SIG, true>(z[i], shift);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) s[i] = score<SIG, false>(z[i], shift);
+  }
 }
 
 struct RouterArgs {
@@ -106,23 +129,44 @@ struct RouterArgs {
   uint32_t* ticket;
 };
 
-// Candidates of a wave, or a row by expert.
-struct Candidates {
-  uint64_t key[64];
-  float z[64];
+__device__ __forceinline__ uint64_t readlane64(uint64_t v, int lane) {
+  return (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(v >> 32), lane) << 32 |
+         (uint32_t)__builtin_amdgcn_readlane((int)v, lane);
+}
+
+// A wave's row of logits by expert, and the candidates' ids.  The row's place takes the scores in 64 bits where more
+// than 64 candidates ask for them.
+template <int N, bool BIAS>
+struct WaveRow {
+  union {
+    float z[64 * N];
+    uint64_t wide[BIAS ? 64 * N : 1];
+  };
   int32_t id[64];
 };
 
+// The logits of token t; -inf for a masked one and past the last.
+template <bool BF, int V, int J>
+__device__ __forceinline__ void load_token(const situ_moe_router_t& p, int64_t t, int lane, bool vec, float z[V * J]) {
+  if (t < p.tokens && (!p.mask || p.mask[t])) {
+    load_row<BF, V, J>(p.logits, t * p.logits_stride, lane, p.experts, vec, z);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V * J; ++i) z[i] = -__builtin_inff();
+  }
+}
+
 template <bool BF, int V, int J, bool SIG, bool BIAS, bool BAL>
-__global__ __launch_bounds__(64 * kRouterWaves) void router_kernel(RouterArgs a) {
+__global__ __launch_bounds__(64 * kRouterWaves, 4) void router_kernel(RouterArgs a) {
   constexpr int N = V * J;
-  __shared__ Candidates cands[kRouterWaves];
+  __shared__ WaveRow<N, BIAS> wave_rows[kRouterWaves];
+  __shared__ float biases[BIAS ? 64 * N : 1];
   __shared__ float sums[BAL ? 64 * N : 1];
   __shared__ int32_t hits[BAL ? 64 * N : 1];
   const situ_moe_router_t& p = a.p;
-  const int lane = lane_id(), wave = threadIdx.x / kWave;
+  const int lane = lane_id(), wave = wave_id();
   const int experts = p.experts, top_k = p.top_k;
-  Candidates& cd = cands[wave];
+  WaveRow<N, BIAS>& cd = wave_rows[wave];
   float acc[BAL ? N : 1];
   if constexpr (BAL) {
 #pragma unroll
@@ -137,153 +181,160 @@ __global__ __launch_bounds__(64 * kRouterWaves) void router_kernel(RouterArgs a)
     for (int i = 0; i < N; ++i) {
       const int e = 64 * V * (i / V) + V * lane + i % V;
       bias[i] = e < experts ? p.bias[e] : 0.0f;
+      if (wave == 0) biases[e] = bias[i];
     }
+    __syncthreads();
   }
   const int64_t step = (int64_t)gridDim.x * kRouterWaves;
   for (int64_t t = (int64_t)blockIdx.x * kRouterWaves + wave; t < p.tokens; t += step) {
     const int64_t row = t * top_k;
-    uint32_t best = 0, k32[N];
-    float z[N];
-    if (!p.mask || p.mask[t]) {
-      load_row<BF, V, J>(p.logits, t * p.logits_stride, lane, experts, a.vec, z);
+    float z[N], best = -__builtin_inff();
+    load_token<BF, V, J>(p, t, lane, a.vec, z);
+#pragma unroll
+    for (int i = 0; i < N; ++i) best = fmaxf(best, z[i]);     // passes over NaN
+    const float zmax = wave_most(best);
+    const bool live = zmax > -__builtin_inff();      // the row has an expert to choose
+    // what is compared: the logit, or the fp32 score with its bias
+    float c[BIAS ? N : 1], top = zmax;
+    if constexpr (BIAS) {
+      best = -__builtin_inff();
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        k32[i] = key_of(z[i]);
-        best = max(best, k32[i]);
+        c[i] = z[i] > -__builtin_inff() ? __builtin_amdgcn_rcpf(1.0f + e_to(-z[i])) + bias[i] : -__builtin_inff();
+        best = fmaxf(best, c[i]);
       }
-    } else {
-#pragma unroll
-      for (int i = 0; i < N; ++i) { z[i] = -__builtin_inff(); k32[i] = 0; }
+      top = wave_most(best);
     }
-    const uint32_t top = wave_max(best);
-    const float zmax = value_of(top);
-    const bool live = top != 0;                      // the row has an expert to choose
-    if constexpr (BIAS) {
-      best = 0;
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const float o = __builtin_amdgcn_rcpf(1.0f + e_to(-z[i]));
-        k32[i] = k32[i] ? key_of(o + bias[i]) : 0u;
-        best = max(best, k32[i]);
+    // a threshold that top_k of the lanes' largest reach (all lanes' that have an expert do reach the least of
+    // them), or the lowest value of all: every expert that can be chosen
+    float least = -3.40282347e38f;
+    const bool some = best > -__builtin_inff();
+    if (__popcll(__ballot(some)) >= top_k) {
+      uint32_t lo = key_of(-wave_most(some ? -best : -__builtin_inff())), hi = key_of(top);
+      while (hi > lo + 1) {
+        const uint32_t mid = lo + (hi - lo) / 2;
+        const int n = __popcll(__ballot(best >= value_of(mid)));
+        if (n >= top_k) {
+          lo = mid;
+          if (n <= top_k + 8) break;
+        } else {
+          hi = mid;
+        }
       }
+      least = fmaxf(value_of(lo), least);
+      // the k-th largest fp32 score is `least` at the least; one is off by less than 2^-21 + 2^-23 of its magnitude
+      if (BIAS && least < __builtin_inff()) least = fmaxf(least - 0x1p-19f * (1.0f + fabsf(least)), -3.40282347e38f);
     }
-    // a threshold that top_k of the lanes' largest keys reach, or 1: every expert that can be chosen
-    uint32_t lo = 1, hi = (BIAS ? wave_max(best) : top);
-    while (live && hi > lo + 1) {
-      const uint32_t mid = lo + (hi - lo) / 2;
-      const int n = __popcll(__ballot(best >= mid));
-      if (n >= top_k) {
-        lo = mid;
-        if (n <= top_k + 8) break;
-      } else {
-        hi = mid;
-      }
-    }
-    if constexpr (BIAS) {
-      // the k-th largest fp32 key is lo at least; an fp32 key is off by less than 2^-21 + 2^-23 |key|
-      const float f = value_of(lo);
-      if (lo > 1 && f < __builtin_inff()) lo = max(key_of(f - 0x1p-19f * (1.0f + fabsf(f))), 1u);
-    }
-    int n = 0;
+    // a lane's candidates as bits, the first the highest; then one of each lane at a time into LDS
+    uint32_t mine = 0;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const uint64_t in = __ballot(k32[i] >= lo);
-      if (in) {
-        const int at = n + (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(in >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)in, 0));
-        if (k32[i] >= lo && at < 64) {
-          const int e = 64 * V * (i / V) + V * lane + i % V;
-          cd.z[at] = z[i];
-          cd.id[at] = e;
-          if constexpr (BIAS)
-            cd.key[at] = __builtin_bit_cast(uint64_t, (double)bias[i]);
-          else
-            cd.key[at] = ((uint64_t)k32[i] << 32) | (uint32_t)(~e);
-        }
-        n += __popcll(in);
-      }
+      mine = mine + mine + ((BIAS ? c[BIAS ? i : 0] : z[i]) >= least ? 1u : 0u);
+      cd.z[64 * V * (i / V) + V * lane + i % V] = z[i];
+    }
+    int n = 0;
+    for (uint64_t who = __ballot(mine != 0); who; who = __ballot(mine != 0)) {
+      const int at = (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(who >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)who, n));
+      const uint32_t i = N - 1 - (uint32_t)__builtin_ctz(mine | 0x80000000u);
+      if (mine && at < 64) cd.id[at] = 64 * V * (i / V) + V * lane + i % V;
+      mine &= mine - 1;
+      n += __popcll(who);
     }
     wave_lds();
     int id = -1, place = lane;                       // a lane's expert and its place in the row
     float zc = 0.0f;
     if (n <= 64) {
-      uint64_t key = 0;
       if (lane < n) {
         id = cd.id[lane];
-        zc = cd.z[lane];
-        key = cd.key[lane];
-        if constexpr (BIAS) key = key_of(1.0 / (1.0 + exp(-(double)zc)) + __builtin_bit_cast(double, key));
+        zc = cd.z[id];
       }
       int before = 0;
-      for (int c = 0; c < n; ++c) {
-        const uint64_t other = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(key >> 32), c) << 32 |
-                               (uint32_t)__builtin_amdgcn_readlane((int)key, c);
-        if constexpr (BIAS) {
-          const int oid = __builtin_amdgcn_readlane(id, c);
-          before += other > key || (other == key && oid < id);
-        } else {
-          before += other > key;
+      if constexpr (BIAS) {
+        // fp32 tells all of them apart but for a token in some hundreds
+        const float b = lane < n ? biases[id] : 0.0f;
+        const float mine = __builtin_amdgcn_rcpf(1.0f + e_to(-zc)) + b, apart = 0x1p-19f * (1.0f + fabsf(mine));
+        int near = 0;
+        for (int o = 0; o < n; ++o) {
+          const float other = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, mine), o));
+          before += other > mine;
+          near += !(fabsf(other - mine) > apart);    // itself, and infinities, too
+        }
+        if (__ballot(lane < n && near > 1)) {
+          const uint64_t key = key_of(1.0 / (1.0 + exp(-(double)zc)) + (double)b);
+          before = 0;
+          for (int o = 0; o < n; ++o) {
+            const uint64_t other = readlane64(key, o);
+            const int oid = __builtin_amdgcn_readlane(id, o);
+            before += other > key || (other == key && oid < id);
+          }
+        }
+      } else {
+        // fp32 logits are hardly ever equal, bf16 ones often; equal ones leave places double and others empty
+        const float key = lane < n ? zc : -__builtin_inff();
+        if (!BF)
+          for (int o = 0; o < n; ++o)
+            before += __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, key), o)) > key;
+        if (BF || wave_sum(lane < n ? (float)before : 0.0f) != 0.5f * (float)(n * (n - 1))) {
+          const uint64_t key64 = (uint64_t)key_of(zc) << 32 | (uint32_t)~id;
+          before = 0;
+          for (int o = 0; o < n; ++o) before += readlane64(key64, o) > key64;
         }
       }
       if (lane < n) place = before;
     } else {
-      // the largest left, top_k times
-      uint64_t k64[N];
+      // the largest left, top_k times: the largest behind the last one in the order of (key, lowest id)
+      if constexpr (BIAS) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        if constexpr (BIAS)
-          k64[i] = k32[i] ? key_of(1.0 / (1.0 + exp(-(double)z[i])) + (double)bias[i]) : 0;
-        else
-          k64[i] = k32[i];
+        for (int i = 0; i < N; ++i)
+          cd.wide[BIAS ? 64 * i + lane : 0] =
+              c[BIAS ? i : 0] > -__builtin_inff() ? key_of(1.0 / (1.0 + exp(-(double)z[i])) + (double)bias[BIAS ? i : 0]) : 0;
       }
-      for (int c = 0; c < top_k; ++c) {
-        uint64_t mine = 0;
-        int which = 0;
-#pragma unroll
-        for (int i = 0; i < N; ++i)                  // ascending ids: the first of equals stays
-          if (k64[i] > mine) { mine = k64[i]; which = i; }
-        const uint32_t h = wave_max((uint32_t)(mine >> 32));
-        const uint32_t l = wave_max((uint32_t)(mine >> 32) == h ? (uint32_t)mine : 0u);
-        const uint64_t largest = (uint64_t)h << 32 | l;
-        if (!largest) break;
-        const int e = 64 * V * (which / V) + V * lane + which % V;
-        const uint32_t first = ~wave_max(mine == largest ? ~(uint32_t)e : 0u);
-        if (mine == largest && e == (int)first) {
-#pragma unroll
-          for (int i = 0; i < N; ++i)
-            if (i == which) { k64[i] = 0; cd.z[c] = z[i]; }
+      wave_lds();
+      uint64_t last = ~0ull;
+      int last_id = -1;
+      for (int o = 0; o < top_k; ++o) {
+        uint64_t most = 0;
+        int at = 0;
+#pragma unroll 1
+        for (int i = 0; i < N; ++i) {                // ascending ids: the first of equals stays
+          const int e = 64 * V * (i / V) + V * lane + i % V;
+          const uint64_t k = BIAS ? cd.wide[BIAS ? 64 * i + lane : 0] : (uint64_t)key_of(cd.z[e]);
+          if (k > most && (k < last || (k == last && e > last_id))) { most = k; at = e; }
         }
-        wave_lds();
-        if (lane == c) { id = (int)first; zc = cd.z[c]; }
+        const uint32_t h = BIAS ? wave_max((uint32_t)(most >> 32)) : 0u;
+        const uint32_t l = wave_max((uint32_t)(most >> 32) == h ? (uint32_t)most : 0u);
+        last = (uint64_t)h << 32 | l;
+        if (!last) break;
+        last_id = (int)~wave_max(most == last ? ~(uint32_t)at : 0u);
+        if (lane == o) id = last_id;
       }
+      if (id >= 0) zc = load_one<BF>(p.logits, t * p.logits_stride + id);
     }
     const bool chosen = id >= 0 && place < top_k;
     // renormalized weights are shares of the chosen: their own largest is the one to be near
     float wshift = SIG ? 0.0f : zmax;
-    if (SIG && p.renormalize) wshift = fminf(BIAS ? value_of(wave_max(chosen ? key_of(zc) : 0u)) : zmax, 0.0f);
-    float w = chosen ? score(SIG, zc, wshift) : 0.0f;
+    if (SIG && p.renormalize) wshift = fminf(BIAS ? wave_most(chosen ? zc : -__builtin_inff()) : zmax, 0.0f);
+    float w = chosen ? score<SIG>(zc, wshift) : 0.0f;
     float all = 0.0f;
-    if (BAL || (!SIG && !p.renormalize)) {
+    if (live && (BAL || (!SIG && !p.renormalize))) {
       float s[N];
-      if (live) {
+      scores<SIG, N>(z, SIG ? fminf(zmax, 0.0f) : zmax, s);
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          s[i] = score(SIG, z[i], SIG ? fminf(zmax, 0.0f) : zmax);
-          all += s[i];
-        }
-        all = wave_sum(all);
-        if constexpr (BAL) {
-          const float r = 1.0f / all;
+      for (int i = 0; i < N; ++i) all += s[i];
+      all = wave_sum(all);
+      if constexpr (BAL) {
+        const float r = __builtin_amdgcn_rcpf(all);
 #pragma unroll
-          for (int i = 0; i < N; ++i) acc[i] = fmaf(s[i], r, acc[i]);
-          if (chosen) atomicAdd(&hits[id], 1);
-        }
+        for (int i = 0; i < N; ++i) acc[i] = fmaf(s[i], r, acc[i]);
+        if (chosen) atomicAdd(&hits[id], 1);
       }
     }
     const float total = p.renormalize ? wave_sum(w) : (SIG ? 1.0f : all);
     w = chosen ? p.scale * (w / total) : 0.0f;
-    if (chosen || (lane >= n && lane < top_k && n <= 64) || (n > 64 && lane < top_k)) {
+    // the lanes behind the candidates fill the places that none has
+    if (chosen || (lane < top_k && (n > 64 || lane >= n))) {
       const int64_t at = row + place;
-      if (p.ids) p.ids[at] = id;
+      p.ids[at] = id;
       const uint32_t b = f32_to_bf16_rne(w);
       if (p.weights) {
         if (p.weights_dtype == SITU_OUT_F32)
@@ -309,53 +360,61 @@ __global__ __launch_bounds__(64 * kRouterWaves) void router_kernel(RouterArgs a)
     int32_t* co = alone ? p.counts : a.part_count + (int64_t)blockIdx.x * experts;
     for (int e = threadIdx.x; e < experts; e += 64 * kRouterWaves) { so[e] = sums[e]; co[e] = hits[e]; }
     if (alone && wave == 0) {
-      float c = 0.0f, d = 0.0f;
+      float n = 0.0f, d = 0.0f;
       for (int e = lane; e < experts; e += 64) {
-        c += (float)hits[e];
+        n += (float)hits[e];
         d += (float)hits[e] * sums[e];
       }
-      c = wave_sum(c);
+      n = wave_sum(n);
       d = wave_sum(d);
-      if (lane == 0) *p.loss = c > 0.0f ? (float)experts * (float)top_k * (d / c) / c : 0.0f;
+      if (lane == 0) *p.loss = n > 0.0f ? (float)experts * (float)top_k * (d / n) / n : 0.0f;
     }
   }
 }
 
-// Sums of the workgroups' parts, 64 experts a workgroup; the last one to finish
-// takes the loss.  Its reads of the others' results go past the caches of its
-// die, as their writes do.
-constexpr int kFinishWaves = 16;
+// Sums of the workgroups' parts, 16 experts a workgroup, 64 parts at a time; the
+// last one to finish takes the loss.  Results that one workgroup hands another are
+// written and read past the caches of the dies, so that no fence has to write
+// back a whole cache: waiting for the stores before the ticket is enough.
+constexpr int kFinishWaves = 16, kFinishExperts = 16;
 __global__ __launch_bounds__(64 * kFinishWaves) void router_finish_kernel(RouterArgs a, int parts) {
-  __shared__ float s_sum[kFinishWaves][64];
-  __shared__ int32_t s_count[kFinishWaves][64];
+  __shared__ float s_sum[kFinishWaves][kFinishExperts];
+  __shared__ int32_t s_count[kFinishWaves][kFinishExperts];
   __shared__ float s_c[kFinishWaves], s_d[kFinishWaves];
   __shared__ uint32_t place;
   const situ_moe_router_t& p = a.p;
-  const int lane = lane_id(), wave = threadIdx.x / kWave, e = blockIdx.x * 64 + lane;
+  const int lane = lane_id(), wave = wave_id(), e = blockIdx.x * kFinishExperts + lane % kFinishExperts;
+  constexpr int kAtOnce = 64 * kFinishWaves / kFinishExperts;
   float sum = 0.0f;
   int32_t count = 0;
   if (e < p.experts) {
-#pragma unroll 8
-    for (int i = wave; i < parts; i += kFinishWaves) {
+#pragma unroll 4
+    for (int i = threadIdx.x / kFinishExperts; i < parts; i += kAtOnce) {
       sum += a.part_sum[(int64_t)i * p.experts + e];
       count += a.part_count[(int64_t)i * p.experts + e];
     }
   }
-  s_sum[wave][lane] = sum;
-  s_count[wave][lane] = count;
+#pragma unroll
+  for (int m = kFinishExperts; m < kWave; m *= 2) {
+    sum += __shfl_xor(sum, m, kWave);
+    count += __shfl_xor(count, m, kWave);
+  }
+  if (lane < kFinishExperts) {
+    s_sum[wave][lane] = sum;
+    s_count[wave][lane] = count;
+  }
   __syncthreads();
   if (wave == 0) {
-    for (int w = 1; w < kFinishWaves; ++w) { sum += s_sum[w][lane]; count += s_count[w][lane]; }
-    if (e < p.experts) {
+    if (lane < kFinishExperts && e < p.experts) {
+      for (int w = 1; w < kFinishWaves; ++w) { sum += s_sum[w][lane]; count += s_count[w][lane]; }
       __hip_atomic_store(&p.prob_sum[e], sum, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       __hip_atomic_store(&p.counts[e], count, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
-    __threadfence();
-    if (lane == 0) place = __hip_atomic_fetch_add(a.ticket, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+    __builtin_amdgcn_s_waitcnt(0);                   // the stores have reached where the others look
+    if (lane == 0) place = __hip_atomic_fetch_add(a.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
   __syncthreads();
   if (place + 1 != gridDim.x) return;
-  __threadfence();
   float c = 0.0f, d = 0.0f;
   for (int i = threadIdx.x; i < p.experts; i += 64 * kFinishWaves) {
     const float n = (float)__hip_atomic_load(&p.counts[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -379,10 +438,10 @@ __global__ __launch_bounds__(64 * kFinishWaves) void router_finish_kernel(Router
 // and for sigmoid the whole times 1 - sigmoid(z_e).  A row of floats by expert
 // in LDS takes the x to the lanes that hold their experts.
 template <bool BF, bool BFO, int V, int J, bool SIG>
-__global__ __launch_bounds__(64 * kRouterWaves) void router_backward_kernel(situ_moe_router_backward_t p, int vec, int vec_out) {
+__global__ __launch_bounds__(64 * kBackWaves) void router_backward_kernel(situ_moe_router_backward_t p, int vec, int vec_out) {
   constexpr int N = V * J;
-  __shared__ float rows[kRouterWaves][64 * N];
-  const int lane = lane_id(), wave = threadIdx.x / kWave;
+  __shared__ float rows[kBackWaves][64 * N];
+  const int lane = lane_id(), wave = wave_id();
   float* x = rows[wave];
   float g[N];
 #pragma unroll
@@ -400,8 +459,8 @@ __global__ __launch_bounds__(64 * kRouterWaves) void router_backward_kernel(situ
 #pragma unroll
     for (int i = 0; i < N; ++i) g[i] *= f;
   }
-  const int64_t step = (int64_t)gridDim.x * kRouterWaves;
-  for (int64_t t = (int64_t)blockIdx.x * kRouterWaves + wave; t < p.tokens; t += step) {
+  const int64_t step = (int64_t)gridDim.x * kBackWaves;
+  for (int64_t t = (int64_t)blockIdx.x * kBackWaves + wave; t < p.tokens; t += step) {
     const int64_t in = t * p.logits_stride, out = t * p.out_stride;
     float z[N], d[N];
     uint32_t best = 0;
@@ -422,29 +481,28 @@ __global__ __launch_bounds__(64 * kRouterWaves) void router_backward_kernel(situ
         if (id >= p.experts) id = -1;
         if (id >= 0) {
           dw = p.d_weights[t * p.top_k + lane] * p.scale;
-          zc = BF ? bf16_to_f32(static_cast<const uint16_t*>(p.logits)[in + id])
-                  : static_cast<const float*>(p.logits)[in + id];
+          zc = load_one<BF>(p.logits, in + id);
         }
       }
       float all = 0.0f, pg = 0.0f;
+      scores<SIG, N>(z, shift, d);
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        d[i] = score(SIG, z[i], shift);
         all += d[i];
         pg = fmaf(d[i], g[i], pg);
       }
-      const float r = 1.0f / wave_sum(all);
+      const float r = __builtin_amdgcn_rcpf(wave_sum(all));
       pg = loss ? wave_sum(pg) * r : 0.0f;
       if (p.d_weights) {
         float xc;
         if (p.renormalize) {
           const uint32_t topc = wave_max(id >= 0 ? key_of(zc) : 0u);     // of the chosen: they need not be the largest
-          const float sc = id >= 0 && topc ? score(SIG, zc, SIG ? fminf(value_of(topc), 0.0f) : value_of(topc)) : 0.0f;
+          const float sc = id >= 0 && topc ? score<SIG>(zc, SIG ? fminf(value_of(topc), 0.0f) : value_of(topc)) : 0.0f;
           const float total = wave_sum(sc);
           const float q = topc ? sc / total : 0.0f;
           xc = q * (dw - wave_sum(q * dw));
         } else {
-          xc = id >= 0 ? (SIG ? score(true, zc, 0.0f) : score(false, zc, shift) * r) * dw : 0.0f;
+          xc = id >= 0 ? (SIG ? score<SIG>(zc, 0.0f) : score<SIG>(zc, shift) * r) * dw : 0.0f;
           if constexpr (!SIG) pg += wave_sum(xc);
         }
         if (id >= 0) atomicAdd(&x[id], xc);
@@ -518,9 +576,9 @@ void router_sized(const RouterArgs& a, int blocks, hipStream_t s) {
 template <bool BF, bool BFO, int V, int J>
 void backward_scored(const situ_moe_router_backward_t& p, int vec, int vec_out, int blocks, hipStream_t s) {
   if (p.scoring == SITU_SCORE_SOFTMAX)
-    hipLaunchKernelGGL((router_backward_kernel<BF, BFO, V, J, false>), dim3(blocks), dim3(64 * kRouterWaves), 0, s, p, vec, vec_out);
+    hipLaunchKernelGGL((router_backward_kernel<BF, BFO, V, J, false>), dim3(blocks), dim3(64 * kBackWaves), 0, s, p, vec, vec_out);
   else
-    hipLaunchKernelGGL((router_backward_kernel<BF, BFO, V, J, true>), dim3(blocks), dim3(64 * kRouterWaves), 0, s, p, vec, vec_out);
+    hipLaunchKernelGGL((router_backward_kernel<BF, BFO, V, J, true>), dim3(blocks), dim3(64 * kBackWaves), 0, s, p, vec, vec_out);
 }
 template <bool BF, bool BFO>
 void backward_sized(const situ_moe_router_backward_t& p, int vec, int vec_out, int blocks, hipStream_t s) {
@@ -551,7 +609,7 @@ hipError_t launch_router(const situ_moe_router_t& p, hipStream_t s) {
   const bool balance = p.counts != nullptr;
   // without the loss nothing is shared: as many workgroups as there are tokens for
   const int blocks = balance ? router_blocks(p.tokens)
-                             : (int)std::min<int64_t>(((int64_t)p.tokens + kRouterWaves - 1) / kRouterWaves, 4 * kRouterBlocks);
+                             : (int)std::min<int64_t>(((int64_t)p.tokens + kRouterWaves - 1) / kRouterWaves, 8 * kRouterBlocks);
   if (balance) {
     const int64_t part = (int64_t)router_blocks(p.tokens) * p.experts;
     a.part_sum = static_cast<float*>(p.workspace);
@@ -562,14 +620,14 @@ hipError_t launch_router(const situ_moe_router_t& p, hipStream_t s) {
   else router_sized<false>(a, blocks, s);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || !balance || blocks == 1) return e;
-  hipLaunchKernelGGL(router_finish_kernel, dim3((p.experts + 63) / 64), dim3(64 * kFinishWaves), 0, s, a, blocks);
+  hipLaunchKernelGGL(router_finish_kernel, dim3((p.experts + kFinishExperts - 1) / kFinishExperts), dim3(64 * kFinishWaves), 0, s, a, blocks);
   return hipGetLastError();
 }
 
 hipError_t launch_router_backward(const situ_moe_router_backward_t& p, hipStream_t s) {
   const bool bf = p.logits_dtype == SITU_OUT_BF16, bfo = p.out_dtype == SITU_OUT_BF16;
   const int vec = four_at_once(p.logits, p.logits_stride, bf), vec_out = four_at_once(p.d_logits, p.out_stride, bfo);
-  const int blocks = (int)std::min<int64_t>(((int64_t)p.tokens + kRouterWaves - 1) / kRouterWaves, kRouterBlocks);
+  const int blocks = (int)std::min<int64_t>(((int64_t)p.tokens + kBackWaves - 1) / kBackWaves, 1024);
   if (bf) {
     if (bfo) backward_sized<true, true>(p, vec, vec_out, blocks, s);
     else backward_sized<true, false>(p, vec, vec_out, blocks, s);

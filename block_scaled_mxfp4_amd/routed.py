@@ -100,6 +100,8 @@ def _adapters_bytes(rows, n, k, rank):
 
 def _workspace(given, need, device, dev):
     """Address and bytes of a workspace, and the tensor that holds them."""
+    if not need:
+        return 0, 0, given
     if given is None:
         given = _G._empty(need, dtype=_G.torch.uint8, device=device)
         return given.data_ptr(), need, given

@@ -67,7 +67,7 @@ def check(x, a, b, offsets, adapter, base=None, ranks=None, scales=None, before=
 
 
 SHAPES = [(8, 8, 8), (64, 128, 16), (264, 200, 16), (1000, 72, 32), (520, 3584, 24), (136, 1040, 64), (72, 264, 128),
-          (200, 136, 256)]                              # n, k, rank
+          (200, 136, 256), (136, 8200, 24), (264, 2056, 72)]                   # n, k, rank
 BATCHES = {"one_token": [1], "decode": [1] * 37, "decode_large": [1] * 131, "ragged": [3, 0, 17, 1, 64, 0, 0, 33, 2],
            "long": [300, 0, 5, 411], "many_empty": [0] * 150 + [5] + [0] * 200 + [40, 1] + [0] * 90,
            "many": [(5 * i) % 4 for i in range(700)]}
