@@ -364,7 +364,7 @@ __global__ __launch_bounds__(64 * kUpWaves) void adapters_up_kernel(AdapterArgs 
 // workgroups lie on one die (workgroups go round the eight dies), so that a is read into one cache.  Of b, as many
 // lanes as a row of it has pieces of eight ranks (the next power of two) share a column; its first pieces and base are
 // requested before t is known.
-constexpr int kRowWaves = 8, kRowCols = 2048, kRowAhead = 8;
+constexpr int kRowWaves = 8, kRowPieces = 2, kRowCols = kRowPieces * 64 * kRowWaves * 8, kRowAhead = 8;
 template <bool F32>
 __global__ __launch_bounds__(64 * kRowWaves) void adapters_row_kernel(AdapterArgs a, int log_pieces) {
   __shared__ float ts[256], sums[kRowCols];
@@ -373,13 +373,17 @@ __global__ __launch_bounds__(64 * kRowWaves) void adapters_row_kernel(AdapterArg
   const int slot = blockIdx.x / 8, row = slot / a.chunks * 8 + blockIdx.x % 8, chunk = slot % a.chunks;
   if (row >= p.rows) return;
   const int c0 = chunk * a.run, c1 = min(c0 + a.run, p.n);       // run: columns of a workgroup
-  // base: eight columns a thread
-  const int cb = c0 + 8 * (int)threadIdx.x;
+  // base: eight columns a thread and piece
   constexpr int NB = F32 ? 2 : 1;
-  uint4 base[NB];
+  uint4 base[kRowPieces][NB];
 #pragma unroll
-  for (int h = 0; h < NB; ++h)
-    base[h] = load16(static_cast<const char*>(p.base) + ((int64_t)row * p.base_stride + cb) * (F32 ? 4 : 2) + 16 * h, p.base && cb < c1);
+  for (int o = 0; o < kRowPieces; ++o) {
+    const int c = c0 + 8 * ((int)threadIdx.x + 64 * kRowWaves * o);
+#pragma unroll
+    for (int h = 0; h < NB; ++h)
+      base[o][h] = load16(static_cast<const char*>(p.base) + ((int64_t)row * p.base_stride + c) * (F32 ? 4 : 2) + 16 * h,
+                          p.base && c < c1);
+  }
   // x: eight of k a lane and piece
   const uint16_t* xr = p.x + (int64_t)row * p.x_stride;
   uint4 x[kRowAhead];
@@ -460,34 +464,48 @@ __global__ __launch_bounds__(64 * kRowWaves) void adapters_row_kernel(AdapterArg
       finish(load16(b + (int64_t)c * p.rank, 8 * mine < rank && c < c1), c);
     __syncthreads();
   }
-  if (cb >= c1) return;
-  float f[8];
-  if constexpr (F32) {
-    const uint32_t u[8] = {base[0].x, base[0].y, base[0].z, base[0].w, base[NB - 1].x, base[NB - 1].y, base[NB - 1].z, base[NB - 1].w};
 #pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(u[e]);
-  } else {
-    unpack8(base[0], f);
-  }
-  if (rank > 0) {
+  for (int o = 0; o < kRowPieces; ++o) {
+    const int at = 8 * ((int)threadIdx.x + 64 * kRowWaves * o), c = c0 + at;
+    if (c >= c1) continue;
+    float f[8];
+    if constexpr (F32) {
+      const uint4 u = base[o][0], v = base[o][NB - 1];
+      const uint32_t w[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] += sums[cb - c0 + e];
-  }
-  if constexpr (F32) {
-    float* o = static_cast<float*>(p.out) + (int64_t)row * p.out_stride + cb;
-    *reinterpret_cast<f32x4*>(o) = f32x4{f[0], f[1], f[2], f[3]};
-    *reinterpret_cast<f32x4*>(o + 4) = f32x4{f[4], f[5], f[6], f[7]};
-  } else {
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + (int64_t)row * p.out_stride + cb) = pack8(f);
+      for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(w[e]);
+    } else {
+      unpack8(base[o][0], f);
+    }
+    if (rank > 0) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] += sums[at + e];
+    }
+    if constexpr (F32) {
+      float* to = static_cast<float*>(p.out) + (int64_t)row * p.out_stride + c;
+      *reinterpret_cast<f32x4*>(to) = f32x4{f[0], f[1], f[2], f[3]};
+      *reinterpret_cast<f32x4*>(to + 4) = f32x4{f[4], f[5], f[6], f[7]};
+    } else {
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + (int64_t)row * p.out_stride + c) = pack8(f);
+    }
   }
 }
 
-// Few rows: a row a tile, as decode's requests have one each; else whole tiles.
+// Tiles of the two launches: as many of the first product's as there are CUs, where there are rows for them.
 int up_tile_rows(int32_t rows) { return rows <= 64 ? 1 : rows <= 256 ? 4 : 16; }
-int down_tile_rows(int32_t rows, int32_t rank) { return rows <= 2048 || rank > 64 ? up_tile_rows(rows) : 32; }
-
-// The one launch reads an adapter's a for each row and share of its columns, from its die's cache.
-bool row_by_row(int32_t rows, int32_t k, int32_t rank) { return rows <= 64 && (int64_t)rank * k <= 1 << 17; }
+int down_tile_rows(int32_t rows, int32_t rank) {
+  int tile = 1;
+  while (tile < (rank > 64 ? 16 : 32) && rows > 256 * tile) tile *= 2;
+  return tile;
+}
+// The one launch reads both matrices of its adapter for every row; two launches read them once for the rows of a request
+// in a tile.  Rank 16, 3584 to 7168, requests of one row: 64 rows 8.7 us against 14.8, 256 rows 20 against 27; rank 32:
+// 64 rows 14 against 17, 128 rows 22 against 21.  Requests of 32 rows, rank 16: 64 rows 8.8 against 12.1, 128 rows 12.4
+// against 12.6, 256 rows 20 against 15.
+bool row_by_row(const situ_moe_adapters_t& p) {
+  if (p.rank > 16) return p.rows <= 64;
+  return p.rows <= 128 || (p.rows <= 512 && p.rows <= 2 * p.requests);
+}
 
 template <bool F32>
 void up_go(const AdapterArgs& a, int64_t items, hipStream_t s) {
@@ -502,19 +520,19 @@ void up_go(const AdapterArgs& a, int64_t items, hipStream_t s) {
 
 }  // namespace
 
-uint64_t adapters_workspace_bytes(int32_t rows, int32_t k, int32_t rank) {
-  return row_by_row(rows, k, rank) ? 0 : 4ull * (uint64_t)rows * (uint64_t)rank;
+uint64_t adapters_workspace_bytes(const situ_moe_adapters_t& p) {
+  return row_by_row(p) ? 0 : 4ull * (uint64_t)p.rows * (uint64_t)p.rank;
 }
 
 hipError_t launch_adapters(const situ_moe_adapters_t& p, hipStream_t s) {
   AdapterArgs a{};
   a.p = p;
   const int r = p.rank;
-  if (row_by_row(p.rows, p.k, r)) {
-    // workgroups of a row: 256 in all, each 256 to 2048 columns
+  if (row_by_row(p)) {
+    // workgroups of a row: 256 in all, each 256 to 8192 columns
     const int eights = (p.rows + 7) / 8;
     const int most = (p.n + 255) / 256, least = (p.n + kRowCols - 1) / kRowCols;
-    a.chunks = std::max(least, std::min(most, 32 / eights));
+    a.chunks = std::max({1, least, std::min(most, 32 / eights)});
     a.run = ((p.n + a.chunks - 1) / a.chunks + 7) / 8 * 8;
     a.chunks = (p.n + a.run - 1) / a.run;
     int log_pieces = 0;

@@ -13,11 +13,12 @@ namespace situ {
 
 // ---- the gate
 // Workspace: [blocks][experts] partial probability sums, then as many partial
-// counts, then the finishing kernel's ticket.
+// counts, then the finishing kernel's ticket; none where one workgroup does it all.
 constexpr int kRouterMaxExperts = 1024, kRouterMaxK = 64;
 int router_blocks(int32_t tokens);
 inline uint64_t router_workspace_bytes(int32_t tokens, int32_t experts) {
-  return 8ull * (uint64_t)router_blocks(tokens) * (uint64_t)experts + 16;
+  const uint64_t blocks = (uint64_t)router_blocks(tokens);
+  return blocks == 1 ? 0 : 8ull * blocks * (uint64_t)experts + 16;
 }
 hipError_t launch_router(const situ_moe_router_t& a, hipStream_t s);
 hipError_t launch_router_backward(const situ_moe_router_backward_t& a, hipStream_t s);
@@ -32,7 +33,7 @@ hipError_t launch_pair_combine_backward(const situ_moe_combine_t& a, hipStream_t
 
 // ---- the adapters
 // Workspace: two bf16 terms of t a row and rank; none where one launch does it all.
-uint64_t adapters_workspace_bytes(int32_t rows, int32_t k, int32_t rank);
+uint64_t adapters_workspace_bytes(const situ_moe_adapters_t& a);
 hipError_t launch_adapters(const situ_moe_adapters_t& a, hipStream_t s);
 
 }  // namespace situ

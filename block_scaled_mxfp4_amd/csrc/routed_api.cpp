@@ -230,7 +230,7 @@ situ_status situ_moe_combine_backward(const situ_moe_combine_t* p, void* hip_str
 situ_status situ_moe_adapters_workspace(const situ_moe_adapters_t* p, uint64_t* bytes) {
   SITU_TRY(check_adapter_sizes(p));
   if (!bytes) return fail_status(SITU_E_NULL_ARG, "bytes is NULL");
-  *bytes = situ::adapters_workspace_bytes(p->rows, p->k, p->rank);
+  *bytes = situ::adapters_workspace_bytes(*p);
   return SITU_OK;
 }
 
@@ -252,7 +252,7 @@ situ_status situ_moe_adapters(const situ_moe_adapters_t* p, void* hip_stream) {
   SITU_TRY(check_array("b", p->b, 16));
   if (p->base) SITU_TRY(check_in("base", p->base, p->base_stride, p->n, size_of(p->out_dtype)));
   SITU_TRY(check_in("out", p->out, p->out_stride, p->n, size_of(p->out_dtype)));
-  SITU_TRY(check_workspace(p->workspace, p->workspace_bytes, situ::adapters_workspace_bytes(p->rows, p->k, p->rank)));
+  SITU_TRY(check_workspace(p->workspace, p->workspace_bytes, situ::adapters_workspace_bytes(*p)));
   int cus = 0;
   SITU_TRY(situ::require_device(&cus));
   return launched(situ::launch_adapters(*p, stream(hip_stream)), "adapters");

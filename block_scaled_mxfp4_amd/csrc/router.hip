@@ -124,7 +124,7 @@ __device__ __forceinline__ void scores(const float z[N], float shift, float s[N]
 struct RouterArgs {
   situ_moe_router_t p;
   int32_t vec;
-  float* part_sum;            // [gridDim.x][experts], or null: no balance loss
+  float* part_sum;            // [gridDim.x][experts], or null: one workgroup, or no balance loss
   int32_t* part_count;
   uint32_t* ticket;
 };
@@ -172,7 +172,7 @@ __global__ __launch_bounds__(64 * kRouterWaves, 4) void router_kernel(RouterArgs
 #pragma unroll
     for (int i = 0; i < N; ++i) acc[i] = 0.0f;
     for (int i = threadIdx.x; i < 64 * N; i += 64 * kRouterWaves) { sums[i] = 0.0f; hits[i] = 0; }
-    if (blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0;     // for the launch that follows
+    if (a.ticket && blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0;     // for the launch that follows
     __syncthreads();
   }
   float bias[BIAS ? N : 1];
@@ -552,7 +552,7 @@ __global__ __launch_bounds__(64 * kBackWaves) void router_backward_kernel(situ_m
 
 template <bool BF, int V, int J, bool SIG, bool BIAS>
 void router_go(const RouterArgs& a, int blocks, hipStream_t s) {
-  if (a.part_sum)
+  if (a.p.counts)
     hipLaunchKernelGGL((router_kernel<BF, V, J, SIG, BIAS, true>), dim3(blocks), dim3(64 * kRouterWaves), 0, s, a);
   else
     hipLaunchKernelGGL((router_kernel<BF, V, J, SIG, BIAS, false>), dim3(blocks), dim3(64 * kRouterWaves), 0, s, a);
@@ -610,7 +610,7 @@ hipError_t launch_router(const situ_moe_router_t& p, hipStream_t s) {
   // without the loss nothing is shared: as many workgroups as there are tokens for
   const int blocks = balance ? router_blocks(p.tokens)
                              : (int)std::min<int64_t>(((int64_t)p.tokens + kRouterWaves - 1) / kRouterWaves, 8 * kRouterBlocks);
-  if (balance) {
+  if (balance && blocks > 1) {
     const int64_t part = (int64_t)router_blocks(p.tokens) * p.experts;
     a.part_sum = static_cast<float*>(p.workspace);
     a.part_count = reinterpret_cast<int32_t*>(a.part_sum + part);

@@ -15,10 +15,9 @@ import struct
 
 import block_scaled_mxfp4_amd as _B
 from . import grouped as _G
-from .grouped import _at, _bad, _dense, _fail, _lead, _out_code, _rows
+from .grouped import _Place, _bad, _dense, _fail, _lead, _out_code, _rows
 
 SCORINGS = {"softmax": 0, "sigmoid": 1}
-CONSTANTS = {"situ": ("situ_beta", "situ_linear_beta"), "swiglu": (), "swiglu_bias": ("swiglu_alpha", "swiglu_beta")}
 
 
 class SituMoeRouter(ctypes.Structure):
@@ -67,15 +66,33 @@ assert all(s.size == ctypes.sizeof(c) for s, c in (
     (_COMBINE, SituMoeCombine), (_ADAPTERS, SituMoeAdapters)))
 
 
-def _pack(form, *fields):
+# looked up once, as grouped.py does: importing this package imports neither torch nor the library
+torch = _device = _raw_stream = _empty = _library = None
+_BF16 = _F32 = _EITHER = _CODES = _INT32 = _MASK = ()
+
+
+def _first():
+    global torch, _device, _raw_stream, _empty, _library, _BF16, _F32, _EITHER, _CODES, _INT32, _MASK
+    if _G.torch is None:
+        _G._first()
+    _device, _raw_stream, _empty, _library = _G._device, _G._raw_stream, _G._empty, _G._library
+    _BF16, _F32, _EITHER, _CODES, _INT32 = _G._BF16, _G._F32, _G._EITHER, _G._CODES, _G._INT32
+    _MASK = (_G.torch.bool, _G.torch.uint8)
+    torch = _G.torch
+
+
+def _elsewhere(dev, stream, call, *args):
+    """call(handle, *args) on a device or stream that is not the current one."""
+    with _Place(dev, stream) as handle:
+        return call(handle, *args)
+
+
+def _run(entry, handle, form, *fields):
     try:
-        return form.pack(*fields)
+        args = form.pack(*fields)
     except (struct.error, OverflowError):
         _fail(3, "a size past 32 bits, or a scale past fp32")
-
-
-def _call(fn, args, handle):
-    status = fn(args, handle)
+    status = entry(args, handle)
     if status:
         _B._check(status)
 
@@ -88,14 +105,14 @@ def _need_bytes(fn, args):
 
 @functools.lru_cache(maxsize=256)
 def _router_bytes(tokens, experts):
-    return _need_bytes(_G._library.situ_moe_router_workspace,
-                       _pack(_ROUTER, tokens, experts, 1, 0, 0, 0, 0, 1.0, 0, *[0] * 6, 1, 1, 1, 0, 0))
+    return _need_bytes(_library.situ_moe_router_workspace,
+                       _ROUTER.pack(tokens, experts, 1, 0, 0, 0, 0, 1.0, 0, *[0] * 6, 1, 1, 1, 0, 0))
 
 
 @functools.lru_cache(maxsize=256)
-def _adapters_bytes(rows, n, k, rank):
-    return _need_bytes(_G._library.situ_moe_adapters_workspace,
-                       _pack(_ADAPTERS, rows, n, k, rank, *[0] * 7, *[0] * 11))
+def _adapters_bytes(rows, n, k, rank, requests):
+    return _need_bytes(_library.situ_moe_adapters_workspace,
+                       _ADAPTERS.pack(rows, n, k, rank, requests, *[0] * 6, *[0] * 11))
 
 
 def _workspace(given, need, device, dev):
@@ -103,7 +120,7 @@ def _workspace(given, need, device, dev):
     if not need:
         return 0, 0, given
     if given is None:
-        given = _G._empty(need, dtype=_G.torch.uint8, device=device)
+        given = _empty(need, dtype=torch.uint8, device=device)
         return given.data_ptr(), need, given
     if given.get_device() != dev or not given.is_contiguous():
         _bad(given, "workspace", (given.dtype,), dev, "contiguous")
@@ -117,7 +134,7 @@ def _maybe(t, name, shape, dtypes, dev):
 def _made(t, name, shape, dtype, device, dev):
     """An output and its address, allocated here if it is None."""
     if t is None:
-        t = _G._empty(shape, dtype=dtype, device=device)
+        t = _empty(*shape, dtype=dtype, device=device)
         return t, t.data_ptr()
     return t, _dense(t, name, shape, (dtype,), dev)
 
@@ -125,10 +142,6 @@ def _made(t, name, shape, dtype, device, dev):
 def _scoring(name):
     code = SCORINGS.get(name)
     return _fail(3, f"scoring {name!r} (softmax or sigmoid)") if code is None else code
-
-
-def _mask_types():
-    return (_G.torch.bool, _G.torch.uint8)
 
 
 def situ_moe_router(logits, top_k, *, scoring="softmax", bias=None, renormalize=True, scale=1.0, mask=None,
@@ -151,16 +164,19 @@ def situ_moe_router(logits, top_k, *, scoring="softmax", bias=None, renormalize=
         experts * top_k / C^2 * sum_e counts[e] prob_sum[e],  C = sum counts.
 
     Returns (ids, weights[, packed][, counts, prob_sum, loss])."""
-    if _G.torch is None:
-        _G._first()
-    dev, tokens, experts, stride, lp = _lead(logits, "logits", _G._EITHER)
-    return _at(dev, stream, _router, logits, dev, tokens, experts, stride, lp, int(top_k), _scoring(scoring), bias,
-               bool(renormalize), scale, mask, balance, packed, ids, weights, weights_dtype, counts, prob_sum, loss, workspace)
+    if torch is None:
+        _first()
+    dev, tokens, experts, stride, lp = _lead(logits, "logits", _EITHER)
+    args = (logits, dev, tokens, experts, stride, lp, int(top_k), _scoring(scoring), bias, bool(renormalize), scale,
+            mask, balance, packed, ids, weights, weights_dtype, counts, prob_sum, loss, workspace)
+    if stream is None and dev == _device():
+        return _router(_raw_stream(dev), *args)
+    return _elsewhere(dev, stream, _router, *args)
 
 
 def _router(handle, logits, dev, tokens, experts, stride, lp, top_k, scoring, bias, renormalize, scale, mask, balance,
             packed, ids, weights, weights_dtype, counts, prob_sum, loss, workspace):
-    torch, device = _G.torch, logits.device
+    device = logits.device
     if not 0 < top_k <= experts:
         _fail(2, f"top_k {top_k} of {experts} experts")
     shape = (tokens, top_k)
@@ -181,11 +197,11 @@ def _router(handle, logits, dev, tokens, experts, stride, lp, top_k, scoring, bi
         loss, op = _made(loss, "loss", (1,), torch.float32, device, dev)
         wsp, need, workspace = _workspace(workspace, _router_bytes(tokens, experts), device, dev)
         out += (counts, prob_sum, loss)
-    bp = _maybe(bias, "bias", (experts,), _G._F32, dev)
-    mp = _maybe(mask, "mask", (tokens,), _mask_types(), dev)
-    _call(_G._library.situ_moe_router,
-          _pack(_ROUTER, tokens, experts, top_k, scoring, _out_code(logits.dtype), code, renormalize, scale, stride, lp, bp,
-                mp, ip, wp, pp, cp, sp, op, wsp, need), handle)
+    bp = _maybe(bias, "bias", (experts,), _F32, dev)
+    mp = _maybe(mask, "mask", (tokens,), _MASK, dev)
+    _run(_library.situ_moe_router, handle, _ROUTER,
+         tokens, experts, top_k, scoring, _out_code(logits.dtype), code, renormalize, scale, stride, lp, bp, mp, ip,
+         wp, pp, cp, sp, op, wsp, need)
     return out
 
 
@@ -196,54 +212,57 @@ def situ_moe_router_backward(logits, ids, d_weights=None, *, scoring="softmax", 
     (fp32 [tokens, top_k]) and through the balance loss from counts (those of
     the loss) and d_loss (fp32 [1]); either may be None.  ids and counts are
     constants of it.  Rows of masked tokens are 0."""
-    if _G.torch is None:
-        _G._first()
-    dev, tokens, experts, stride, lp = _lead(logits, "logits", _G._EITHER)
-    return _at(dev, stream, _router_backward, logits, dev, tokens, experts, stride, lp, ids, d_weights, _scoring(scoring),
-               bool(renormalize), scale, mask, counts, d_loss, out, out_dtype)
+    if torch is None:
+        _first()
+    dev, tokens, experts, stride, lp = _lead(logits, "logits", _EITHER)
+    args = (logits, dev, tokens, experts, stride, lp, ids, d_weights, _scoring(scoring), bool(renormalize), scale,
+            mask, counts, d_loss, out, out_dtype)
+    if stream is None and dev == _device():
+        return _router_backward(_raw_stream(dev), *args)
+    return _elsewhere(dev, stream, _router_backward, *args)
 
 
-def _router_backward(handle, logits, dev, tokens, experts, stride, lp, ids, d_weights, scoring, renormalize, scale, mask,
+def _router_backward(handle, logits, dev, tokens, experts, stride, lp, ids, d_weights, scoring, renormalize, scale,
+                     mask,
                      counts, d_loss, out, out_dtype):
-    if ids is None:
-        if d_weights is not None:
-            _fail(1, "ids is None")
-        if counts is not None:
-            _fail(1, "ids is None: the loss is of top_k choices a token")
-    if ids is None or ids.dim() != 2:
-        _bad(ids, "ids", _G._INT32, dev, "[tokens, top_k]")
+    if ids is None or ids.dim() != 2:          # the loss alone takes top_k from them
+        _bad(ids, "ids", _INT32, dev, "[tokens, top_k]")
     top_k = ids.shape[1]
-    ip = _dense(ids, "ids", (tokens, top_k), _G._INT32, dev)
-    dp = _maybe(d_weights, "d_weights", (tokens, top_k), _G._F32, dev)
-    mp = _maybe(mask, "mask", (tokens,), _mask_types(), dev)
-    cp = _maybe(counts, "counts", (experts,), _G._INT32, dev)
-    if d_loss is not None and d_loss.numel() == 1:
+    ip = _dense(ids, "ids", (tokens, top_k), _INT32, dev)
+    dp = _maybe(d_weights, "d_weights", (tokens, top_k), _F32, dev)
+    mp = _maybe(mask, "mask", (tokens,), _MASK, dev)
+    cp = _maybe(counts, "counts", (experts,), _INT32, dev)
+    if d_loss is not None and d_loss.dim() == 0:
         d_loss = d_loss.view(1)
-    gp = _maybe(d_loss, "d_loss", (1,), _G._F32, dev)
+    gp = _maybe(d_loss, "d_loss", (1,), _F32, dev)
     if out is None:
-        out = _G._empty(tokens, experts, dtype=out_dtype or logits.dtype, device=logits.device)
+        out = _empty(tokens, experts, dtype=out_dtype or logits.dtype, device=logits.device)
     elif out_dtype is not None and out.dtype != out_dtype:
         _bad(out, "out", (out_dtype,), dev, f"({tokens}, {experts})")
     code = _out_code(out.dtype)
-    _, out_stride, op = _rows(out, "out", tokens, experts, _G._EITHER, dev)
-    _call(_G._library.situ_moe_router_backward,
-          _pack(_ROUTER_BACKWARD, tokens, experts, top_k, scoring, _out_code(logits.dtype), code, renormalize, scale, stride,
-                out_stride, lp, mp, ip, dp, cp, gp, op), handle)
+    _, out_stride, op = _rows(out, "out", tokens, experts, _EITHER, dev)
+    _run(_library.situ_moe_router_backward, handle, _ROUTER_BACKWARD,
+         tokens, experts, top_k, scoring, _out_code(logits.dtype), code, renormalize, scale, stride, out_stride, lp,
+         mp, ip, dp, cp, gp, op)
     return out
 
 
-def _groups(activation, constants, offsets, dev):
+def _groups(activation, situ_beta, situ_linear_beta, swiglu_alpha, swiglu_beta, offsets, dev):
     """Code, experts and addresses of offsets and constants."""
-    names = CONSTANTS.get(activation)
-    if names is None:
-        _fail(3, f"activation {activation!r} ({', '.join(CONSTANTS)})")
     if offsets is None:
         experts, op = 1, 0
     else:
         experts = offsets.numel() - 1
-        op = _dense(offsets, "offsets", (experts + 1,), _G._INT32, dev)
-    p = [_dense(constants[n], n, (experts,), _G._F32, dev) for n in names] or [0, 0]
-    return _B.ACTIVATIONS[activation], experts, op, p
+        op = _dense(offsets, "offsets", (experts + 1,), _INT32, dev)
+    if activation == "situ":
+        return (0, experts, op, _dense(situ_beta, "situ_beta", (experts,), _F32, dev),
+                _dense(situ_linear_beta, "situ_linear_beta", (experts,), _F32, dev))
+    if activation == "swiglu":
+        return 1, experts, op, 0, 0
+    if activation == "swiglu_bias":
+        return (2, experts, op, _dense(swiglu_alpha, "swiglu_alpha", (experts,), _F32, dev),
+                _dense(swiglu_beta, "swiglu_beta", (experts,), _F32, dev))
+    _fail(3, f"activation {activation!r} ({', '.join(_B.ACTIVATIONS)})")
 
 
 def situ_moe_activation(gate_up, *, activation="situ", situ_beta=None, situ_linear_beta=None, swiglu_alpha=None,
@@ -258,37 +277,39 @@ def situ_moe_activation(gate_up, *, activation="situ", situ_beta=None, situ_line
     situ_moe_activation_backward: E4M3 codes uint8 [rows, 2I] and fp32 scales
     [rows, 2 ceil(I / 128)], and returns (h, codes, scales).  Rows outside
     every group are left as they are (undefined in an output allocated here)."""
-    if _G.torch is None:
-        _G._first()
-    dev, rows, width, stride, gp = _lead(gate_up, "gate_up", _G._BF16)
-    constants = dict(situ_beta=situ_beta, situ_linear_beta=situ_linear_beta, swiglu_alpha=swiglu_alpha, swiglu_beta=swiglu_beta)
-    return _at(dev, stream, _activation, gate_up.device, dev, rows, width, stride, gp, activation, constants, offsets, out,
-               checkpoint, codes, scales)
+    if torch is None:
+        _first()
+    dev, rows, width, stride, gp = _lead(gate_up, "gate_up", _BF16)
+    args = (gate_up.device, dev, rows, width, stride, gp, activation, situ_beta, situ_linear_beta, swiglu_alpha,
+            swiglu_beta, offsets, out, checkpoint, codes, scales)
+    if stream is None and dev == _device():
+        return _activation(_raw_stream(dev), *args)
+    return _elsewhere(dev, stream, _activation, *args)
 
 
-def _activation(handle, device, dev, rows, width, stride, gp, activation, constants, offsets, out, checkpoint, codes, scales):
-    torch = _G.torch
+def _activation(handle, device, dev, rows, width, stride, gp, activation, situ_beta, situ_linear_beta, swiglu_alpha,
+                swiglu_beta, offsets, out, checkpoint, codes, scales):
     if width % 16:
         _fail(2, f"gate_up has {width} columns, not a multiple of 16")
     inner = width // 2
-    code, experts, op, (p0, p1) = _groups(activation, constants, offsets, dev)
+    code, experts, op, p0, p1 = _groups(activation, situ_beta, situ_linear_beta, swiglu_alpha, swiglu_beta, offsets, dev)
     if out is None:
-        out = _G._empty(rows, inner, dtype=torch.bfloat16, device=device)
+        out = _empty(rows, inner, dtype=torch.bfloat16, device=device)
         h_stride, hp = inner, out.data_ptr()
     else:
-        _, h_stride, hp = _rows(out, "out", rows, inner, _G._BF16, dev)
+        _, h_stride, hp = _rows(out, "out", rows, inner, _BF16, dev)
     cp = sp = 0
     if checkpoint or codes is not None or scales is not None:
         checkpoint = True
         shape = (rows, 2 * -(-inner // 128))
         if codes is None:
-            codes = _G._empty(rows, width, dtype=torch.uint8, device=device)
+            codes = _empty(rows, width, dtype=torch.uint8, device=device)
             cp = codes.data_ptr()
         else:
-            cp = _dense(codes, "codes", (rows, width), _G._CODES, dev)
+            cp = _dense(codes, "codes", (rows, width), _CODES, dev)
         scales, sp = _made(scales, "scales", shape, torch.float32, device, dev)
-    _call(_G._library.situ_moe_activation,
-          _pack(_ACTIVATION, rows, inner, experts, code, stride, h_stride, 0, 0, op, p0, p1, gp, hp, cp, sp, 0, 0), handle)
+    _run(_library.situ_moe_activation, handle, _ACTIVATION,
+         rows, inner, experts, code, stride, h_stride, 0, 0, op, p0, p1, gp, hp, cp, sp, 0, 0)
     return (out, codes, scales) if checkpoint else out
 
 
@@ -300,54 +321,55 @@ def situ_moe_activation_backward(dh, gate_up, scales=None, *, activation="situ",
     codes that were kept.  recompute=True (or h given) also returns h at those
     values, (d_gate_up, h): the down product's input for its wgrad.  The
     activation's constants get no gradient."""
-    if _G.torch is None:
-        _G._first()
-    dev, rows, inner, stride, dp = _lead(dh, "dh", _G._BF16)
-    constants = dict(situ_beta=situ_beta, situ_linear_beta=situ_linear_beta, swiglu_alpha=swiglu_alpha, swiglu_beta=swiglu_beta)
-    return _at(dev, stream, _activation_backward, dh.device, dev, rows, inner, stride, dp, gate_up, scales, activation,
-               constants, offsets, out, recompute, h)
+    if torch is None:
+        _first()
+    dev, rows, inner, stride, dp = _lead(dh, "dh", _BF16)
+    args = (dh.device, dev, rows, inner, stride, dp, gate_up, scales, activation, situ_beta, situ_linear_beta,
+            swiglu_alpha, swiglu_beta, offsets, out, recompute, h)
+    if stream is None and dev == _device():
+        return _activation_backward(_raw_stream(dev), *args)
+    return _elsewhere(dev, stream, _activation_backward, *args)
 
 
-def _activation_backward(handle, device, dev, rows, inner, stride, dp, gate_up, scales, activation, constants, offsets, out,
+def _activation_backward(handle, device, dev, rows, inner, stride, dp, gate_up, scales, activation, situ_beta,
+                         situ_linear_beta, swiglu_alpha, swiglu_beta, offsets, out,
                          recompute, h):
-    torch = _G.torch
     if inner % 8:
         _fail(2, f"dh has {inner} columns, not a multiple of 8")
-    code, experts, op, (p0, p1) = _groups(activation, constants, offsets, dev)
+    code, experts, op, p0, p1 = _groups(activation, situ_beta, situ_linear_beta, swiglu_alpha, swiglu_beta, offsets, dev)
     g_stride = gp = cp = sp = 0
     if scales is None:
-        _, g_stride, gp = _rows(gate_up, "gate_up", rows, 2 * inner, _G._BF16, dev)
+        _, g_stride, gp = _rows(gate_up, "gate_up", rows, 2 * inner, _BF16, dev)
     else:
-        cp = _dense(gate_up, "gate_up", (rows, 2 * inner), _G._CODES, dev)
-        sp = _dense(scales, "scales", (rows, 2 * -(-inner // 128)), _G._F32, dev)
+        cp = _dense(gate_up, "gate_up", (rows, 2 * inner), _CODES, dev)
+        sp = _dense(scales, "scales", (rows, 2 * -(-inner // 128)), _F32, dev)
     if out is None:
-        out = _G._empty(rows, 2 * inner, dtype=torch.bfloat16, device=device)
+        out = _empty(rows, 2 * inner, dtype=torch.bfloat16, device=device)
         o_stride, outp = 2 * inner, out.data_ptr()
     else:
-        _, o_stride, outp = _rows(out, "out", rows, 2 * inner, _G._BF16, dev)
+        _, o_stride, outp = _rows(out, "out", rows, 2 * inner, _BF16, dev)
     h_stride = hp = 0
     if h is not None:
         recompute = True
-        _, h_stride, hp = _rows(h, "h", rows, inner, _G._BF16, dev)
+        _, h_stride, hp = _rows(h, "h", rows, inner, _BF16, dev)
     elif recompute:
-        h = _G._empty(rows, inner, dtype=torch.bfloat16, device=device)
+        h = _empty(rows, inner, dtype=torch.bfloat16, device=device)
         h_stride, hp = inner, h.data_ptr()
-    _call(_G._library.situ_moe_activation_backward,
-          _pack(_ACTIVATION, rows, inner, experts, code, g_stride, h_stride, stride, o_stride, op, p0, p1, gp, hp, cp, sp, dp,
-                outp), handle)
+    _run(_library.situ_moe_activation_backward, handle, _ACTIVATION,
+         rows, inner, experts, code, g_stride, h_stride, stride, o_stride, op, p0, p1, gp, hp, cp, sp, dp, outp)
     return (out, h) if recompute else out
 
 
 def _pairs(weights, inv, dev):
     """Tokens, slots and addresses of weights [tokens, top_k] and inv (of as many)."""
-    if weights is None or weights.dim() != 2 or weights.dtype not in _G._EITHER:
-        _bad(weights, "weights", _G._EITHER, dev, "[tokens, top_k]")
+    if weights is None or weights.dim() != 2 or weights.dtype not in _EITHER:
+        _bad(weights, "weights", _EITHER, dev, "[tokens, top_k]")
     tokens, top_k = weights.shape
-    wp = _dense(weights, "weights", (tokens, top_k), _G._EITHER, dev)
+    wp = _dense(weights, "weights", (tokens, top_k), _EITHER, dev)
     if inv is None or inv.dim() != 1:
-        ip = _dense(inv, "inv", (tokens, top_k), _G._INT32, dev)
+        ip = _dense(inv, "inv", (tokens, top_k), _INT32, dev)
     else:
-        ip = _dense(inv, "inv", (tokens * top_k,), _G._INT32, dev)
+        ip = _dense(inv, "inv", (tokens * top_k,), _INT32, dev)
     return tokens, top_k, wp, ip
 
 
@@ -359,23 +381,26 @@ def situ_moe_combine(y, weights, inv, *, out=None, out_dtype=None, stream=None):
     fp32 [tokens, top_k]; inv: int32 [tokens, top_k] or [tokens * top_k], the
     row of each pair as situ_moe_route leaves it (outside [0, rows): the pair
     is not local)."""
-    if _G.torch is None:
-        _G._first()
-    dev, rows, hidden, stride, yp = _lead(y, "y", _G._EITHER)
-    return _at(dev, stream, _combine, y, dev, rows, hidden, stride, yp, weights, inv, out, out_dtype)
+    if torch is None:
+        _first()
+    dev, rows, hidden, stride, yp = _lead(y, "y", _EITHER)
+    args = (y, dev, rows, hidden, stride, yp, weights, inv, out, out_dtype)
+    if stream is None and dev == _device():
+        return _combine(_raw_stream(dev), *args)
+    return _elsewhere(dev, stream, _combine, *args)
 
 
 def _combine(handle, y, dev, rows, hidden, stride, yp, weights, inv, out, out_dtype):
     tokens, top_k, wp, ip = _pairs(weights, inv, dev)
     if out is None:
-        out = _G._empty(tokens, hidden, dtype=out_dtype or _G.torch.bfloat16, device=y.device)
+        out = _empty(tokens, hidden, dtype=out_dtype or torch.bfloat16, device=y.device)
     elif out_dtype is not None and out.dtype != out_dtype:
         _bad(out, "out", (out_dtype,), dev, f"({tokens}, {hidden})")
     code = _out_code(out.dtype)
-    _, out_stride, op = _rows(out, "out", tokens, hidden, _G._EITHER, dev)
-    _call(_G._library.situ_moe_combine,
-          _pack(_COMBINE, tokens, top_k, hidden, rows, _out_code(y.dtype), _out_code(weights.dtype), code, 0, stride,
-                out_stride, 0, yp, wp, ip, op, 0, 0), handle)
+    _, out_stride, op = _rows(out, "out", tokens, hidden, _EITHER, dev)
+    _run(_library.situ_moe_combine, handle, _COMBINE,
+         tokens, top_k, hidden, rows, _out_code(y.dtype), _out_code(weights.dtype), code, 0, stride, out_stride, 0,
+         yp, wp, ip, op, 0, 0)
     return out
 
 
@@ -386,24 +411,27 @@ def situ_moe_combine_backward(d_out, y, weights, inv, *, dy=None, d_weights=None
     hidden].  Each row of y belongs to one pair at most; rows of no pair are
     left as they are (undefined in a dy allocated here).  Returns (dy,
     d_weights)."""
-    if _G.torch is None:
-        _G._first()
-    dev, rows, hidden, stride, yp = _lead(y, "y", _G._EITHER)
-    return _at(dev, stream, _combine_backward, d_out, y, dev, rows, hidden, stride, yp, weights, inv, dy, d_weights)
+    if torch is None:
+        _first()
+    dev, rows, hidden, stride, yp = _lead(y, "y", _EITHER)
+    args = (d_out, y, dev, rows, hidden, stride, yp, weights, inv, dy, d_weights)
+    if stream is None and dev == _device():
+        return _combine_backward(_raw_stream(dev), *args)
+    return _elsewhere(dev, stream, _combine_backward, *args)
 
 
 def _combine_backward(handle, d_out, y, dev, rows, hidden, stride, yp, weights, inv, dy, d_weights):
     tokens, top_k, wp, ip = _pairs(weights, inv, dev)
-    _, d_stride, dp = _rows(d_out, "d_out", tokens, hidden, _G._EITHER, dev)
+    _, d_stride, dp = _rows(d_out, "d_out", tokens, hidden, _EITHER, dev)
     if dy is None:
-        dy = _G._empty(rows, hidden, dtype=y.dtype, device=y.device)
+        dy = _empty(rows, hidden, dtype=y.dtype, device=y.device)
         dy_stride, dyp = hidden, dy.data_ptr()
     else:
         _, dy_stride, dyp = _rows(dy, "dy", rows, hidden, (y.dtype,), dev)
-    d_weights, gp = _made(d_weights, "d_weights", (tokens, top_k), _G.torch.float32, y.device, dev)
-    _call(_G._library.situ_moe_combine_backward,
-          _pack(_COMBINE, tokens, top_k, hidden, rows, _out_code(y.dtype), _out_code(weights.dtype), _out_code(d_out.dtype), 0,
-                stride, d_stride, dy_stride, yp, wp, ip, dp, dyp, gp), handle)
+    d_weights, gp = _made(d_weights, "d_weights", (tokens, top_k), torch.float32, y.device, dev)
+    _run(_library.situ_moe_combine_backward, handle, _COMBINE,
+         tokens, top_k, hidden, rows, _out_code(y.dtype), _out_code(weights.dtype), _out_code(d_out.dtype), 0, stride,
+         d_stride, dy_stride, yp, wp, ip, dp, dyp, gp)
     return dy, d_weights
 
 
@@ -422,43 +450,46 @@ def situ_moe_adapters(x, a, b, offsets, adapter, *, base=None, ranks=None, scale
     [rows, n] of base's type, or out_dtype (bf16) without one; it may be base
     itself.  Rows of no request are left as they are (undefined in an output
     allocated here)."""
-    if _G.torch is None:
-        _G._first()
-    dev, rows, k, stride, xp = _lead(x, "x", _G._BF16)
-    return _at(dev, stream, _adapters, x.device, dev, rows, k, stride, xp, a, b, offsets, adapter, base, ranks, scales, out,
-               out_dtype, workspace)
+    if torch is None:
+        _first()
+    dev, rows, k, stride, xp = _lead(x, "x", _BF16)
+    args = (x.device, dev, rows, k, stride, xp, a, b, offsets, adapter, base, ranks, scales, out, out_dtype, workspace)
+    if stream is None and dev == _device():
+        return _adapters(_raw_stream(dev), *args)
+    return _elsewhere(dev, stream, _adapters, *args)
 
 
-def _adapters(handle, device, dev, rows, k, stride, xp, a, b, offsets, adapter, base, ranks, scales, out, out_dtype, workspace):
+def _adapters(handle, device, dev, rows, k, stride, xp, a, b, offsets, adapter, base, ranks, scales, out, out_dtype,
+              workspace):
     if a is None or a.dim() != 3:
-        _bad(a, "a", _G._BF16, dev, "[adapters, rank, k]")
+        _bad(a, "a", _BF16, dev, "[adapters, rank, k]")
     if b is None or b.dim() != 3:
-        _bad(b, "b", _G._BF16, dev, "[adapters, n, rank]")
+        _bad(b, "b", _BF16, dev, "[adapters, n, rank]")
     held, rank, _ = a.shape
     n = b.shape[1]
-    ap = _dense(a, "a", (held, rank, k), _G._BF16, dev)
-    bp = _dense(b, "b", (held, n, rank), _G._BF16, dev)
+    ap = _dense(a, "a", (held, rank, k), _BF16, dev)
+    bp = _dense(b, "b", (held, n, rank), _BF16, dev)
     if offsets is None:
         _fail(1, "offsets is None")
     requests = offsets.numel() - 1
-    op = _dense(offsets, "offsets", (requests + 1,), _G._INT32, dev)
-    ip = _dense(adapter, "adapter", (requests,), _G._INT32, dev)
-    rp = _maybe(ranks, "ranks", (held,), _G._INT32, dev)
-    sp = _maybe(scales, "scales", (held,), _G._F32, dev)
+    op = _dense(offsets, "offsets", (requests + 1,), _INT32, dev)
+    ip = _dense(adapter, "adapter", (requests,), _INT32, dev)
+    rp = _maybe(ranks, "ranks", (held,), _INT32, dev)
+    sp = _maybe(scales, "scales", (held,), _F32, dev)
     if out is None:
-        dtype = out_dtype or (_G.torch.bfloat16 if base is None else base.dtype)
-        out = _G._empty(rows, n, dtype=dtype, device=device)
+        dtype = out_dtype or (torch.bfloat16 if base is None else base.dtype)
+        out = _empty(rows, n, dtype=dtype, device=device)
         code, o_stride, outp = _out_code(dtype), n, out.data_ptr()
     else:
         if out_dtype is not None and out.dtype != out_dtype:
             _bad(out, "out", (out_dtype,), dev, f"({rows}, {n})")
         code = _out_code(out.dtype)
-        _, o_stride, outp = _rows(out, "out", rows, n, _G._EITHER, dev)
+        _, o_stride, outp = _rows(out, "out", rows, n, _EITHER, dev)
     b_stride = basep = 0
     if base is not None:
         _, b_stride, basep = _rows(base, "base", rows, n, (out.dtype,), dev)
-    wsp, need, workspace = _workspace(workspace, _adapters_bytes(rows, n, k, rank), device, dev)
-    _call(_G._library.situ_moe_adapters,
-          _pack(_ADAPTERS, rows, n, k, rank, requests, held, code, 0, stride, b_stride, o_stride, op, ip, rp, sp, xp, ap, bp,
-                basep, outp, wsp, need), handle)
+    wsp, need, workspace = _workspace(workspace, _adapters_bytes(rows, n, k, rank, requests), device, dev)
+    _run(_library.situ_moe_adapters, handle, _ADAPTERS,
+         rows, n, k, rank, requests, held, code, 0, stride, b_stride, o_stride, op, ip, rp, sp, xp, ap, bp, basep,
+         outp, wsp, need)
     return out

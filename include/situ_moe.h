@@ -538,7 +538,7 @@ typedef struct situ_moe_adapters_t {
   void* workspace;            /* (device) 16-byte aligned; calls sharing it must not overlap in time */
   uint64_t workspace_bytes;
 } situ_moe_adapters_t;
-/* Bytes of workspace an adapters call needs (rows, n, k and rank are read). */
+/* Bytes of workspace an adapters call needs (rows, n, k, rank and requests are read). */
 situ_status situ_moe_adapters_workspace(const situ_moe_adapters_t* args, uint64_t* bytes);
 situ_status situ_moe_adapters(const situ_moe_adapters_t* args, void* hip_stream);
 
