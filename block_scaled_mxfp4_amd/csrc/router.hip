@@ -21,9 +21,9 @@
 // they are: a row whose scores all underflow keeps its weights.
 //
 // Balance loss: a wave sums its tokens' shares in registers, the workgroup's
-// waves add up in LDS in turn, and each workgroup writes partial sums and counts;
-// a second launch adds them in a fixed order, and its last workgroup (by a
-// ticket) takes the loss.  One workgroup finishes by itself.
+// waves add theirs in LDS, and each workgroup writes partial sums and counts; a
+// second launch adds them in a fixed order, and its last workgroup (by a ticket)
+// takes the loss.  One workgroup finishes by itself.
 #include <algorithm>
 
 #include "common.hpp"
@@ -73,6 +73,20 @@ __device__ __forceinline__ void load_row(const void* logits, int64_t at, int lan
 #pragma unroll
   for (int j = 0; j < J; ++j) {
     const int e = 64 * V * j + V * lane;
+    if constexpr (V == 2) {
+      if (vec && e + 2 <= experts) {
+        if constexpr (BF) {
+          const uint32_t w = *reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(logits) + at + e);
+          z[2 * j] = bf16_to_f32(w & 0xffffu);
+          z[2 * j + 1] = bf16_to_f32(w >> 16);
+        } else {
+          const f32x2 w = *reinterpret_cast<const f32x2*>(static_cast<const float*>(logits) + at + e);
+          z[2 * j] = w[0];
+          z[2 * j + 1] = w[1];
+        }
+        continue;
+      }
+    }
     if constexpr (V == 4) {
       if (vec && e + 4 <= experts) {
         if constexpr (BF) {
@@ -171,7 +185,7 @@ __global__ __launch_bounds__(64 * kRouterWaves, 4) void router_kernel(RouterArgs
   if constexpr (BAL) {
 #pragma unroll
     for (int i = 0; i < N; ++i) acc[i] = 0.0f;
-    for (int i = threadIdx.x; i < 64 * N; i += 64 * kRouterWaves) { sums[i] = 0.0f; hits[i] = 0; }
+    for (int i = threadIdx.x; i < 64 * N; i += 64 * kRouterWaves) hits[i] = 0;
     if (a.ticket && blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0;     // for the launch that follows
     __syncthreads();
   }
@@ -216,7 +230,7 @@ __global__ __launch_bounds__(64 * kRouterWaves, 4) void router_kernel(RouterArgs
         const int n = __popcll(__ballot(best >= value_of(mid)));
         if (n >= top_k) {
           lo = mid;
-          if (n <= top_k + 8) break;
+          if (n <= top_k + 2) break;
         } else {
           hi = mid;
         }
@@ -347,12 +361,15 @@ __global__ __launch_bounds__(64 * kRouterWaves, 4) void router_kernel(RouterArgs
     wave_lds();
   }
   if constexpr (BAL) {
-    for (int w = 0; w < kRouterWaves; ++w) {         // in turn: a fixed order
-      __syncthreads();
-      if (wave == w) {
+    // the waves' sums take their rows' place, and are added in a fixed order
 #pragma unroll
-        for (int i = 0; i < N; ++i) sums[64 * V * (i / V) + V * lane + i % V] += acc[i];
-      }
+    for (int i = 0; i < N; ++i) cd.z[64 * V * (i / V) + V * lane + i % V] = acc[i];
+    __syncthreads();
+    for (int e = threadIdx.x; e < 64 * N; e += 64 * kRouterWaves) {
+      float sum = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kRouterWaves; ++w) sum += wave_rows[w].z[e];
+      sums[e] = sum;
     }
     __syncthreads();
     const bool alone = gridDim.x == 1;
@@ -590,9 +607,10 @@ void backward_sized(const situ_moe_router_backward_t& p, int vec, int vec_out, i
   else backward_scored<BF, BFO, 4, 4>(p, vec, vec_out, blocks, s);
 }
 
-// Rows of four experts start on 16 bytes (8 in bf16).
-int four_at_once(const void* p, int64_t stride, bool bf) {
-  return reinterpret_cast<uintptr_t>(p) % (bf ? 8 : 16) == 0 && stride % 4 == 0;
+// Whether every row's experts can be moved four (two up to 128 experts) at a time.
+int at_once(const void* p, int64_t stride, bool bf, int experts) {
+  const int v = experts <= 128 ? 2 : 4;
+  return reinterpret_cast<uintptr_t>(p) % (unsigned)(bf ? 2 * v : 4 * v) == 0 && stride % v == 0;
 }
 
 }  // namespace
@@ -605,7 +623,7 @@ hipError_t launch_router(const situ_moe_router_t& p, hipStream_t s) {
   RouterArgs a{};
   a.p = p;
   const bool bf = p.logits_dtype == SITU_OUT_BF16;
-  a.vec = four_at_once(p.logits, p.logits_stride, bf);
+  a.vec = at_once(p.logits, p.logits_stride, bf, p.experts);
   const bool balance = p.counts != nullptr;
   // without the loss nothing is shared: as many workgroups as there are tokens for
   const int blocks = balance ? router_blocks(p.tokens)
@@ -626,7 +644,7 @@ hipError_t launch_router(const situ_moe_router_t& p, hipStream_t s) {
 
 hipError_t launch_router_backward(const situ_moe_router_backward_t& p, hipStream_t s) {
   const bool bf = p.logits_dtype == SITU_OUT_BF16, bfo = p.out_dtype == SITU_OUT_BF16;
-  const int vec = four_at_once(p.logits, p.logits_stride, bf), vec_out = four_at_once(p.d_logits, p.out_stride, bfo);
+  const int vec = at_once(p.logits, p.logits_stride, bf, p.experts), vec_out = at_once(p.d_logits, p.out_stride, bfo, p.experts);
   const int blocks = (int)std::min<int64_t>(((int64_t)p.tokens + kBackWaves - 1) / kBackWaves, 1024);
   if (bf) {
     if (bfo) backward_sized<true, true>(p, vec, vec_out, blocks, s);
