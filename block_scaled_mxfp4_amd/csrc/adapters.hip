@@ -32,7 +32,7 @@ constexpr int kUpWaves = 4;
 struct AdapterArgs {
   situ_moe_adapters_t p;
   uint16_t *high, *low;       // t as two bf16 terms, [rows][rank] each
-  int32_t tile;               // rows of a tile of the first product, 1 .. 32
+  int32_t tile;               // rows of a tile of the first product, 1 .. 16
   int32_t up_tile;            // of the second, 1 .. 16
   int32_t up_tiles;
   int32_t run;                // of them a wave takes in turn (one launch: columns of a workgroup)
@@ -83,10 +83,15 @@ __device__ __forceinline__ int next_bit(uint64_t& m) {
 // Sixteen bytes, zeros where there are none: the address is chosen and not the load branched around, since behind
 // branches the compiler cannot count the loads in flight and waits for all of them.
 __device__ const uint4 kZeros[1] = {};
-__device__ __forceinline__ uint4 load16(const void* p, bool in) {
-  typedef const i32x4 __attribute__((address_space(1)))* Global;
-  const Global at = (Global)p, zeros = (Global)kZeros;
-  return __builtin_bit_cast(uint4, *(in ? at : zeros));
+typedef const i32x4 __attribute__((address_space(1)))* Sixteen;
+__device__ __forceinline__ Sixteen sixteen(const void* p, bool in) {
+  const Sixteen at = (Sixteen)p, zeros = (Sixteen)kZeros;
+  return in ? at : zeros;
+}
+__device__ __forceinline__ uint4 load16(const void* p, bool in) { return __builtin_bit_cast(uint4, *sixteen(p, in)); }
+// Read once: past the caches, which a and t then stay in (8192 rows, the first product: 24 us, 21 so).
+__device__ __forceinline__ uint4 load16_once(const void* p, bool in) {
+  return __builtin_bit_cast(uint4, __builtin_nontemporal_load(sixteen(p, in)));
 }
 __device__ __forceinline__ f32x4 mfma(const uint4& a, const uint4& b, const f32x4& c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
@@ -122,13 +127,13 @@ __device__ __forceinline__ void two_terms(const f32x4& t, uint2& high, uint2& lo
 
 // t.  A workgroup takes a tile of rows, its waves every W-th unit of 64 of k.  A unit of x and a is requested by whole
 // lines, eight lanes of 16 bytes a row (rows of 64 bytes, as the matrix instruction holds them, go through the address
-// unit at half the rate), put into the wave's own LDS and read back as operands: lane l ranks 16 i + l % 16 of a (rows
-// of the instruction) and tokens 16 j + l % 16 of x (columns), eight of k.  Piece c of row r lies in place c ^ (r % 8).
-// U units are under way while one is multiplied.  RT: tiles of 16 ranks; TG: of 16 tokens.
-template <int RT, int TG, int U, int W>
+// unit at half the rate: 8192 x 3584 of rank 32 in 36 us), put into the wave's own LDS and read back as operands: lane l
+// ranks 16 i + l % 16 of a (rows of the instruction) and token l % 16 of x (columns), eight of k.  Piece c of row r lies
+// in place c ^ (r % 8).  The next unit is under way while one is multiplied; waves in number hide the rest (17.8 us; two
+// and three units ahead, with the registers of fewer waves, 19 and 21; tiles of 32 rows the same).  RT: tiles of 16 ranks.
+template <int RT, int W>
 __global__ __launch_bounds__(64 * W) void adapters_down_kernel(AdapterArgs a) {
-  constexpr int kParts = 2 * (RT + TG);               // of eight rows in a unit
-  static_assert(RT * TG <= kParts, "the sums take the units' place");
+  constexpr int kParts = 2 * (RT + 1);                // of eight rows in a unit
   __shared__ uint4 lds[W][kParts * 64];
   const situ_moe_adapters_t& p = a.p;
   const int lane = lane_id(), wave = wave_id(), col = lane & 15, group = lane >> 4;
@@ -136,9 +141,9 @@ __global__ __launch_bounds__(64 * W) void adapters_down_kernel(AdapterArgs a) {
   const int r0 = blockIdx.x * a.tile, r1 = min(r0 + a.tile, p.rows);
   const int units = (p.k + 63) / 64;
   uint4* mine = lds[wave];
-  const uint16_t* x[2 * TG];
+  const uint16_t* x[2];
 #pragma unroll
-  for (int j = 0; j < 2 * TG; ++j) x[j] = p.x + (int64_t)min(r0 + 8 * j + line, r1 - 1) * p.x_stride + 8 * piece;
+  for (int j = 0; j < 2; ++j) x[j] = p.x + (int64_t)min(r0 + 8 * j + line, r1 - 1) * p.x_stride + 8 * piece;
   Requests q;
   for (int first = first_request(p, r0, lane);; first += 64) {
     load_requests(p, first, lane, q);
@@ -148,72 +153,51 @@ __global__ __launch_bounds__(64 * W) void adapters_down_kernel(AdapterArgs a) {
       const int i = __builtin_amdgcn_readlane(q.adapter, at);
       if (i < 0) continue;
       const int lo = max(__builtin_amdgcn_readlane(q.begin, at), r0), hi = min(__builtin_amdgcn_readlane(q.end, at), r1);
+      const float c = p.scales ? p.scales[i] : 1.0f;
+      const int rank = p.ranks ? min(max(p.ranks[i], 0), p.rank) : p.rank;
       const uint16_t* w[2 * RT];
 #pragma unroll
       for (int j = 0; j < 2 * RT; ++j) w[j] = p.a + ((int64_t)i * p.rank + min(8 * j + line, p.rank - 1)) * p.k + 8 * piece;
-      f32x4 acc[RT][TG];
+      f32x4 acc[RT];
 #pragma unroll
-      for (int j = 0; j < RT; ++j)
-#pragma unroll
-        for (int g = 0; g < TG; ++g) acc[j][g] = f32x4{0, 0, 0, 0};
-      struct Unit { uint4 v[kParts]; };
-      auto request = [&](Unit& f, int u) {
+      for (int j = 0; j < RT; ++j) acc[j] = f32x4{0, 0, 0, 0};
+      uint4 v[kParts];
+      auto request = [&](int u) {                     // of units past the last: zeros
         const bool in = u < units && u * 64 + 8 * piece < p.k;
 #pragma unroll
-        for (int j = 0; j < 2 * TG; ++j) f.v[j] = load16(x[j] + u * 64, in);
+        for (int j = 0; j < 2; ++j) v[j] = load16(x[j] + u * 64, in);
 #pragma unroll
-        for (int j = 0; j < 2 * RT; ++j) f.v[2 * TG + j] = load16(w[j] + u * 64, in);
+        for (int j = 0; j < 2 * RT; ++j) v[2 + j] = load16(w[j] + u * 64, in);
       };
-      auto store = [&](const Unit& f) {
+      request(wave);
+      for (int u = wave; u < units; u += W) {
 #pragma unroll
-        for (int j = 0; j < kParts; ++j) mine[64 * j + 8 * line + (piece ^ line)] = f.v[j];
+        for (int j = 0; j < kParts; ++j) mine[64 * j + 8 * line + (piece ^ line)] = v[j];
         wave_lds();
-      };
-      auto multiply = [&] {
+        request(u + W);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int c = (4 * h + group) ^ (col & 7);
-          uint4 xt[TG], at_[RT];
+          const uint4 xt = mine[8 * col + c];
 #pragma unroll
-          for (int g = 0; g < TG; ++g) xt[g] = mine[8 * (16 * g + col) + c];
-#pragma unroll
-          for (int j = 0; j < RT; ++j) at_[j] = mine[8 * (16 * (TG + j) + col) + c];
-#pragma unroll
-          for (int j = 0; j < RT; ++j)
-#pragma unroll
-            for (int g = 0; g < TG; ++g) acc[j][g] = mfma(at_[j], xt[g], acc[j][g]);
+          for (int j = 0; j < RT; ++j) acc[j] = mfma(mine[8 * (16 * (1 + j) + col) + c], xt, acc[j]);
         }
         wave_lds();
-      };
-      Unit f[U];
-#pragma unroll
-      for (int v = 0; v < U; ++v) request(f[v], wave + v * W);
-      for (int u = wave; u < units; u += U * W) {
-#pragma unroll
-        for (int v = 0; v < U; ++v) {
-          store(f[v]);                                // of units past the last: zeros
-          request(f[v], u + (U + v) * W);
-          multiply();
-        }
       }
-      // the waves' sums: each adds up every W-th tile of 16 ranks and tokens
+      // the waves' sums: each wave adds up every W-th tile of 16 ranks
 #pragma unroll
-      for (int j = 0; j < RT; ++j)
-#pragma unroll
-        for (int g = 0; g < TG; ++g) mine[64 * (j * TG + g) + lane] = __builtin_bit_cast(uint4, acc[j][g]);
+      for (int j = 0; j < RT; ++j) mine[64 * j + lane] = __builtin_bit_cast(uint4, acc[j]);
       __syncthreads();
-      const float c = p.scales ? p.scales[i] : 1.0f;
-      const int rank = p.ranks ? min(max(p.ranks[i], 0), p.rank) : p.rank;
-      for (int o = wave; o < RT * TG; o += W) {
-        f32x4 v = f32x4{0, 0, 0, 0};
+      for (int j = wave; j < RT; j += W) {
+        f32x4 t = f32x4{0, 0, 0, 0};
 #pragma unroll
-        for (int e = 0; e < W; ++e) v += __builtin_bit_cast(f32x4, lds[e][64 * o + lane]);
-        const int r = 16 * (o / TG) + 4 * group, row = r0 + 16 * (o % TG) + col;
+        for (int e = 0; e < W; ++e) t += __builtin_bit_cast(f32x4, lds[e][64 * j + lane]);
+        const int r = 16 * j + 4 * group, row = r0 + col;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = r + e < rank ? v[e] * c : 0.0f;
+        for (int e = 0; e < 4; ++e) t[e] = r + e < rank ? t[e] * c : 0.0f;
         if (row >= lo && row < hi && r < p.rank) {
           uint2 high, low;
-          two_terms(v, high, low);
+          two_terms(t, high, low);
           *reinterpret_cast<uint2*>(a.high + (int64_t)row * p.rank + r) = high;
           *reinterpret_cast<uint2*>(a.low + (int64_t)row * p.rank + r) = low;
         }
@@ -265,7 +249,7 @@ __global__ __launch_bounds__(64 * kUpWaves) void adapters_up_kernel(AdapterArgs 
       const int row = r0 + 4 * group + i;
 #pragma unroll
       for (int h = 0; h < NB; ++h)
-        f.base[i][h] = load16(static_cast<const char*>(p.base) + ((int64_t)row * p.base_stride + c) * (F32 ? 4 : 2) + 16 * h,
+        f.base[i][h] = load16_once(static_cast<const char*>(p.base) + ((int64_t)row * p.base_stride + c) * (F32 ? 4 : 2) + 16 * h,
                               p.base && in && row < r1);
     }
     // of token l % 16: rows of requests without an adapter hold anything, and are not used
@@ -493,9 +477,9 @@ __global__ __launch_bounds__(64 * kRowWaves) void adapters_row_kernel(AdapterArg
 
 // Tiles of the two launches: as many of the first product's as there are CUs, where there are rows for them.
 int up_tile_rows(int32_t rows) { return rows <= 64 ? 1 : rows <= 256 ? 4 : 16; }
-int down_tile_rows(int32_t rows, int32_t rank) {
+int down_tile_rows(int32_t rows) {
   int tile = 1;
-  while (tile < (rank > 64 ? 16 : 32) && rows > 256 * tile) tile *= 2;
+  while (tile < 16 && rows > 256 * tile) tile *= 2;
   return tile;
 }
 // The one launch reads both matrices of its adapter for every row; two launches read them once for the rows of a request
@@ -545,19 +529,13 @@ hipError_t launch_adapters(const situ_moe_adapters_t& p, hipStream_t s) {
   a.high = static_cast<uint16_t*>(p.workspace);
   a.low = a.high + (int64_t)p.rows * r;
   a.up_tile = up_tile_rows(p.rows);
-  a.tile = down_tile_rows(p.rows, r);
+  a.tile = down_tile_rows(p.rows);
   const dim3 grid((unsigned)((p.rows + a.tile - 1) / a.tile));
-  if (a.tile > 16) {
-    if (r <= 16) hipLaunchKernelGGL((adapters_down_kernel<1, 2, 4, 8>), grid, dim3(512), 0, s, a);
-    else if (r <= 32) hipLaunchKernelGGL((adapters_down_kernel<2, 2, 3, 8>), grid, dim3(512), 0, s, a);
-    else hipLaunchKernelGGL((adapters_down_kernel<4, 2, 1, 8>), grid, dim3(512), 0, s, a);
-  } else {
-    if (r <= 16) hipLaunchKernelGGL((adapters_down_kernel<1, 1, 2, 16>), grid, dim3(1024), 0, s, a);
-    else if (r <= 32) hipLaunchKernelGGL((adapters_down_kernel<2, 1, 3, 8>), grid, dim3(512), 0, s, a);
-    else if (r <= 64) hipLaunchKernelGGL((adapters_down_kernel<4, 1, 2, 8>), grid, dim3(512), 0, s, a);
-    else if (r <= 128) hipLaunchKernelGGL((adapters_down_kernel<8, 1, 1, 8>), grid, dim3(512), 0, s, a);
-    else hipLaunchKernelGGL((adapters_down_kernel<16, 1, 1, 4>), grid, dim3(256), 0, s, a);
-  }
+  if (r <= 16) hipLaunchKernelGGL((adapters_down_kernel<1, 8>), grid, dim3(512), 0, s, a);
+  else if (r <= 32) hipLaunchKernelGGL((adapters_down_kernel<2, 8>), grid, dim3(512), 0, s, a);
+  else if (r <= 64) hipLaunchKernelGGL((adapters_down_kernel<4, 8>), grid, dim3(512), 0, s, a);
+  else if (r <= 128) hipLaunchKernelGGL((adapters_down_kernel<8, 8>), grid, dim3(512), 0, s, a);
+  else hipLaunchKernelGGL((adapters_down_kernel<16, 4>), grid, dim3(256), 0, s, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   a.up_tiles = (p.rows + a.up_tile - 1) / a.up_tile;

@@ -32,6 +32,15 @@ __device__ __forceinline__ Eight<F32> load8(const void* p, int64_t at) {
     return {*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + at)};
   }
 }
+// The gradient's y is read once (4095 x 16 x 3584: 195 us with ordinary loads, 190 so).
+template <bool F32>
+__device__ __forceinline__ Eight<F32> load8_once(const void* p, int64_t at) {
+  const i32x4* q = reinterpret_cast<const i32x4*>(static_cast<const char*>(p) + at * (F32 ? 4 : 2));
+  if constexpr (F32)
+    return {__builtin_bit_cast(uint4, __builtin_nontemporal_load(q)), __builtin_bit_cast(uint4, __builtin_nontemporal_load(q + 1))};
+  else
+    return {__builtin_bit_cast(uint4, __builtin_nontemporal_load(q))};
+}
 template <bool F32>
 __device__ __forceinline__ void widen(const Eight<F32>& v, float f[8]) {
   const uint32_t w[4] = {v.a.x, v.a.y, v.a.z, v.a.w};
@@ -151,7 +160,7 @@ __global__ __launch_bounds__(64 * kWaves) void pair_combine_backward_kernel(situ
         if (p.d_weights) {
 #pragma unroll
           for (int i = 0; i < kAtOnce; ++i)
-            if (i < n) v[i] = load8<YF>(p.y, r[i] * p.y_stride + col);
+            if (i < n) v[i] = load8_once<YF>(p.y, r[i] * p.y_stride + col);
         }
         widen<OF>(vd, d);
 #pragma unroll

@@ -175,8 +175,8 @@ situ_status situ_moe_router_backward(const situ_moe_router_backward_t* p, void* 
   SITU_TRY(check_dtype("out_dtype", p->out_dtype));
   if ((p->counts == nullptr) != (p->d_loss == nullptr))
     return fail_status(SITU_E_NULL_ARG, "counts and d_loss are given together or not at all");
+  if (p->tokens == 0) return SITU_OK;                // empty arrays may be NULL
   if (!p->counts && !p->d_weights) return fail_status(SITU_E_NULL_ARG, "neither d_weights nor d_loss is given");
-  if (p->tokens == 0) return SITU_OK;
   SITU_TRY(check_out("logits", p->logits, p->logits_stride, p->experts, size_of(p->logits_dtype)));
   SITU_TRY(check_out("d_logits", p->d_logits, p->out_stride, p->experts, size_of(p->out_dtype)));
   if (p->d_weights) SITU_TRY(check_array("ids", p->ids, 4));

@@ -37,7 +37,7 @@ namespace {
 constexpr float kL2e = 1.44269502162933349609375f;   // log2(e) rounded to fp32
 constexpr int kRouterWaves = 8;                       // of a workgroup
 constexpr int kRouterBlocks = 768;                    // workgroups at most where the loss is taken
-constexpr int kBackWaves = 8;
+constexpr int kBackWaves = 8, kBackBlocks = 640;      // of the gradient (16384 x 896: 24 us; 512 or 768 26, 1024 29)
 constexpr int kOneBlockTokens = 32;                   // up to here one workgroup finishes the loss by itself
 
 // Keys ascend with the values; 0 is an expert that cannot be chosen (-inf, NaN).
@@ -645,7 +645,7 @@ hipError_t launch_router(const situ_moe_router_t& p, hipStream_t s) {
 hipError_t launch_router_backward(const situ_moe_router_backward_t& p, hipStream_t s) {
   const bool bf = p.logits_dtype == SITU_OUT_BF16, bfo = p.out_dtype == SITU_OUT_BF16;
   const int vec = at_once(p.logits, p.logits_stride, bf, p.experts), vec_out = at_once(p.d_logits, p.out_stride, bfo, p.experts);
-  const int blocks = (int)std::min<int64_t>(((int64_t)p.tokens + kBackWaves - 1) / kBackWaves, 1024);
+  const int blocks = (int)std::min<int64_t>(((int64_t)p.tokens + kBackWaves - 1) / kBackWaves, kBackBlocks);
   if (bf) {
     if (bfo) backward_sized<true, true>(p, vec, vec_out, blocks, s);
     else backward_sized<true, false>(p, vec, vec_out, blocks, s);
