@@ -11,8 +11,10 @@
 // t' = 1 - t^2 = 4 e / (1 + e)^2 with e = e^-2|x|, and s(-x) from the same
 // exponential as s(x): neither is a difference of near numbers.
 //
-// Elementwise, bound by HBM: 8 bytes a (gate, up) pair forward with codes, as
-// many backward from codes.  Sixteen lanes take 128 columns of a row's gate and
+// Elementwise, bound by HBM and nearly by the vector units: 8 bytes a (gate, up)
+// pair forward with codes, 10 backward from codes with h; 57 and 64 issue slots.
+// 262144 x 384 forward with codes: 150 to 166 us (4.9 TB/s and more); 65521 x 768
+// backward: 106 (4.8 TB/s; a large copy moves 4.9).  Sixteen lanes take 128 columns of a row's gate and
 // the same of its up, eight each (16 bytes): a block of the 8-bit format, whose
 // maximum is then four DPP moves.  They walk the row's blocks, so that the row's
 // expert is looked up once, in LDS, where the offsets and constants are copied.
@@ -175,7 +177,8 @@ __device__ __forceinline__ void codes8(const uint2& c, float s, float f[8]) {
 // The largest magnitude of the sixteen lanes' eight (a NaN is passed over).
 template <int kCtrl>
 __device__ __forceinline__ float row_max(float v) {
-  return fmaxf(v, __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), kCtrl, 0xf, 0xf, true)));
+  const int o = __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), kCtrl, 0xf, 0xf, true);
+  return fmaxf(v, __builtin_bit_cast(float, o));
 }
 __device__ __forceinline__ float amax16(const float f[8]) {
   float m = 0.0f;
@@ -272,7 +275,8 @@ __global__ __launch_bounds__(kActThreads) void activation_backward_kernel(ActArg
       if (col + 8 * at >= p.inner) continue;
       float g[8], u[8], dh[8], h[8];
       if constexpr (KEPT) {
-        const uint2 cg = *reinterpret_cast<const uint2*>(codes + col), cu = *reinterpret_cast<const uint2*>(codes + p.inner + col);
+        const uint2 cg = *reinterpret_cast<const uint2*>(codes + col);
+        const uint2 cu = *reinterpret_cast<const uint2*>(codes + p.inner + col);
         codes8(cg, scales[b], g);
         codes8(cu, scales[a.blocks + b], u);
       } else {

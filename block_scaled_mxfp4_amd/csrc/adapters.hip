@@ -2,22 +2,22 @@
 // (situ_moe_adapters): out[r] = base[r] + c_i b_i (a_i x[r]), i the adapter of
 // r's request.
 //
-// Two launches: t = c a_i x in fp32 into the workspace, then out = base + b_i t.
-// Prefill is bound by HBM (x read once, base and out once; the adapters come from
-// L2), decode by the two launches and their memory latencies.
+// A batch of many rows takes two launches: t = c a_i x into the workspace, then out
+// = base + b_i t.  They are bound by HBM: 8192 rows, 3584 to 7168, rank 32, take 18
+// and 46 us, the second at 5.1 TB/s of base and out.  Few rows (decode) take one
+// launch, a row a workgroup, bound by its memory latencies in turn: 64 rows of
+// rank 16 in 8.3 us, 14.8 in two.
 //
-// Both work on tiles of up to 16 rows in the order of the batch, whatever
+// The two work on tiles of up to 16 rows in the order of the batch, whatever
 // requests they belong to, so that neither the host nor the grid needs to know
 // the requests' lengths: a wave holds the requests that reach into its tile one
-// a lane and takes them in turn.  Tokens lie on the column side of the matrix
-// instruction, so that a lane ends with consecutive ranks, or columns of out, of
-// one token.  Every request's product is kept by its own rows alone: what another
-// request's adapter holds (infinities, NaN) does not reach them.
+// a lane and takes them in turn.  Every request's product is kept by its own rows
+// alone: what another request's adapter holds (infinities, NaN) does not reach
+// them.
 //
-// The first product splits k over the waves of a workgroup and over workgroups
-// (`parts`), whose sums the second one adds.  The second takes t as two bf16
-// terms, high and low, so that no more than 2^-16 of it is lost; with ranks up to
-// 16 both fit in one instruction's 32 columns.
+// Between the two, t is held as two bf16 terms, high and low, so that no more than
+// 2^-16 of it is lost; with ranks up to 16 both fit in one instruction's 32
+// columns.
 #include <algorithm>
 
 #include "routed.hpp"
@@ -125,12 +125,13 @@ __device__ __forceinline__ void two_terms(const f32x4& t, uint2& high, uint2& lo
   low = __builtin_bit_cast(uint2, l);
 }
 
-// t.  A workgroup takes a tile of rows, its waves every W-th unit of 64 of k.  A unit of x and a is requested by whole
-// lines, eight lanes of 16 bytes a row (rows of 64 bytes, as the matrix instruction holds them, go through the address
-// unit at half the rate: 8192 x 3584 of rank 32 in 36 us), put into the wave's own LDS and read back as operands: lane l
-// ranks 16 i + l % 16 of a (rows of the instruction) and token l % 16 of x (columns), eight of k.  Piece c of row r lies
-// in place c ^ (r % 8).  The next unit is under way while one is multiplied; waves in number hide the rest (17.8 us; two
-// and three units ahead, with the registers of fewer waves, 19 and 21; tiles of 32 rows the same).  RT: tiles of 16 ranks.
+// t.  A workgroup takes a tile of rows, its waves every W-th unit of 64 of k.  A unit of x and a is requested by
+// whole lines, eight lanes of 16 bytes a row (rows of 64 bytes, as the matrix instruction holds them, go through the
+// address unit at half the rate: 8192 x 3584 of rank 32 in 36 us), put into the wave's own LDS and read back as
+// operands: lane l ranks 16 i + l % 16 of a (rows of the instruction) and token l % 16 of x (columns), eight of k, so
+// that it ends with four consecutive ranks of a token.  Piece c of row r lies in place c ^ (r % 8).  The next unit is
+// under way while one is multiplied; waves in number hide the rest (17.8 us; two and three units ahead, with the
+// registers of fewer waves, 19 and 21; tiles of 32 rows the same).  RT: tiles of 16 ranks.
 template <int RT, int W>
 __global__ __launch_bounds__(64 * W) void adapters_down_kernel(AdapterArgs a) {
   constexpr int kParts = 2 * (RT + 1);                // of eight rows in a unit
@@ -152,12 +153,14 @@ __global__ __launch_bounds__(64 * W) void adapters_down_kernel(AdapterArgs a) {
       const int at = next_bit(some);
       const int i = __builtin_amdgcn_readlane(q.adapter, at);
       if (i < 0) continue;
-      const int lo = max(__builtin_amdgcn_readlane(q.begin, at), r0), hi = min(__builtin_amdgcn_readlane(q.end, at), r1);
+      const int lo = max(__builtin_amdgcn_readlane(q.begin, at), r0);
+      const int hi = min(__builtin_amdgcn_readlane(q.end, at), r1);
       const float c = p.scales ? p.scales[i] : 1.0f;
       const int rank = p.ranks ? min(max(p.ranks[i], 0), p.rank) : p.rank;
       const uint16_t* w[2 * RT];
 #pragma unroll
-      for (int j = 0; j < 2 * RT; ++j) w[j] = p.a + ((int64_t)i * p.rank + min(8 * j + line, p.rank - 1)) * p.k + 8 * piece;
+      for (int j = 0; j < 2 * RT; ++j)
+        w[j] = p.a + ((int64_t)i * p.rank + min(8 * j + line, p.rank - 1)) * p.k + 8 * piece;
       f32x4 acc[RT];
 #pragma unroll
       for (int j = 0; j < RT; ++j) acc[j] = f32x4{0, 0, 0, 0};
@@ -242,6 +245,7 @@ __global__ __launch_bounds__(64 * kUpWaves) void adapters_up_kernel(AdapterArgs 
   const int tile1 = min((run + 1) * a.run, a.up_tiles);
   // what a tile needs of base and of t, requested while the one before is computed
   struct Tile { uint4 base[4][NB], high[S], low[KS ? S : 1]; };
+  const char* base_at = static_cast<const char*>(p.base);
   auto request = [&](Tile& f, int tile) {
     const int r0 = tile * a.up_tile, r1 = tile < tile1 ? min(r0 + a.up_tile, p.rows) : 0;
 #pragma unroll
@@ -249,8 +253,8 @@ __global__ __launch_bounds__(64 * kUpWaves) void adapters_up_kernel(AdapterArgs 
       const int row = r0 + 4 * group + i;
 #pragma unroll
       for (int h = 0; h < NB; ++h)
-        f.base[i][h] = load16_once(static_cast<const char*>(p.base) + ((int64_t)row * p.base_stride + c) * (F32 ? 4 : 2) + 16 * h,
-                              p.base && in && row < r1);
+        f.base[i][h] = load16_once(base_at + ((int64_t)row * p.base_stride + c) * (F32 ? 4 : 2) + 16 * h,
+                                   p.base && in && row < r1);
     }
     // of token l % 16: rows of requests without an adapter hold anything, and are not used
     const int64_t t = (int64_t)(r0 + col) * p.rank + r_at;
@@ -359,14 +363,14 @@ __global__ __launch_bounds__(64 * kRowWaves) void adapters_row_kernel(AdapterArg
   const int c0 = chunk * a.run, c1 = min(c0 + a.run, p.n);       // run: columns of a workgroup
   // base: eight columns a thread and piece
   constexpr int NB = F32 ? 2 : 1;
+  const char* base_at = static_cast<const char*>(p.base);
   uint4 base[kRowPieces][NB];
 #pragma unroll
   for (int o = 0; o < kRowPieces; ++o) {
     const int c = c0 + 8 * ((int)threadIdx.x + 64 * kRowWaves * o);
 #pragma unroll
     for (int h = 0; h < NB; ++h)
-      base[o][h] = load16(static_cast<const char*>(p.base) + ((int64_t)row * p.base_stride + c) * (F32 ? 4 : 2) + 16 * h,
-                          p.base && c < c1);
+      base[o][h] = load16(base_at + ((int64_t)row * p.base_stride + c) * (F32 ? 4 : 2) + 16 * h, p.base && c < c1);
   }
   // x: eight of k a lane and piece
   const uint16_t* xr = p.x + (int64_t)row * p.x_stride;

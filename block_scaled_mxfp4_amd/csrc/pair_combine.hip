@@ -1,10 +1,13 @@
 // The weighted sum of each token's expert rows and its gradients
 // (situ_moe_combine, situ_moe_combine_backward).
 //
-// Both move rows and compute little: HBM bounds them.  A lane takes eight columns
+// Both move rows and compute little: HBM bounds them (8192 tokens of an EP8 shard,
+// 16 x 3584: 29 us, 6.1 TB/s, part of it from the caches; the gradients of 4095 x 16
+// x 3584: 185 us, 5.2 TB/s).  A lane takes eight columns
 // (16 bytes of bf16), a wave 512.  The token's rows and weights are read by its
 // first lanes together, those that are not local drop out of a ballot, and the
 // others' rows are requested four at a time from addresses the whole wave shares.
+// Local weights of 0 are products too, as the formula has them.
 #include <algorithm>
 
 #include "routed.hpp"
@@ -14,7 +17,9 @@ namespace situ {
 
 namespace {
 
-constexpr int kCols = 512;            // of a wave
+constexpr int kCols = 512;            // of a wave at once
+// Of them a wave of the sum takes two (8192 tokens, an eighth of 16 x 3584: 29.2 us; one 31.2, four 31.2).
+constexpr int kPieces = 2;
 constexpr int kAtOnce = 4;            // rows requested together
 constexpr int kWaves = 4;             // of a workgroup
 
@@ -37,7 +42,8 @@ template <bool F32>
 __device__ __forceinline__ Eight<F32> load8_once(const void* p, int64_t at) {
   const i32x4* q = reinterpret_cast<const i32x4*>(static_cast<const char*>(p) + at * (F32 ? 4 : 2));
   if constexpr (F32)
-    return {__builtin_bit_cast(uint4, __builtin_nontemporal_load(q)), __builtin_bit_cast(uint4, __builtin_nontemporal_load(q + 1))};
+    return {__builtin_bit_cast(uint4, __builtin_nontemporal_load(q)),
+            __builtin_bit_cast(uint4, __builtin_nontemporal_load(q + 1))};
   else
     return {__builtin_bit_cast(uint4, __builtin_nontemporal_load(q))};
 }
@@ -50,7 +56,10 @@ __device__ __forceinline__ void widen(const Eight<F32>& v, float f[8]) {
     for (int i = 0; i < 4; ++i) { f[i] = __uint_as_float(w[i]); f[4 + i] = __uint_as_float(u[i]); }
   } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) { f[2 * i] = bf16_to_f32(w[i] & 0xffffu); f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u); }
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = bf16_to_f32(w[i] & 0xffffu);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
   }
 }
 template <bool F32>
@@ -88,39 +97,45 @@ template <bool YF, bool OF>
 __global__ __launch_bounds__(64 * kWaves) void pair_combine_kernel(situ_moe_combine_t p, int parts, int64_t items) {
   const int lane = lane_id();
   for (int64_t item = (int64_t)blockIdx.x * kWaves + wave_id(); item < items; item += (int64_t)gridDim.x * kWaves) {
-    const int64_t t = (uint32_t)item / (uint32_t)parts;
-    const int col = (int)(item - t * parts) * kCols + 8 * lane;
-    const bool in = col < p.hidden;
-    float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    const int64_t t = (uint32_t)item / (uint32_t)parts;         // items: 512 columns each of what lies in memory
+    const int col = (int)(item - t * parts) * kCols * kPieces + 8 * lane;
+    float acc[kPieces][8] = {};
     for (int first = 0; first < p.top_k; first += kWave) {
       int row;
       float w;
       load_slot(p, t, first + lane, p.top_k, row, w);
       uint64_t local = __ballot(row >= 0);
       while (local) {
-        Eight<YF> v[kAtOnce];
+        Eight<YF> v[kAtOnce][kPieces];
         float wt[kAtOnce];
 #pragma unroll
         for (int i = 0; i < kAtOnce; ++i) {
           wt[i] = 0.0f;
-          v[i] = Eight<YF>{};
+#pragma unroll
+          for (int o = 0; o < kPieces; ++o) v[i][o] = Eight<YF>{};
           if (local) {
             const int s = next_bit(local);
             wt[i] = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, w), s));
             const int64_t r = __builtin_amdgcn_readlane(row, s);
-            if (in) v[i] = load8<YF>(p.y, r * p.y_stride + col);
+#pragma unroll
+            for (int o = 0; o < kPieces; ++o)
+              if (col + kCols * o < p.hidden) v[i][o] = load8<YF>(p.y, r * p.y_stride + col + kCols * o);
           }
         }
 #pragma unroll
-        for (int i = 0; i < kAtOnce; ++i) {
-          float f[8];
-          widen<YF>(v[i], f);
+        for (int i = 0; i < kAtOnce; ++i)
 #pragma unroll
-          for (int c = 0; c < 8; ++c) acc[c] = fmaf(wt[i], f[c], acc[c]);
-        }
+          for (int o = 0; o < kPieces; ++o) {
+            float f[8];
+            widen<YF>(v[i][o], f);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) acc[o][c] = fmaf(wt[i], f[c], acc[o][c]);
+          }
       }
     }
-    if (in) store8<OF>(p.out, t * p.out_stride + col, acc);
+#pragma unroll
+    for (int o = 0; o < kPieces; ++o)
+      if (col + kCols * o < p.hidden) store8<OF>(p.out, t * p.out_stride + col + kCols * o, acc[o]);
   }
 }
 
@@ -198,7 +213,7 @@ unsigned grid_of(int64_t items) { return (unsigned)std::min<int64_t>((items + kW
 }  // namespace
 
 hipError_t launch_pair_combine(const situ_moe_combine_t& p, hipStream_t s) {
-  const int parts = (p.hidden + kCols - 1) / kCols;
+  const int parts = (p.hidden + kPieces * kCols - 1) / (kPieces * kCols);
   const int64_t items = (int64_t)p.tokens * parts;
   const dim3 grid(grid_of(items)), threads(64 * kWaves);
   const bool yf = p.y_dtype == SITU_OUT_F32, of = p.out_dtype == SITU_OUT_F32;

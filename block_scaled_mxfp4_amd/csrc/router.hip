@@ -6,16 +6,15 @@
 //
 // Choice without sorting.  Where top_k of the 64 lanes' largest logits reach a
 // threshold, the top_k largest of all do; a bisection on the lanes' largest finds
-// one that few more do.  What
-// reaches it (some 1.3 top_k) is packed into LDS, one candidate a lane, and a
-// candidate's place is the number of candidates before it.  Where more than 64
-// reach it (many equals; top_k near 64), the wave takes its largest remaining
-// key top_k times instead.
+// one that hardly more do.  What reaches it (some 1.3 top_k) is packed into LDS,
+// one candidate a lane, and a candidate's place is the number of candidates before
+// it.  Where more than 64 reach it (many equals; top_k near 64), the wave takes
+// the largest that is left top_k times instead.
 //
 // A selection by sigmoid + bias is compared in 64 bits, since the neighbours of
-// 900 experts lie as near as fp32 rounds.  The threshold is taken on fp32 scores and
-// lowered by more than twice their error, and only where two candidates are nearer
-// than that are the candidates' scores computed again in 64 bits.
+// 900 experts lie as near as fp32 rounds.  The threshold is taken on fp32 scores
+// and lowered by more than twice their error, and only where two candidates are
+// nearer than that are the candidates' scores computed again in 64 bits.
 //
 // Sigmoid scores are held divided by e^min(zmax, 0), which leaves their shares as
 // they are: a row whose scores all underflow keeps its weights.
@@ -24,6 +23,11 @@
 // waves add theirs in LDS, and each workgroup writes partial sums and counts; a
 // second launch adds them in a fixed order, and its last workgroup (by a ticket)
 // takes the loss.  One workgroup finishes by itself.
+//
+// Bound by HBM and the vector units alike: 32768 x 896 fp32 with the loss takes 33
+// us and 6 for the second launch, against 20 for the logits at HBM's rate and 27
+// for the 415 vector instructions of a token.  More registers a wave (a token's
+// logits ahead: 42 us) or fewer waves (512 workgroups: 42) did worse.
 #include <algorithm>
 
 #include "common.hpp"
@@ -69,7 +73,8 @@ __device__ __forceinline__ float load_one(const void* logits, int64_t at) {
 
 // The logits of a row, -inf past the last expert.
 template <bool BF, int V, int J>
-__device__ __forceinline__ void load_row(const void* logits, int64_t at, int lane, int experts, bool vec, float z[V * J]) {
+__device__ __forceinline__ void load_row(const void* logits, int64_t at, int lane, int experts, bool vec,
+                                         float z[V * J]) {
 #pragma unroll
   for (int j = 0; j < J; ++j) {
     const int e = 64 * V * j + V * lane;
@@ -300,8 +305,11 @@ __global__ __launch_bounds__(64 * kRouterWaves, 4) void router_kernel(RouterArgs
       if constexpr (BIAS) {
 #pragma unroll
         for (int i = 0; i < N; ++i)
-          cd.wide[BIAS ? 64 * i + lane : 0] =
-              c[BIAS ? i : 0] > -__builtin_inff() ? key_of(1.0 / (1.0 + exp(-(double)z[i])) + (double)bias[BIAS ? i : 0]) : 0;
+        {
+          const bool can = c[BIAS ? i : 0] > -__builtin_inff();
+          const double score64 = 1.0 / (1.0 + exp(-(double)z[i])) + (double)bias[BIAS ? i : 0];
+          cd.wide[BIAS ? 64 * i + lane : 0] = can ? key_of(score64) : 0;
+        }
       }
       wave_lds();
       uint64_t last = ~0ull;
@@ -448,14 +456,15 @@ __global__ __launch_bounds__(64 * kFinishWaves) void router_finish_kernel(Router
   }
 }
 
-// The gradient.  With a the scores up to the row's factor, P = a / sum a, q =
-// a / (sum of the chosen):
+// The gradient, bound by HBM (16384 x 896 fp32: 24 us, 4.9 TB/s).  With a the
+// scores up to the row's factor, P = a / sum a, q = a / (sum of the chosen):
 //   renormalized  x_i = scale q_i (dw_i - sum q dw)     else  x_i = score_i scale dw_i
 //   dz_e = P_e (g_e - sum P g) + x_e     (softmax, not renormalized: - P_e sum x)
 // and for sigmoid the whole times 1 - sigmoid(z_e).  A row of floats by expert
 // in LDS takes the x to the lanes that hold their experts.
 template <bool BF, bool BFO, int V, int J, bool SIG>
-__global__ __launch_bounds__(64 * kBackWaves) void router_backward_kernel(situ_moe_router_backward_t p, int vec, int vec_out) {
+__global__ __launch_bounds__(64 * kBackWaves) void router_backward_kernel(situ_moe_router_backward_t p, int vec,
+                                                                          int vec_out) {
   constexpr int N = V * J;
   __shared__ float rows[kBackWaves][64 * N];
   const int lane = lane_id(), wave = wave_id();
@@ -592,10 +601,11 @@ void router_sized(const RouterArgs& a, int blocks, hipStream_t s) {
 
 template <bool BF, bool BFO, int V, int J>
 void backward_scored(const situ_moe_router_backward_t& p, int vec, int vec_out, int blocks, hipStream_t s) {
+  const dim3 grid(blocks), threads(64 * kBackWaves);
   if (p.scoring == SITU_SCORE_SOFTMAX)
-    hipLaunchKernelGGL((router_backward_kernel<BF, BFO, V, J, false>), dim3(blocks), dim3(64 * kBackWaves), 0, s, p, vec, vec_out);
+    hipLaunchKernelGGL((router_backward_kernel<BF, BFO, V, J, false>), grid, threads, 0, s, p, vec, vec_out);
   else
-    hipLaunchKernelGGL((router_backward_kernel<BF, BFO, V, J, true>), dim3(blocks), dim3(64 * kBackWaves), 0, s, p, vec, vec_out);
+    hipLaunchKernelGGL((router_backward_kernel<BF, BFO, V, J, true>), grid, threads, 0, s, p, vec, vec_out);
 }
 template <bool BF, bool BFO>
 void backward_sized(const situ_moe_router_backward_t& p, int vec, int vec_out, int blocks, hipStream_t s) {
@@ -626,8 +636,8 @@ hipError_t launch_router(const situ_moe_router_t& p, hipStream_t s) {
   a.vec = at_once(p.logits, p.logits_stride, bf, p.experts);
   const bool balance = p.counts != nullptr;
   // without the loss nothing is shared: as many workgroups as there are tokens for
-  const int blocks = balance ? router_blocks(p.tokens)
-                             : (int)std::min<int64_t>(((int64_t)p.tokens + kRouterWaves - 1) / kRouterWaves, 8 * kRouterBlocks);
+  const int groups = (p.tokens + kRouterWaves - 1) / kRouterWaves;
+  const int blocks = balance ? router_blocks(p.tokens) : std::min(groups, 8 * kRouterBlocks);
   if (balance && blocks > 1) {
     const int64_t part = (int64_t)router_blocks(p.tokens) * p.experts;
     a.part_sum = static_cast<float*>(p.workspace);
@@ -638,13 +648,15 @@ hipError_t launch_router(const situ_moe_router_t& p, hipStream_t s) {
   else router_sized<false>(a, blocks, s);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || !balance || blocks == 1) return e;
-  hipLaunchKernelGGL(router_finish_kernel, dim3((p.experts + kFinishExperts - 1) / kFinishExperts), dim3(64 * kFinishWaves), 0, s, a, blocks);
+  const dim3 grid((p.experts + kFinishExperts - 1) / kFinishExperts);
+  hipLaunchKernelGGL(router_finish_kernel, grid, dim3(64 * kFinishWaves), 0, s, a, blocks);
   return hipGetLastError();
 }
 
 hipError_t launch_router_backward(const situ_moe_router_backward_t& p, hipStream_t s) {
   const bool bf = p.logits_dtype == SITU_OUT_BF16, bfo = p.out_dtype == SITU_OUT_BF16;
-  const int vec = at_once(p.logits, p.logits_stride, bf, p.experts), vec_out = at_once(p.d_logits, p.out_stride, bfo, p.experts);
+  const int vec = at_once(p.logits, p.logits_stride, bf, p.experts);
+  const int vec_out = at_once(p.d_logits, p.out_stride, bfo, p.experts);
   const int blocks = (int)std::min<int64_t>(((int64_t)p.tokens + kBackWaves - 1) / kBackWaves, kBackBlocks);
   if (bf) {
     if (bfo) backward_sized<true, true>(p, vec, vec_out, blocks, s);
