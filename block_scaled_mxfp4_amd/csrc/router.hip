@@ -116,15 +116,16 @@ __device__ __forceinline__ void load_row(const void* logits, int64_t at, int lan
 }
 
 // Scores of a row, up to a factor the whole row shares: e^(z - zmax), or
-// sigmoid(z) e^-min(zmax, 0).  FAR: the shift is next to the type's lowest value,
-// where its product with log2 e overflows; the difference is taken first.
+// sigmoid(z) e^-min(zmax, 0).  FAR: the difference is taken first.  Otherwise the
+// rounding of shift log2 e is a factor of the row too, 2^-25 |shift| log2 e in the
+// exponent: near 1 up to the 2^20 of is_far, but past fp32's range from 2^31 on.
 template <bool SIG, bool FAR>
 __device__ __forceinline__ float score(float z, float shift) {
   const float x = SIG ? fminf(z, 0.0f) : z;
   const float n = FAR ? e_to(x - shift) : __builtin_amdgcn_exp2f(fmaf(x, kL2e, -shift * kL2e));
   return SIG ? n * __builtin_amdgcn_rcpf(1.0f + e_to(-fabsf(z))) : n;
 }
-__device__ __forceinline__ bool is_far(float shift) { return fabsf(shift) > 0x1p100f; }
+__device__ __forceinline__ bool is_far(float shift) { return fabsf(shift) > 0x1p20f; }
 template <bool SIG>
 __device__ __forceinline__ float score(float z, float shift) {
   return is_far(shift) ? score<SIG, true>(z, shift) : score<SIG, false>(z, shift);

@@ -210,6 +210,24 @@ def test_router_far_scores():
     assert not ((ids == 3) | (ids == 5)).any() and (ids[:, 0] == 4).all()
 
 
+@pytest.mark.parametrize("size", [2.0 ** 19, 2.0 ** 20, 2.0 ** 21, 1e8, 2e9, 1e10, 1e20, 2.0 ** 100, 1e38])
+def test_router_large_logits(size):
+    """Logits far from 0 (equals, or neighbours that differ by one step of fp32) have the scores of their differences."""
+    g = gen_of(12)
+    T, E, k = 40, 200, 8
+    step = size * 2.0 ** -23
+    for sign in (1, -1):
+        z = sign * (size - step * torch.randint(0, 4, (T, E), generator=g, device="cuda").to(D))
+        z[0] = sign * size
+        z[1, 5:] = -size
+        z = z.float()
+        for scoring in ("softmax", "sigmoid"):
+            for renormalize in (True, False):
+                ids, _, _, counts, _, _ = run(z, k, scoring, None, renormalize, 1.0, weights_dtype=F32)
+                dw = torch.randn(T, k, generator=g, device="cuda")
+                check_backward(z, ids, dw, scoring, renormalize, 1.0, None, counts, torch.ones(1, device="cuda"))
+
+
 def test_router_nan():
     """A NaN is never chosen, and shows in the loss; other rows' ids and weights are their own."""
     z = torch.randn(70, 96, generator=gen_of(11), device="cuda")
