@@ -106,7 +106,7 @@ __device__ __forceinline__ float act(float g, float u, const RowK& k) {
     return (n1 * n3) * __builtin_amdgcn_rcpf(fmaf(t, e, t)) * (k.b * k.l);
   } else {
     const float e = __builtin_amdgcn_exp2f(k.b * g * -kL2e);
-    return g * (u + k.l) * __builtin_amdgcn_rcpf(1.0f + e);
+    return g * __builtin_amdgcn_rcpf(1.0f + e) * (u + k.l);      // the small factor first: g u may overflow
   }
 }
 
@@ -137,15 +137,18 @@ __device__ __forceinline__ void act_backward(float g, float u, float dh, const R
     sigmoid_both(g, s, left);
     const float gate = k.b * t1 * s, up = k.l * t3;
     h = gate * up;
-    dg = dh * up * fmaf(gate, left, s1 * s);
+    dg = dh * fmaf(gate, left, s1 * s) * up;
     du = dh * gate * s3;
   } else {
     float s, left;
-    const float x = k.b * g;
+    float x = k.b * g;
+    // an overflow to infinity would meet a factor of 0; s is 0 or 1 from 2^7 on.  A NaN stays one
+    if constexpr (KIND == SITU_ACTIVATION_SWIGLU_BIAS)
+      x = __builtin_elementwise_maximum(__builtin_elementwise_minimum(x, 0x1p20f), -0x1p20f);
     sigmoid_both(x, s, left);
     const float gate = g * s, up = u + k.l;
     h = gate * up;
-    dg = dh * up * (s * fmaf(x, left, 1.0f));
+    dg = dh * (s * fmaf(x, left, 1.0f)) * up;
     du = dh * gate;
   }
 }

@@ -173,6 +173,27 @@ def test_rows_of_no_group_stay(kind):
 
 
 @pytest.mark.parametrize("kind", list(KINDS))
+def test_lowest_values(kind):
+    """The type's largest magnitudes, as masks leave them: the formulas' limits, though products on the way overflow."""
+    low = torch.finfo(BF).min
+    con = {n: torch.tensor([1.7], device="cuda") for n in KINDS[kind]}
+    vals = torch.tensor([low, -low, 1e20, -1e20, 2.0 ** 21, -2.0 ** 21, 1000.0, -1000.0], dtype=BF, device="cuda")
+    g, u = torch.meshgrid(vals, torch.cat([vals, torch.tensor([0.0, 3.0, -0.5], dtype=BF, device="cuda")]), indexing="ij")
+    g, u = (t.reshape(1, -1) for t in (g, u))                   # 88 columns
+    h = B.situ_moe_activation(torch.cat([g, u], 1), activation=kind, **con)
+    for dh in (1.0, -0.02, 0.0):
+        d_h = torch.full_like(g, dh)
+        d, again = B.situ_moe_activation_backward(d_h, torch.cat([g, u], 1), activation=kind, recompute=True, **con)
+        p = [con[n].to(D) for n in KINDS[kind]]
+        wh, wg, wu, *_ = formulas(kind, g.to(D), u.to(D), d_h.to(D), p)
+        # exponentials are 0 here and tanh and the sigmoid 0 or 1 up to 6 u; 1000 c rounds u + c by u of it
+        for got, want in ((h, wh), (again, wh), (d[:, :88], wg), (d[:, 88:], wu)):
+            over = torch.isinf(want.to(F32).to(BF))
+            assert torch.equal(got[over], want[over].to(F32).to(BF))
+            assert ((got[~over].to(D) - want[~over]).abs() <= (2.0 ** -8 + 64 * U) * want[~over].abs()).all()
+
+
+@pytest.mark.parametrize("kind", list(KINDS))
 def test_not_finite(kind):
     """NaN and infinities stay in their element; large magnitudes saturate as the formulas do."""
     con = {n: torch.tensor([1.5], device="cuda") for n in KINDS[kind]}
