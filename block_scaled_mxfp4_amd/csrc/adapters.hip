@@ -544,8 +544,9 @@ hipError_t launch_adapters(const situ_moe_adapters_t& p, hipStream_t s) {
   if (e != hipSuccess) return e;
   a.up_tiles = (p.rows + a.up_tile - 1) / a.up_tile;
   a.chunks = (p.n + 127) / 128;
-  // tiles of a wave: as many as leave 3072 waves, three a SIMD
-  a.run = (int)std::min<int64_t>(std::max<int64_t>(1, ((int64_t)a.up_tiles * a.chunks + 3071) / 3072), a.up_tiles);
+  // tiles of a wave: as many as leave three waves a SIMD
+  constexpr int64_t kUpItems = 256 * 4 * 3;
+  a.run = (int)std::min<int64_t>(std::max<int64_t>(1, ((int64_t)a.up_tiles * a.chunks + kUpItems - 1) / kUpItems), a.up_tiles);
   const int64_t items = (int64_t)((a.up_tiles + a.run - 1) / a.run) * a.chunks;
   if (p.out_dtype == SITU_OUT_F32) up_go<true>(a, items, s);
   else up_go<false>(a, items, s);

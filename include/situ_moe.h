@@ -384,9 +384,11 @@ const char* situ_moe_grouped_matmul_kernel(int32_t direction, const situ_moe_gro
  *                experts); 0 if C is 0
  * Where the batch lies on several ranks, the counts and prob_sums are summed
  * over them and the loss follows from the sums.
- * A NaN logit makes its row's softmax, and so the loss, NaN; so does +inf.
+ * A NaN logit makes its row's scores, and so the loss, NaN (so does +inf, for
+ * softmax), but for a row without any logit above -inf, which has no part.
  * ids, packed and weights feed topk_ids, topk_packed and topk_weights of the
  * layer (an id of -1 is outside every shard; packed, 0xFFFF is).
+ * Outputs must not overlap inputs.
  * Sizes: tokens 0 .. 2^24, experts 1 .. 1024, top_k 1 .. min(experts, 64). */
 enum { SITU_SCORE_SOFTMAX = 0, SITU_SCORE_SIGMOID = 1 };
 typedef struct situ_moe_router_t {
@@ -421,7 +423,8 @@ situ_status situ_moe_router(const situ_moe_router_t* args, void* hip_stream);
  * an id that a row holds twice counts twice).  counts are those of the loss (of
  * all ranks, if it was taken over them) and are constants of it, as the choice
  * is.  d_weights or counts and d_loss may be NULL: that part is 0.  Rows of
- * masked tokens, and of tokens without a logit above -inf, are 0. */
+ * masked tokens, and of tokens without a logit above -inf, are 0.  d_logits must
+ * not overlap the inputs. */
 typedef struct situ_moe_router_backward_t {
   int32_t tokens, experts, top_k;
   int32_t scoring, logits_dtype;
@@ -486,8 +489,8 @@ situ_status situ_moe_activation_backward(const situ_moe_activation_t* args, void
  * the workspace; a value outside [0, rows) is a pair that is not local.  For the
  * gradient each row belongs to one pair at most; rows of no pair are not written.
  * hidden a multiple of 8 up to 2^18, rows and tokens 0 .. 2^24, top_k 1 .. 1024.
- * Arrays 16-byte aligned, strides a multiple of 8 elements.  dy may be y
- * itself; otherwise outputs must not overlap inputs. */
+ * Rows of y, out and dy start on 16 bytes.  dy may be y itself (the same address
+ * and stride); otherwise outputs must not overlap inputs. */
 typedef struct situ_moe_combine_t {
   int32_t tokens, top_k, hidden;
   int32_t rows;               /* rows of y */
@@ -515,9 +518,11 @@ situ_status situ_moe_combine_backward(const situ_moe_combine_t* args, void* hip_
  * leading rows of a[i] (and columns of b[i]) that count, NULL: all; scales
  * NULL: 1.  Sums, and a[i] x[r] between the two products, are held to fp32
  * accuracy (the second product takes it as two bf16 terms, 2^-16 of it); one
- * rounding at the end for bf16.  k, n and rank multiples of 8, k and n up to 2^18,
- * rank up to 256, rows 0 .. 2^24, requests and adapters 1 .. 2^20.  x, a, b, base and out
- * 16-byte aligned, strides a multiple of 8 elements. */
+ * rounding at the end for bf16.  An infinity in b[i] makes its column infinite
+ * or NaN in the request's rows.  k, n and rank multiples of 8, k and n up to 2^18,
+ * rank up to 256, rows 0 .. 2^24, requests and adapters 1 .. 2^20.  Rows of x, a, b,
+ * base and out start on 16 bytes.  Except for out and base, outputs and workspace must
+ * not overlap inputs. */
 typedef struct situ_moe_adapters_t {
   int32_t rows, n, k;
   int32_t rank;               /* of a and b */
