@@ -154,10 +154,10 @@ __device__ __forceinline__ uint64_t readlane64(uint64_t v, int lane) {
          (uint32_t)__builtin_amdgcn_readlane((int)v, lane);
 }
 
-// A wave's row of logits by expert, and the candidates' ids.  The row's place takes the scores in 64 bits where more
+// A wave's row of logits by expert, and the candidates' ids, then what they are ordered by.  The row's place takes the scores in 64 bits where more
 // than 64 candidates ask for them.
 template <int N, bool BIAS>
-struct WaveRow {
+struct alignas(16) WaveRow {
   union {
     float z[64 * N];
     uint64_t wide[BIAS ? 64 * N : 1];
@@ -264,20 +264,36 @@ __global__ __launch_bounds__(64 * kRouterWaves, 4) void router_kernel(RouterArgs
     int id = -1, place = lane;                       // a lane's expert and its place in the row
     float zc = 0.0f;
     if (n <= 64) {
-      if (lane < n) {
-        id = cd.id[lane];
+      // a candidate's place is the number of those before it: four at a time from LDS, and up to 32 of them by both
+      // halves of the wave, each against half of them
+      const bool halves = n <= 32;
+      const int sub = halves ? lane & 31 : lane, quads = ((halves ? (n + 1) / 2 : n) + 3) / 4;
+      const int from = halves ? (lane >> 5) * 4 * quads : 0;
+      if (sub < n) {
+        id = cd.id[sub];
         zc = cd.z[id];
       }
-      int before = 0;
+      wave_lds();
+      uint32_t before = 0;
       if constexpr (BIAS) {
         // fp32 tells all of them apart but for a token in some hundreds
-        const float b = lane < n ? biases[id] : 0.0f;
+        const float b = sub < n ? biases[id] : 0.0f;
         const float mine = __builtin_amdgcn_rcpf(1.0f + e_to(-zc)) + b, apart = 0x1p-19f * (1.0f + fabsf(mine));
-        int near = 0;
-        for (int o = 0; o < n; ++o) {
-          const float other = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, mine), o));
-          before += other > mine;
-          near += !(fabsf(other - mine) > apart);    // itself, and infinities, too
+        uint32_t near = 0;
+        cd.id[lane] = __float_as_int(lane < n ? mine : __builtin_nanf(""));
+        wave_lds();
+        for (int o = 0; o < quads; ++o) {
+          const f32x4 others = *reinterpret_cast<const f32x4*>(&cd.id[from + 4 * o]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            before += others[i] > mine;
+            near += fabsf(others[i] - mine) <= apart || others[i] == mine;    // itself, and infinities, too
+          }
+        }
+        if (halves) {
+          before = halves_sum(near << 16 | before);
+          near = before >> 16;
+          before &= 0xffffu;
         }
         if (__ballot(lane < n && near > 1)) {
           const uint64_t key = key_of(1.0 / (1.0 + exp(-(double)zc)) + (double)b);
@@ -289,18 +305,27 @@ __global__ __launch_bounds__(64 * kRouterWaves, 4) void router_kernel(RouterArgs
           }
         }
       } else {
-        // fp32 logits are hardly ever equal, bf16 ones often; equal ones leave places double and others empty
-        const float key = lane < n ? zc : -__builtin_inff();
-        if (!BF)
-          for (int o = 0; o < n; ++o)
-            before += __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, key), o)) > key;
-        if (BF || wave_sum(lane < n ? (float)before : 0.0f) != 0.5f * (float)(n * (n - 1))) {
+        // a bf16 logit leaves room for the id in 32 bits.  fp32 ones are hardly ever equal: equal ones leave places
+        // double and others empty
+        const uint32_t key = BF ? (key_of(zc) & 0xffff0000u) | (uint32_t)(0xffff - id) : key_of(zc);
+        cd.id[lane] = (int32_t)(lane < n ? key : 0u);
+        wave_lds();
+        for (int o = 0; o < quads; ++o) {
+          const uint4 others = *reinterpret_cast<const uint4*>(&cd.id[from + 4 * o]);
+          before += others.x > key;
+          before += others.y > key;
+          before += others.z > key;
+          before += others.w > key;
+        }
+        if (halves) before = halves_sum(before);
+        if (!BF && wave_sum(lane < n ? (float)before : 0.0f) != 0.5f * (float)(n * (n - 1))) {
           const uint64_t key64 = (uint64_t)key_of(zc) << 32 | (uint32_t)~id;
           before = 0;
           for (int o = 0; o < n; ++o) before += readlane64(key64, o) > key64;
         }
       }
-      if (lane < n) place = before;
+      if (lane < n) place = (int)before;
+      else id = -1;                                  // of the other half
     } else {
       // the largest left, top_k times: the largest behind the last one in the order of (key, lowest id)
       if constexpr (BIAS) {
@@ -353,12 +378,12 @@ __global__ __launch_bounds__(64 * kRouterWaves, 4) void router_kernel(RouterArgs
       }
     }
     const float total = p.renormalize ? wave_sum(w) : (SIG ? 1.0f : all);
-    w = chosen ? p.scale * (w / total) : 0.0f;
+    w = chosen ? p.scale * (w * __builtin_amdgcn_rcpf(total)) : 0.0f;
     // the lanes behind the candidates fill the places that none has
     if (chosen || (lane < top_k && (n > 64 || lane >= n))) {
       const int64_t at = row + place;
       p.ids[at] = id;
-      const uint32_t b = f32_to_bf16_rne(w);
+      const uint32_t b = __builtin_bit_cast(uint16_t, (__bf16)w);    // nearest even
       if (p.weights) {
         if (p.weights_dtype == SITU_OUT_F32)
           static_cast<float*>(p.weights)[at] = w;

@@ -33,7 +33,7 @@ __device__ __forceinline__ float wave_sum(float v) {
 }
 template <int kCtrl>
 __device__ __forceinline__ uint32_t dpp_max(uint32_t v) {
-  const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, kCtrl, 0xf, 0xf, false);
+  const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, kCtrl, 0xf, 0xf, true);   // 0 from outside
   return v > o ? v : o;
 }
 __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
@@ -44,6 +44,12 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
   v = dpp_max<0x142>(v);
   v = dpp_max<0x143>(v);
   return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+
+// The sum of lane l and lane l ^ 32, in both.
+__device__ __forceinline__ uint32_t halves_sum(uint32_t v) {
+  const auto both = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  return both[0] + both[1];
 }
 
 }  // namespace situ
