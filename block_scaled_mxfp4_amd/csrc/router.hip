@@ -6,7 +6,8 @@
 //
 // Choice without sorting.  Where top_k of the 64 lanes' largest logits reach a
 // threshold, the top_k largest of all do; a bisection on the lanes' largest finds
-// one that hardly more do.  What reaches it (some 1.3 top_k) is packed into LDS,
+// one that hardly more do (over their values, three or four steps, where one over the
+// float's bits takes ten: 32768 x 64 17 us for 24).  What reaches it (some 1.3 top_k) is packed into LDS,
 // one candidate a lane, and a candidate's place is the number of candidates before
 // it.  Where more than 64 reach it (many equals; top_k near 64), the wave takes
 // the largest that is left top_k times instead.
@@ -24,10 +25,12 @@
 // second launch adds them in a fixed order, and its last workgroup (by a ticket)
 // takes the loss.  One workgroup finishes by itself.
 //
-// Bound by HBM and the vector units alike: 32768 x 896 fp32 with the loss takes 33
-// us and 6 for the second launch, against 20 for the logits at HBM's rate and 27
-// for the 415 vector instructions of a token.  More registers a wave (a token's
-// logits ahead: 42 us) or fewer waves (512 workgroups: 42) did worse.
+// Bound by instruction issue and HBM alike: 32768 x 896 fp32 with the loss takes 29
+// us and 6 for the second launch, against 20 for the logits at HBM's rate and 22
+// for the 350 vector instructions of a token.  Up to 128 experts the CU's one scalar
+// unit binds as much as the vector units (32768 x 64: 17 us, some 170 instructions a
+// token of each); there and with few registers, logits requested a token ahead gained
+// nothing, and at 896 experts they cost (42 us, by the registers).
 #include <algorithm>
 
 #include "common.hpp"
@@ -215,12 +218,14 @@ __global__ __launch_bounds__(64 * kRouterWaves, 4) void router_kernel(RouterArgs
     const float zmax = wave_most(best);
     const bool live = zmax > -__builtin_inff();      // the row has an expert to choose
     // what is compared: the logit, or the fp32 score with its bias
-    float c[BIAS ? N : 1], top = zmax;
+    float c[BIAS ? N : 1], sig[BIAS && BAL ? N : 1], top = zmax;
     if constexpr (BIAS) {
       best = -__builtin_inff();
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        c[i] = z[i] > -__builtin_inff() ? __builtin_amdgcn_rcpf(1.0f + e_to(-z[i])) + bias[i] : -__builtin_inff();
+        const float sigmoid = __builtin_amdgcn_rcpf(1.0f + e_to(-z[i]));
+        if constexpr (BAL) sig[i] = sigmoid;
+        c[i] = z[i] > -__builtin_inff() ? sigmoid + bias[i] : -__builtin_inff();
         best = fmaxf(best, c[i]);
       }
       top = wave_most(best);
@@ -229,19 +234,32 @@ __global__ __launch_bounds__(64 * kRouterWaves, 4) void router_kernel(RouterArgs
     // them), or the lowest value of all: every expert that can be chosen
     float least = -3.40282347e38f;
     const bool some = best > -__builtin_inff();
-    if (__popcll(__ballot(some)) >= top_k) {
-      uint32_t lo = key_of(-wave_most(some ? -best : -__builtin_inff())), hi = key_of(top);
-      while (hi > lo + 1) {
+    int reach = __popcll(__ballot(some));
+    if (reach >= top_k) {
+      const float low = -wave_most(some ? -best : -__builtin_inff());
+      // by values first, a few steps where they are spread evenly; by keys where they span magnitudes or are infinite
+      const float step = (top - low) * 0x1p-8f;
+      int at = 0;
+      for (int w = 128; w && reach > top_k + 4; w /= 2) {
+        const int n = __popcll(__ballot(best >= fmaf((float)(at + w), step, low)));
+        if (n >= top_k) {
+          at += w;
+          reach = n;
+        }
+      }
+      least = at ? fmaf((float)at, step, low) : low;
+      uint32_t lo = key_of(least), hi = key_of(top);
+      while (reach > top_k + 4 && hi > lo + 1) {
         const uint32_t mid = lo + (hi - lo) / 2;
         const int n = __popcll(__ballot(best >= value_of(mid)));
         if (n >= top_k) {
           lo = mid;
-          if (n <= top_k + 2) break;
+          reach = n;
         } else {
           hi = mid;
         }
       }
-      least = fmaxf(value_of(lo), least);
+      least = fmaxf(value_of(lo), -3.40282347e38f);
       // the k-th largest fp32 score is `least` at the least; one is off by less than 2^-21 + 2^-23 of its magnitude
       if (BIAS && least < __builtin_inff()) least = fmaxf(least - 0x1p-19f * (1.0f + fabsf(least)), -3.40282347e38f);
     }
@@ -366,7 +384,12 @@ __global__ __launch_bounds__(64 * kRouterWaves, 4) void router_kernel(RouterArgs
     float all = 0.0f;
     if (live && (BAL || (!SIG && !p.renormalize))) {
       float s[N];
-      scores<SIG, N>(z, SIG ? fminf(zmax, 0.0f) : zmax, s);
+      if (SIG && zmax > -4.0f) {                       // none is lost that is 2^-120 of the largest
+#pragma unroll
+        for (int i = 0; i < N; ++i) s[i] = BIAS && BAL ? sig[BIAS && BAL ? i : 0] : __builtin_amdgcn_rcpf(1.0f + e_to(-z[i]));
+      } else {
+        scores<SIG, N>(z, SIG ? fminf(zmax, 0.0f) : zmax, s);
+      }
 #pragma unroll
       for (int i = 0; i < N; ++i) all += s[i];
       all = wave_sum(all);
@@ -661,11 +684,14 @@ hipError_t launch_router(const situ_moe_router_t& p, hipStream_t s) {
   const bool bf = p.logits_dtype == SITU_OUT_BF16;
   a.vec = at_once(p.logits, p.logits_stride, bf, p.experts);
   const bool balance = p.counts != nullptr;
-  // without the loss nothing is shared: as many workgroups as there are tokens for
+  // Without the loss, more workgroups (32768 x 256, sigmoid and bias: 1536 23.1 us, 768 23.7, 1024 24.5, 4096 26.6).
+  // With it and a bias, the rows of over 512 experts leave LDS for two workgroups a CU (32768 x 896: 512 52.6 us, 768 58).
   const int groups = (p.tokens + kRouterWaves - 1) / kRouterWaves;
-  const int blocks = balance ? router_blocks(p.tokens) : std::min(groups, 8 * kRouterBlocks);
+  const int blocks = !balance                       ? std::min(groups, 2 * kRouterBlocks)
+                     : p.bias && p.experts > 512 ? std::min(router_blocks(p.tokens), 512)
+                                                 : router_blocks(p.tokens);
   if (balance && blocks > 1) {
-    const int64_t part = (int64_t)router_blocks(p.tokens) * p.experts;
+    const int64_t part = (int64_t)blocks * p.experts;
     a.part_sum = static_cast<float*>(p.workspace);
     a.part_count = reinterpret_cast<int32_t*>(a.part_sum + part);
     a.ticket = reinterpret_cast<uint32_t*>(a.part_count + part);
