@@ -137,8 +137,8 @@ __device__ __forceinline__ void act_backward(float g, float u, float dh, const R
     sigmoid_both(g, s, left);
     const float gate = k.b * t1 * s, up = k.l * t3;
     h = gate * up;
-    dg = dh * fmaf(gate, left, s1 * s) * up;
-    du = dh * gate * s3;
+    dg = dh * up * fmaf(gate, left, s1 * s);         // |up| is at most l (the factor first: 110 us for 106)
+    du = dh * (gate * s3);
   } else {
     float s, left;
     float x = k.b * g;
