@@ -7,7 +7,7 @@
 // Choice without sorting.  Where top_k of the 64 lanes' largest logits reach a
 // threshold, the top_k largest of all do; a bisection on the lanes' largest finds
 // one that hardly more do (over their values, three or four steps, where one over the
-// float's bits takes ten: 32768 x 64 17 us for 24).  What reaches it (some 1.3 top_k) is packed into LDS,
+// float's bits takes ten: 32768 x 64 16 us for 24).  What reaches it (some 1.3 top_k) is packed into LDS,
 // one candidate a lane, and a candidate's place is the number of candidates before
 // it.  Where more than 64 reach it (many equals; top_k near 64), the wave takes
 // the largest that is left top_k times instead.
@@ -25,10 +25,10 @@
 // second launch adds them in a fixed order, and its last workgroup (by a ticket)
 // takes the loss.  One workgroup finishes by itself.
 //
-// Bound by instruction issue and HBM alike: 32768 x 896 fp32 with the loss takes 29
+// Bound by instruction issue and HBM alike: 32768 x 896 fp32 with the loss takes 28
 // us and 6 for the second launch, against 20 for the logits at HBM's rate and 22
 // for the 350 vector instructions of a token.  Up to 128 experts the CU's one scalar
-// unit binds as much as the vector units (32768 x 64: 17 us, some 170 instructions a
+// unit binds as much as the vector units (32768 x 64: 16 us, some 160 instructions a
 // token of each); there and with few registers, logits requested a token ahead gained
 // nothing, and at 896 experts they cost (42 us, by the registers).
 #include <algorithm>
@@ -240,26 +240,31 @@ __global__ __launch_bounds__(64 * kRouterWaves, 4) void router_kernel(RouterArgs
       // by values first, a few steps where they are spread evenly; by keys where they span magnitudes or are infinite
       const float step = (top - low) * 0x1p-8f;
       int at = 0;
-      for (int w = 128; w && reach > top_k + 4; w /= 2) {
-        const int n = __popcll(__ballot(best >= fmaf((float)(at + w), step, low)));
+      uint32_t w = 128;
+      while (reach > top_k + 4 && w) {
+        const int mid = at + (int)w, n = __popcll(__ballot(best >= fmaf((float)mid, step, low)));
+        w >>= 1;
         if (n >= top_k) {
-          at += w;
+          at = mid;
           reach = n;
         }
       }
       least = at ? fmaf((float)at, step, low) : low;
-      uint32_t lo = key_of(least), hi = key_of(top);
-      while (reach > top_k + 4 && hi > lo + 1) {
-        const uint32_t mid = lo + (hi - lo) / 2;
-        const int n = __popcll(__ballot(best >= value_of(mid)));
-        if (n >= top_k) {
-          lo = mid;
-          reach = n;
-        } else {
-          hi = mid;
+      if (reach > top_k + 4) {
+        uint32_t lo = key_of(least), hi = key_of(top);
+        while (reach > top_k + 4 && hi > lo + 1) {
+          const uint32_t mid = lo + (hi - lo) / 2;
+          const int n = __popcll(__ballot(best >= value_of(mid)));
+          if (n >= top_k) {
+            lo = mid;
+            reach = n;
+          } else {
+            hi = mid;
+          }
         }
+        least = value_of(lo);
       }
-      least = fmaxf(value_of(lo), -3.40282347e38f);
+      least = fmaxf(least, -3.40282347e38f);
       // the k-th largest fp32 score is `least` at the least; one is off by less than 2^-21 + 2^-23 of its magnitude
       if (BIAS && least < __builtin_inff()) least = fmaxf(least - 0x1p-19f * (1.0f + fabsf(least)), -3.40282347e38f);
     }
