@@ -15,9 +15,14 @@
 // alone: what another request's adapter holds (infinities, NaN) does not reach
 // them.
 //
-// Between the two, t is held as two bf16 terms, high and low, so that no more than
-// 2^-16 of it is lost; with ranks up to 16 both fit in one instruction's 32
-// columns.
+// Between the two, t is held as its output asks for.  For a bf16 out it is two bf16
+// terms, high and low: they lose no more than 2^-16 of it, against the 2^-9 of out's
+// own rounding.  For an fp32 out it is fp32, which the second product takes apart
+// into three bf16 terms, exactly, so that a row has the accuracy that the one
+// launch gives it.  With ranks up to 16 two terms fit in one instruction's 32
+// columns.  Both take 4 bytes a value.  The third term costs the fp32 output 0 to
+// 9 % (8192 rows, 3584 to 7168: rank 16 136 us either way, rank 32 137 us against
+// 130 with two, rank 128 396 against 366).
 #include <algorithm>
 
 #include "routed.hpp"
@@ -31,7 +36,8 @@ constexpr int kUpWaves = 4;
 
 struct AdapterArgs {
   situ_moe_adapters_t p;
-  uint16_t *high, *low;       // t as two bf16 terms, [rows][rank] each
+  uint16_t *high, *low;       // bf16 out: t as two bf16 terms, [rows][rank] each
+  float* t;                   // fp32 out: t, [rows][rank]; else null
   int32_t tile;               // rows of a tile of the first product, 1 .. 16
   int32_t up_tile;            // of the second, 1 .. 16
   int32_t up_tiles;
@@ -124,6 +130,26 @@ __device__ __forceinline__ void two_terms(const f32x4& t, uint2& high, uint2& lo
   high = __builtin_bit_cast(uint2, h);
   low = __builtin_bit_cast(uint2, l);
 }
+// Eight ranks of t as three bf16 terms: eight bits each of its 24, by cutting off, so that nothing is lost and a finite
+// value has finite terms.  A value that is not finite has one term.
+__device__ __forceinline__ void three_terms(const uint4& lo, const uint4& hi, uint4 term[3]) {
+  const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+  uint32_t cut[3][8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float left = __uint_as_float(w[i]);
+#pragma unroll
+    for (int o = 0; o < 3; ++o) {
+      cut[o][i] = __float_as_uint(left) & 0xffff0000u;
+      left -= __uint_as_float(cut[o][i]);
+      left = fabsf(left) < __builtin_inff() ? left : 0.0f;
+    }
+  }
+#pragma unroll
+  for (int o = 0; o < 3; ++o)
+    term[o] = make_uint4(cut[o][0] >> 16 | cut[o][1], cut[o][2] >> 16 | cut[o][3], cut[o][4] >> 16 | cut[o][5],
+                         cut[o][6] >> 16 | cut[o][7]);
+}
 
 // t.  A workgroup takes a tile of rows, its waves every W-th unit of 64 of k.  A unit of x and a is requested by
 // whole lines, eight lanes of 16 bytes a row (rows of 64 bytes, as the matrix instruction holds them, go through the
@@ -198,7 +224,10 @@ __global__ __launch_bounds__(64 * W) void adapters_down_kernel(AdapterArgs a) {
         const int r = 16 * j + 4 * group, row = r0 + col;
 #pragma unroll
         for (int e = 0; e < 4; ++e) t[e] = r + e < rank ? t[e] * c : 0.0f;
-        if (row >= lo && row < hi && r < p.rank) {
+        if (row < lo || row >= hi || r >= p.rank) continue;
+        if (a.t) {
+          *reinterpret_cast<f32x4*>(a.t + (int64_t)row * p.rank + r) = t;
+        } else {
           uint2 high, low;
           two_terms(t, high, low);
           *reinterpret_cast<uint2*>(a.high + (int64_t)row * p.rank + r) = high;
@@ -215,10 +244,11 @@ __global__ __launch_bounds__(64 * W) void adapters_down_kernel(AdapterArgs a) {
 // from 8 (l / 16), and of instruction s column 8 (l % 16) + s, so that it ends with eight consecutive columns of the
 // four tokens 4 (l / 16) ..: 16 bytes of bf16, 256 consecutive ones a token.  A wave takes 128 columns of a run of
 // tiles and keeps its columns of b while the adapter stays the same (KEEP: up to 64 ranks).
-// KS: steps of 32 ranks; 0: at most 16 ranks, the low term beside the high one.
+// KS: steps of 32 ranks; 0: at most 16 ranks, the second term beside the first in one instruction.
 template <int KS, bool F32>
 __global__ __launch_bounds__(64 * kUpWaves) void adapters_up_kernel(AdapterArgs a, int64_t items) {
   constexpr int S = KS ? KS : 1, NB = F32 ? 2 : 1;
+  constexpr int kTerms = F32 ? 3 : 2, kMany = KS ? kTerms : kTerms - 1;    // instructions a step of ranks and column
   constexpr bool KEEP = S <= 2;
   const situ_moe_adapters_t& p = a.p;
   const int lane = lane_id(), col = lane & 15, group = lane >> 4;
@@ -244,7 +274,7 @@ __global__ __launch_bounds__(64 * kUpWaves) void adapters_up_kernel(AdapterArgs 
   };
   const int tile1 = min((run + 1) * a.run, a.up_tiles);
   // what a tile needs of base and of t, requested while the one before is computed
-  struct Tile { uint4 base[4][NB], high[S], low[KS ? S : 1]; };
+  struct Tile { uint4 base[4][NB], t[F32 || KS ? 2 : 1][S]; };   // t: the two terms, or ranks 0 .. 3 and 4 .. 7 in fp32
   const char* base_at = static_cast<const char*>(p.base);
   auto request = [&](Tile& f, int tile) {
     const int r0 = tile * a.up_tile, r1 = tile < tile1 ? min(r0 + a.up_tile, p.rows) : 0;
@@ -261,11 +291,14 @@ __global__ __launch_bounds__(64 * kUpWaves) void adapters_up_kernel(AdapterArgs 
 #pragma unroll
     for (int s = 0; s < S; ++s) {
       const bool on = 32 * s + r_at < p.rank && r0 + col < r1;
-      if constexpr (KS == 0) {
-        f.high[s] = load16((group < 2 ? a.high : a.low) + t, on);
+      if constexpr (F32) {
+        f.t[0][s] = load16(a.t + t + 32 * s, on);
+        f.t[F32 || KS ? 1 : 0][s] = load16(a.t + t + 32 * s + 4, on);
+      } else if constexpr (KS == 0) {
+        f.t[0][s] = load16((group < 2 ? a.high : a.low) + t, on);
       } else {
-        f.high[s] = load16(a.high + t + 32 * s, on);
-        f.low[s] = load16(a.low + t + 32 * s, on);
+        f.t[0][s] = load16(a.high + t + 32 * s, on);
+        f.t[KS ? 1 : 0][s] = load16(a.low + t + 32 * s, on);
       }
     }
   };
@@ -280,6 +313,24 @@ __global__ __launch_bounds__(64 * kUpWaves) void adapters_up_kernel(AdapterArgs 
     const int mine = r0 + 4 * group;                 // the first of the lane's four rows of out
     const Tile f = now;
     request(now, tile + 1);
+    uint4 op[kMany][S];                              // the terms as operands
+#pragma unroll
+    for (int ks = 0; ks < S; ++ks) {
+      if constexpr (F32) {
+        uint4 term[3];
+        three_terms(f.t[0][ks], f.t[F32 || KS ? 1 : 0][ks], term);
+        if constexpr (KS == 0) {
+          op[0][ks] = group < 2 ? term[0] : term[1];
+          op[kMany - 1][ks] = group < 2 ? term[2] : make_uint4(0, 0, 0, 0);
+        } else {
+#pragma unroll
+          for (int o = 0; o < kMany; ++o) op[o][ks] = term[o];
+        }
+      } else {
+#pragma unroll
+        for (int o = 0; o < kMany; ++o) op[o][ks] = f.t[o][ks];
+      }
+    }
     f32x4 sum[8];
 #pragma unroll
     for (int s = 0; s < 8; ++s) sum[s] = f32x4{0, 0, 0, 0};
@@ -311,8 +362,8 @@ __global__ __launch_bounds__(64 * kUpWaves) void adapters_up_kernel(AdapterArgs 
 #pragma unroll
           for (int ks = 0; ks < S; ++ks) {
             const uint4 g = KEEP ? b[KEEP ? ks : 0][s] : load_b(w, rank, s, ks);
-            v = mfma(f.high[ks], g, v);
-            if constexpr (KS != 0) v = mfma(f.low[ks], g, v);
+#pragma unroll
+            for (int o = 0; o < kMany; ++o) v = mfma(op[o][ks], g, v);
           }
           if (all) {
             sum[s] = v;
@@ -530,8 +581,12 @@ hipError_t launch_adapters(const situ_moe_adapters_t& p, hipStream_t s) {
     else hipLaunchKernelGGL(adapters_row_kernel<false>, grid, threads, 0, s, a, log_pieces);
     return hipGetLastError();
   }
-  a.high = static_cast<uint16_t*>(p.workspace);
-  a.low = a.high + (int64_t)p.rows * r;
+  if (p.out_dtype == SITU_OUT_F32) {
+    a.t = static_cast<float*>(p.workspace);
+  } else {
+    a.high = static_cast<uint16_t*>(p.workspace);
+    a.low = a.high + (int64_t)p.rows * r;
+  }
   a.up_tile = up_tile_rows(p.rows);
   a.tile = down_tile_rows(p.rows);
   const dim3 grid((unsigned)((p.rows + a.tile - 1) / a.tile));

@@ -32,7 +32,7 @@ hipError_t launch_pair_combine(const situ_moe_combine_t& a, hipStream_t s);
 hipError_t launch_pair_combine_backward(const situ_moe_combine_t& a, hipStream_t s);
 
 // ---- the adapters
-// Workspace: two bf16 terms of t a row and rank; none where one launch does it all.
+// Workspace: t, two bf16 terms or fp32 a row and rank; none where one launch does it all.
 uint64_t adapters_workspace_bytes(const situ_moe_adapters_t& a);
 hipError_t launch_adapters(const situ_moe_adapters_t& a, hipStream_t s);
 

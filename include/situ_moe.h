@@ -516,9 +516,9 @@ situ_status situ_moe_combine_backward(const situ_moe_combine_t* args, void* hip_
  * base NULL stands for zeros.  out may be base itself (the same address and
  * stride).  Rows of no request are not written.  ranks[i] is the number of
  * leading rows of a[i] (and columns of b[i]) that count, NULL: all; scales
- * NULL: 1.  Sums, and a[i] x[r] between the two products, are held to fp32
- * accuracy (the second product takes it as two bf16 terms, 2^-16 of it); one
- * rounding at the end for bf16.  An infinity in b[i] makes its column infinite
+ * NULL: 1.  Sums are fp32; a[i] x[r] between the two products is fp32 for an fp32
+ * out, and held to 2^-16 of it or better for a bf16 out, which is rounded once at
+ * the end.  An infinity in b[i] makes its column infinite
  * or NaN in the request's rows.  k, n and rank multiples of 8, k and n up to 2^18,
  * rank up to 256, rows 0 .. 2^24, requests and adapters 1 .. 2^20.  Rows of x, a, b,
  * base and out start on 16 bytes.  Except for out and base, outputs and workspace must
