@@ -117,13 +117,16 @@ __device__ __forceinline__ uint4 pack8(const float f[8]) {
   return __builtin_bit_cast(uint4, b);
 }
 
-// Four ranks of t as two bf16 terms.  A rounded value that is not finite has no second.
+// Four ranks of t as two bf16 terms.  A value that is not finite has no second; a finite one past bf16's largest has
+// that as its first.
 __device__ __forceinline__ void two_terms(const f32x4& t, uint2& high, uint2& low) {
   typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
   bf16x4 h, l;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     h[i] = (__bf16)t[i];
+    if (fabsf((float)h[i]) == __builtin_inff() && fabsf(t[i]) < __builtin_inff())
+      h[i] = (__bf16)__builtin_copysignf(0x1.fep127f, t[i]);
     const float d = t[i] - (float)h[i];
     l[i] = (__bf16)(fabsf(d) < __builtin_inff() ? d : 0.0f);
   }
