@@ -41,8 +41,14 @@ struct ActArgs {
 
 // Constants of a row.
 struct RowK {
-  float b, ib, l, il;         // SiTU: beta, 1 / beta, linear beta and its inverse; else b = a, l = c
+  float b, ib, l, il;         // SiTU: |beta|, 1 / |beta|, |linear beta| and its inverse; else b = a, l = c
 };
+// b t(x/b) is even in b and, from |b| = 2^100 on, x for every |x| up to 2^88: larger ones (infinity too) are taken for
+// 2^100, so that no product of the two leaves fp32's range before h does.  NaN stays.
+__device__ __forceinline__ void saturation(float b, float& limit, float& inverse) {
+  limit = __builtin_elementwise_minimum(fabsf(b), 0x1p100f);
+  inverse = __builtin_elementwise_minimum(__builtin_amdgcn_rcpf(limit), 0x1p126f);
+}
 
 struct Experts {
   int32_t offsets[kActExperts + 1];
@@ -74,25 +80,28 @@ __device__ __forceinline__ bool find_expert(const Experts& x, int experts, int r
 template <int KIND>
 __device__ __forceinline__ RowK row_k(const Experts& x, int e) {
   if constexpr (KIND == SITU_ACTIVATION_SWIGLU) return RowK{1.0f, 1.0f, 0.0f, 1.0f};
-  const float b = x.p0[e], l = x.p1[e];
-  if constexpr (KIND == SITU_ACTIVATION_SWIGLU_BIAS) return RowK{b, 1.0f, l, 1.0f};
-  return RowK{b, __builtin_amdgcn_rcpf(b), l, __builtin_amdgcn_rcpf(l)};
+  if constexpr (KIND == SITU_ACTIVATION_SWIGLU_BIAS) return RowK{x.p0[e], 1.0f, x.p1[e], 1.0f};
+  RowK k;
+  saturation(x.p0[e], k.b, k.ib);
+  saturation(x.p1[e], k.l, k.il);
+  return k;
 }
 
-// tanh(x) = n / d of fp32 values: x clamped to [-8, 8] (tanh(8) is 1 - 2^-22), n = x P(x^2), d = Q(x^2) with P of
-// degree 3 and Q of 4, fitted on [0, 8] for the smallest largest relative error (reweighted least squares on the
-// linearized residual x P - tanh(x) Q): 1.5e-7, within 6 * 2^-24 as evaluated here.  Both are divided by 64, so that
+// b tanh(x / b) = n / d of fp32 values: x clamped to 8 b (tanh(8) is 1 - 2^-22), c = x / b, n = x P(c^2), d = Q(c^2) with
+// P of degree 3 and Q of 4, fitted on [0, 8] for the smallest largest relative error (reweighted least squares on the
+// linearized residual c P - tanh(c) Q): 1.5e-7, within 6 * 2^-24 as evaluated here.  With x and not c in n, no b is
+// multiplied back: the value is right where c underflows.  Both are divided by 64, so that
 // the product of two d and 1 + e^-g overflows no sooner than e^-g does.  A NaN stays one.
-__device__ __forceinline__ void tanh_parts(float x, float& n, float& d) {
+__device__ __forceinline__ void tanh_parts(float x, float b, float inverse, float& n, float& d) {
   constexpr float k = 0x1p-6f;
-  const float c = __builtin_elementwise_maximum(__builtin_elementwise_minimum(x, 8.0f), -8.0f);
-  const float s = c * c;
+  x = __builtin_elementwise_maximum(__builtin_elementwise_minimum(x, 8.0f * b), -8.0f * b);
+  const float c = x * inverse, s = c * c;
   float p = 1.1475112e-05f * k, q = 2.4732324e-07f * k;
   q = fmaf(q, s, 0.000239314897f * k);
   p = fmaf(p, s, 0.00295580747f * k);  q = fmaf(q, s, 0.0238357844f * k);
   p = fmaf(p, s, 0.129303546f * k);    q = fmaf(q, s, 0.462636088f * k);
   p = fmaf(p, s, k);                   q = fmaf(q, s, k);
-  n = c * p;
+  n = x * p;
   d = q;
 }
 
@@ -100,26 +109,27 @@ template <int KIND>
 __device__ __forceinline__ float act(float g, float u, const RowK& k) {
   if constexpr (KIND == SITU_ACTIVATION_SITU) {
     float n1, d1, n3, d3;
-    tanh_parts(g * k.ib, n1, d1);
-    tanh_parts(u * k.il, n3, d3);
+    tanh_parts(g, k.b, k.ib, n1, d1);
+    tanh_parts(u, k.l, k.il, n3, d3);
     const float e = __builtin_amdgcn_exp2f(g * -kL2e), t = d1 * d3;
-    return (n1 * n3) * __builtin_amdgcn_rcpf(fmaf(t, e, t)) * (k.b * k.l);
+    return n1 * __builtin_amdgcn_rcpf(fmaf(t, e, t)) * n3;      // the factor that may be 0 first: n1 n3 may overflow
   } else {
     const float e = __builtin_amdgcn_exp2f(k.b * g * -kL2e);
     return g * __builtin_amdgcn_rcpf(1.0f + e) * (u + k.l);      // the small factor first: g u may overflow
   }
 }
 
-// tanh(x) and 1 - tanh(x)^2 = (1 - tanh)(1 + tanh), with e = e^-2|x|: tanh = 1 - e r and 1 + tanh = r, r = 2 / (1 + e).
-// Below 1/16, where 1 - e r is a difference of near numbers, the odd series to x^5, off by less than 2^-27; above it
-// 1 - e r is within 2^-20 of its value.
-__device__ __forceinline__ void tanh_slope(float x, float& t, float& slope) {
+// b t and 1 - t^2 = (1 - t)(1 + t) for t = tanh(x), x = v / b, with e = e^-2|x|: t = 1 - e r and 1 + t = r, r = 2 / (1 + e).
+// Below 1/16, where 1 - e r is a difference of near numbers, the odd series to x^5 (v times its even part: v may be where
+// x underflows), off by less than 2^-27; above it 1 - e r is within 2^-20 of its value.
+__device__ __forceinline__ void tanh_slope(float v, float b, float inverse, float& bt, float& slope) {
+  const float x = v * inverse;
   const float e = __builtin_amdgcn_exp2f(fabsf(x) * (-2.0f * kL2e));
   const float r = __builtin_amdgcn_rcpf(fmaf(e, 0.5f, 0.5f)), er = e * r;
   slope = er * r;
   const float x2 = x * x;
-  const float series = fmaf(x2 * x, fmaf(x2, 2.0f / 15.0f, -1.0f / 3.0f), x);
-  t = fabsf(x) < 0.0625f ? series : __builtin_copysignf(1.0f - er, x);
+  const float series = v * fmaf(x2, fmaf(x2, 2.0f / 15.0f, -1.0f / 3.0f), 1.0f);
+  bt = fabsf(x) < 0.0625f ? series : __builtin_copysignf(b * (1.0f - er), v);
 }
 __device__ __forceinline__ void sigmoid_both(float x, float& s, float& left) {
   const float e = __builtin_amdgcn_exp2f(fabsf(x) * -kL2e);
@@ -131,11 +141,11 @@ __device__ __forceinline__ void sigmoid_both(float x, float& s, float& left) {
 template <int KIND>
 __device__ __forceinline__ void act_backward(float g, float u, float dh, const RowK& k, float& dg, float& du, float& h) {
   if constexpr (KIND == SITU_ACTIVATION_SITU) {
-    float t1, s1, t3, s3, s, left;
-    tanh_slope(g * k.ib, t1, s1);
-    tanh_slope(u * k.il, t3, s3);
+    float gate, s1, up, s3, s, left;
+    tanh_slope(g, k.b, k.ib, gate, s1);
+    tanh_slope(u, k.l, k.il, up, s3);
     sigmoid_both(g, s, left);
-    const float gate = k.b * t1 * s, up = k.l * t3;
+    gate *= s;
     h = gate * up;
     dg = dh * up * fmaf(gate, left, s1 * s);         // |up| is at most l (the factor first: 110 us for 106)
     du = dh * (gate * s3);
