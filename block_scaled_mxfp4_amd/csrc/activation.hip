@@ -129,7 +129,7 @@ __device__ __forceinline__ void tanh_slope(float v, float b, float inverse, floa
   slope = er * r;
   const float x2 = x * x;
   const float series = v * fmaf(x2, fmaf(x2, 2.0f / 15.0f, -1.0f / 3.0f), 1.0f);
-  bt = fabsf(x) < 0.0625f ? series : __builtin_copysignf(b * (1.0f - er), v);
+  bt = fabsf(x) < 0.0625f ? series : __builtin_copysignf(fmaf(-b, er, b), v);
 }
 __device__ __forceinline__ void sigmoid_both(float x, float& s, float& left) {
   const float e = __builtin_amdgcn_exp2f(fabsf(x) * -kL2e);
@@ -147,7 +147,7 @@ __device__ __forceinline__ void act_backward(float g, float u, float dh, const R
     sigmoid_both(g, s, left);
     gate *= s;
     h = gate * up;
-    dg = dh * up * fmaf(gate, left, s1 * s);         // |up| is at most l (the factor first: 110 us for 106)
+    dg = dh * (up * fmaf(gate, left, s1 * s));       // the factor is at most 1.1, and dh up may overflow where it is 0
     du = dh * (gate * s3);
   } else {
     float s, left;
