@@ -90,10 +90,11 @@ __device__ __forceinline__ RowK row_k(const Experts& x, int e) {
 // b tanh(x / b) = n / d of fp32 values: x clamped to 8 b (tanh(8) is 1 - 2^-22), c = x / b, n = x P(c^2), d = Q(c^2) with
 // P of degree 3 and Q of 4, fitted on [0, 8] for the smallest largest relative error (reweighted least squares on the
 // linearized residual c P - tanh(c) Q): 1.5e-7, within 6 * 2^-24 as evaluated here.  With x and not c in n, no b is
-// multiplied back: the value is right where c underflows.  Both are divided by 64, so that
-// the product of two d and 1 + e^-g overflows no sooner than e^-g does.  A NaN stays one.
+// multiplied back: the value is right where c underflows.  Q(64) is 195: both are divided by 256, so that the product of
+// two d, at most 0.59, and 1 + e^-g overflows no sooner than e^-g does, and its reciprocal is a normal value where e^-g
+// is up to 2^126.  A NaN stays one.
 __device__ __forceinline__ void tanh_parts(float x, float b, float inverse, float& n, float& d) {
-  constexpr float k = 0x1p-6f;
+  constexpr float k = 0x1p-8f;
   x = __builtin_elementwise_maximum(__builtin_elementwise_minimum(x, 8.0f * b), -8.0f * b);
   const float c = x * inverse, s = c * c;
   float p = 1.1475112e-05f * k, q = 2.4732324e-07f * k;

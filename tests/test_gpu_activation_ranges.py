@@ -34,3 +34,16 @@ def test_large_gradients(kind, largest):
         tol = (1328 * U * m + floor) * (1 + 2.0 ** -8) + 2.0 ** -8 * want.abs()
         bad = fits & ~((got.to(D) - want).abs() <= tol)
         assert not bad.any(), (g[bad].tolist(), u[bad].tolist(), got[bad].tolist(), want[bad].tolist())
+
+
+def test_last_normal_sigmoids():
+    """Gates down to -87, where sigmoid(g) is fp32's last normal value: h keeps its accuracy with both tanh saturated.
+    Tolerance: (6 m + 64) u a factor with m up to 88, and bf16's rounding; nothing on the way is below 2^-126."""
+    g = torch.arange(-87, -79, 0.5, device="cuda").to(BF)
+    con = dict(situ_beta=torch.tensor([4.0], device="cuda"), situ_linear_beta=torch.tensor([25.0], device="cuda"))
+    for up in (1000.0, -300.0, 10.0, MOST):
+        both = torch.cat([g, torch.full_like(g, up)])[None].contiguous()
+        h = B.situ_moe_activation(both, **con)
+        p = [c.to(D)[:, None] for c in con.values()]
+        want = formulas("situ", both.to(D)[:, :16], both.to(D)[:, 16:], torch.zeros(1, 16, dtype=D, device="cuda"), p)[0]
+        assert ((h.to(D) - want).abs() <= ((12 * 88 + 128) * U + 2.0 ** -8) * want.abs()).all(), (up, h.tolist(), want.tolist())
