@@ -87,12 +87,15 @@ def _elsewhere(dev, stream, call, *args):
         return call(handle, *args)
 
 
-def _run(entry, handle, form, *fields):
+def _pack(form, *fields):
     try:
-        args = form.pack(*fields)
+        return form.pack(*fields)
     except (struct.error, OverflowError):
         _fail(3, "a size past 32 bits, or a scale past fp32")
-    status = entry(args, handle)
+
+
+def _run(entry, handle, form, *fields):
+    status = entry(_pack(form, *fields), handle)
     if status:
         _B._check(status)
 
@@ -106,13 +109,13 @@ def _need_bytes(fn, args):
 @functools.lru_cache(maxsize=256)
 def _router_bytes(tokens, experts):
     return _need_bytes(_library.situ_moe_router_workspace,
-                       _ROUTER.pack(tokens, experts, 1, 0, 0, 0, 0, 1.0, 0, *[0] * 6, 1, 1, 1, 0, 0))
+                       _pack(_ROUTER, tokens, experts, 1, 0, 0, 0, 0, 1.0, 0, *[0] * 6, 1, 1, 1, 0, 0))
 
 
 @functools.lru_cache(maxsize=256)
 def _adapters_bytes(rows, n, k, rank, requests):
     return _need_bytes(_library.situ_moe_adapters_workspace,
-                       _ADAPTERS.pack(rows, n, k, rank, requests, *[0] * 6, *[0] * 11))
+                       _pack(_ADAPTERS, rows, n, k, rank, requests, *[0] * 6, *[0] * 11))
 
 
 def _workspace(given, need, device, dev):
