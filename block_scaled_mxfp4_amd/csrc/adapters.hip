@@ -546,7 +546,7 @@ int down_tile_rows(int32_t rows) {
 // against 12.6, 256 rows 20 against 15.
 bool row_by_row(const situ_moe_adapters_t& p) {
   if (p.rank > 16) return p.rows <= 64;
-  return p.rows <= 128 || (p.rows <= 512 && p.rows <= 2 * p.requests);
+  return p.rows <= 128 || (p.rows <= 512 && p.rows <= 2 * (int64_t)p.requests);
 }
 
 template <bool F32>

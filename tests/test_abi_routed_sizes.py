@@ -1,11 +1,14 @@
 """Sizes at the ends of their types in the calls of the steps around the routed
 products, on the host (no GPU needed, no kernel is launched)."""
 
+import ctypes
+
 import pytest
 import torch
 
 import block_scaled_mxfp4_amd as B
 from test_abi_grouped import _Fake, _status
+from test_abi_routed import ADAPT
 
 BF, F32, I32 = torch.bfloat16, torch.float32, torch.int32
 MANY = (1 << 31) + 4
@@ -49,3 +52,14 @@ def test_sizes_past_32_bits(fakes):
                  lambda: adapters(MANY, 64, 32, 2), lambda: adapters(4, 1 << 31, 32, 2), lambda: adapters(4, 64, 1 << 31, 2),
                  lambda: adapters(4, 64, 32, MANY), lambda: adapters(4, 64, 32, 2, rank=1 << 31)):
         assert _status(call) == "SITU_E_UNSUPPORTED"
+
+
+def test_adapters_workspace_of_many_requests():
+    """The rule that goes by rows and requests does not leave 32 bits: more requests than the call takes ask for no more."""
+    n = ctypes.c_uint64()
+    sizes = []
+    for requests in (1 << 20, (1 << 30) - 1, 1 << 30, (1 << 31) - 1):
+        args = B.SituMoeAdapters(**dict(ADAPT, rows=512, requests=requests))
+        assert B.load().situ_moe_adapters_workspace(ctypes.byref(args), ctypes.byref(n)) == 0
+        sizes.append(n.value)
+    assert sizes == [0] * 4
