@@ -11,10 +11,13 @@
 // t' = 1 - t^2 = 4 e / (1 + e)^2 with e = e^-2|x|, and s(-x) from the same
 // exponential as s(x): neither is a difference of near numbers.
 //
-// Elementwise, bound by HBM and nearly by the vector units: 8 bytes a (gate, up)
-// pair forward with codes, 10 backward from codes with h; 57 and 64 issue slots.
-// 262144 x 384 forward with codes: 150 to 166 us (4.9 TB/s and more); 65521 x 768
-// backward: 106 (4.8 TB/s; a large copy moves 4.9).  Sixteen lanes take 128 columns of a row's gate and
+// Elementwise: 8 bytes a (gate, up) pair forward with codes, 10 backward from codes
+// with h.  Forward with codes the vector units' issue binds as much as HBM does:
+// 262144 x 384 is 56 slots a pair, 145 us of the SIMDs at 2.4 GHz and 165 at 2.1,
+// beside 165 us of the bytes at the 4.9 TB/s of a large copy.  It takes 152 to 166 us,
+// by the clock that the card holds, and has taken 189 for some ten milliseconds
+// after a pause.  The gradient, 65521 x 768, is bound by HBM: 102 to 109 us (4.8
+// TB/s), 124 in such a stretch.  Sixteen lanes take 128 columns of a row's gate and
 // the same of its up, eight each (16 bytes): a block of the 8-bit format, whose
 // maximum is then four DPP moves.  They walk the row's blocks, so that the row's
 // expert is looked up once, in LDS, where the offsets and constants are copied.
@@ -210,7 +213,8 @@ __device__ __forceinline__ void put(uint8_t* p, const uint2& v) {
   __builtin_nontemporal_store(i32x2{(int)v.x, (int)v.y}, reinterpret_cast<i32x2*>(p));
 }
 
-// gate_up is read once (262144 x 384: 168 us with ordinary loads, 150 so; the gradient's inputs gained nothing by it).
+// gate_up is read once (262144 x 384, the least of each: 168 us with ordinary loads, 150 so; the gradient's inputs gained
+// nothing by it).
 __device__ __forceinline__ uint4 load_once(const uint16_t* p) {
   return __builtin_bit_cast(uint4, __builtin_nontemporal_load(reinterpret_cast<const i32x4*>(p)));
 }

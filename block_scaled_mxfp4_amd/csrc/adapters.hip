@@ -16,7 +16,7 @@
 // them.
 //
 // Between the two, t is held as its output asks for.  For a bf16 out it is two bf16
-// terms, high and low: they lose no more than 2^-16 of it, against the 2^-9 of out's
+// terms, high and low: they lose no more than 2^-16 of it, against the 2^-8 of out's
 // own rounding.  For an fp32 out it is fp32, which the second product takes apart
 // into three bf16 terms, exactly, so that a row has the accuracy that the one
 // launch gives it.  With ranks up to 16 two terms fit in one instruction's 32
@@ -543,7 +543,10 @@ int down_tile_rows(int32_t rows) {
 // The one launch reads both matrices of its adapter for every row; two launches read them once for the rows of a request
 // in a tile.  Rank 16, 3584 to 7168, requests of one row: 64 rows 8.7 us against 14.8, 256 rows 20 against 27; rank 32:
 // 64 rows 14 against 17, 128 rows 22 against 21.  Requests of 32 rows, rank 16: 64 rows 8.8 against 12.1, 128 rows 12.4
-// against 12.6, 256 rows 20 against 15.
+// against 12.6, 256 rows 20 against 15.  Larger ranks, requests of one row: 16 rows 11 against 15 at rank 64, 22 against
+// 25 at 128, 42 against 56 at 256; 32 rows 17 against 18, 31 against 28, 62 against 74; 64 rows 23 against 23, 46 against
+// 35, 96 against 107.  One request of 64 rows: 20 against 18, 39 against 34, 92 against 78.  So 64 rows of rank 128 are
+// a quarter slower than they could be.
 bool row_by_row(const situ_moe_adapters_t& p) {
   if (p.rank > 16) return p.rows <= 64;
   return p.rows <= 128 || (p.rows <= 512 && p.rows <= 2 * (int64_t)p.requests);
@@ -602,7 +605,7 @@ hipError_t launch_adapters(const situ_moe_adapters_t& p, hipStream_t s) {
   if (e != hipSuccess) return e;
   a.up_tiles = (p.rows + a.up_tile - 1) / a.up_tile;
   a.chunks = (p.n + 127) / 128;
-  // tiles of a wave: as many as leave three waves a SIMD
+  // tiles of a wave: as many as leave three waves for each of the chip's 1024 SIMDs
   constexpr int64_t kUpItems = 256 * 4 * 3;
   a.run = (int)std::min<int64_t>(std::max<int64_t>(1, ((int64_t)a.up_tiles * a.chunks + kUpItems - 1) / kUpItems), a.up_tiles);
   const int64_t items = (int64_t)((a.up_tiles + a.run - 1) / a.run) * a.chunks;

@@ -4,7 +4,7 @@
 // Both move rows and compute little: HBM bounds them (8192 tokens of an EP8 shard,
 // 16 x 3584: 29 us, 6.1 TB/s, part of it from the caches; the gradients of 4095 x 16
 // x 3584: 185 us, 5.2 TB/s).  A lane takes eight columns
-// (16 bytes of bf16), a wave 512.  The token's rows and weights are read by its
+// (16 bytes of bf16), a wave 512 at once.  The token's rows and weights are read by its
 // first lanes together, those that are not local drop out of a ballot, and the
 // others' rows are requested four at a time from addresses the whole wave shares.
 // Local weights of 0 are products too, as the formula has them.
@@ -37,7 +37,7 @@ __device__ __forceinline__ Eight<F32> load8(const void* p, int64_t at) {
     return {*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + at)};
   }
 }
-// The gradient's y is read once (4095 x 16 x 3584: 195 us with ordinary loads, 190 so).
+// The gradient's y is read once (4095 x 16 x 3584: 195 us with ordinary loads, 185 so).
 template <bool F32>
 __device__ __forceinline__ Eight<F32> load8_once(const void* p, int64_t at) {
   const i32x4* q = reinterpret_cast<const i32x4*>(static_cast<const char*>(p) + at * (F32 ? 4 : 2));
@@ -97,7 +97,7 @@ template <bool YF, bool OF>
 __global__ __launch_bounds__(64 * kWaves) void pair_combine_kernel(situ_moe_combine_t p, int parts, int64_t items) {
   const int lane = lane_id();
   for (int64_t item = (int64_t)blockIdx.x * kWaves + wave_id(); item < items; item += (int64_t)gridDim.x * kWaves) {
-    const int64_t t = (uint32_t)item / (uint32_t)parts;         // items: 512 columns each of what lies in memory
+    const int64_t t = (uint32_t)item / (uint32_t)parts;         // items: kPieces times 512 columns of a token
     const int col = (int)(item - t * parts) * kCols * kPieces + 8 * lane;
     float acc[kPieces][8] = {};
     for (int first = 0; first < p.top_k; first += kWave) {

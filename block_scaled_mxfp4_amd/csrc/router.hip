@@ -9,8 +9,13 @@
 // one that hardly more do (over their values, three or four steps, where one over the
 // float's bits takes ten: 32768 x 64 16 us for 24).  What reaches it (some 1.3 top_k) is packed into LDS,
 // one candidate a lane, and a candidate's place is the number of candidates before
-// it.  Where more than 64 reach it (many equals; top_k near 64), the wave takes
-// the largest that is left top_k times instead.
+// it.  Where more than 64 reach it, the wave takes the largest that is left top_k
+// times instead.  That is slow, and it is not for rows of equals alone (32768 x 896
+// of them, top 16: 262 us for 32): since the threshold goes by the lanes' largest,
+// it meets some ordinary rows from a top_k of some 30 on, most from 40 on, and all
+// where top_k passes the lanes that have experts (34 for 65 or 129 experts).
+// Softmax with the loss, 32768 rows of 896: top 24 34 us, 32 137, 40 762, 64 1316;
+// of 160: top 24 27 us, 32 142; of 65: top 16 22 us, 34 138.
 //
 // A selection by sigmoid + bias is compared in 64 bits, since the neighbours of
 // 900 experts lie as near as fp32 rounds.  The threshold is taken on fp32 scores
@@ -44,7 +49,10 @@ namespace {
 constexpr float kL2e = 1.44269502162933349609375f;   // log2(e) rounded to fp32
 constexpr int kRouterWaves = 8;                       // of a workgroup
 constexpr int kRouterBlocks = 768;                    // workgroups at most where the loss is taken
-constexpr int kBackWaves = 8, kBackBlocks = 640;      // of the gradient (16384 x 896: 24 us; 512 or 768 26, 1024 29)
+// Of the gradient: 640 workgroups suit softmax scores of many experts.  us with 512, 640, 1024 and 1536: 16384 x 896 fp32
+// 24.7, 23.5, 27.6, 31.8 and bf16 21.2, 21.3, 24.2, 26.7; 32768 x 256 fp32 19.0, 17.1, 16.3, 16.5.  Few experts would
+// take more (32768 x 64 fp32 11.6, 11.5, 10.1, 9.7), sigmoids of many fewer (16384 x 896 fp32 28.5, 32.5, 31.7, 32.7).
+constexpr int kBackWaves = 8, kBackBlocks = 640;
 constexpr int kOneBlockTokens = 32;                   // up to here one workgroup finishes the loss by itself
 
 // Keys ascend with the values; 0 is an expert that cannot be chosen (-inf, NaN).
@@ -157,8 +165,8 @@ __device__ __forceinline__ uint64_t readlane64(uint64_t v, int lane) {
          (uint32_t)__builtin_amdgcn_readlane((int)v, lane);
 }
 
-// A wave's row of logits by expert, and the candidates' ids, then what they are ordered by.  The row's place takes the scores in 64 bits where more
-// than 64 candidates ask for them.
+// A wave's row of logits by expert, and the candidates' ids, then what they are ordered by.  The row's place takes the
+// scores in 64 bits where more than 64 candidates ask for them.
 template <int N, bool BIAS>
 struct alignas(16) WaveRow {
   union {
