@@ -46,10 +46,10 @@ struct ActArgs {
 struct RowK {
   float b, ib, l, il;         // SiTU: |beta|, 1 / |beta|, |linear beta| and its inverse; else b = a, l = c
 };
-// b t(x/b) is even in b and, from |b| = 2^100 on, x for every |x| up to 2^88: larger ones (infinity too) are taken for
-// 2^100, so that no product of the two leaves fp32's range before h does.  NaN stays.
+// b t(x/b) is even in b and, from |b| = 2^123 on, x for every |x| up to 2^111: larger ones (infinity too) are taken for
+// 2^123, so that nothing leaves fp32's range before h does (below) and 1 / b is a normal value.  NaN stays.
 __device__ __forceinline__ void saturation(float b, float& limit, float& inverse) {
-  limit = __builtin_elementwise_minimum(fabsf(b), 0x1p100f);
+  limit = __builtin_elementwise_minimum(fabsf(b), 0x1p123f);
   inverse = __builtin_elementwise_minimum(__builtin_amdgcn_rcpf(limit), 0x1p126f);
 }
 
@@ -93,11 +93,13 @@ __device__ __forceinline__ RowK row_k(const Experts& x, int e) {
 // b tanh(x / b) = n / d of fp32 values: x clamped to 8 b (tanh(8) is 1 - 2^-22), c = x / b, n = x P(c^2), d = Q(c^2) with
 // P of degree 3 and Q of 4, fitted on [0, 8] for the smallest largest relative error (reweighted least squares on the
 // linearized residual c P - tanh(c) Q): 1.5e-7, within 6 * 2^-24 as evaluated here.  With x and not c in n, no b is
-// multiplied back: the value is right where c underflows.  Q(64) is 195: both are divided by 256, so that the product of
-// two d, at most 0.59, and 1 + e^-g overflows no sooner than e^-g does, and its reciprocal is a normal value where e^-g
-// is up to 2^126.  A NaN stays one.
+// multiplied back: the value is right where c underflows.  Both are divided by 2^E.  Q lies in [1, 195.2]: with E of 12
+// for gate and 4 for up the product of their d, at most 0.59, and 1 + e^-g overflows no sooner than e^-g does, and its
+// reciprocal is a normal value where e^-g is up to 2^126; for |b| and |l| up to 2^123 gate times the reciprocal, h / (l t3
+// d3), is below 2^128, and so is l t3 d3.  A NaN stays one.
+template <int E>
 __device__ __forceinline__ void tanh_parts(float x, float b, float inverse, float& n, float& d) {
-  constexpr float k = 0x1p-8f;
+  constexpr float k = 1.0f / (1 << E);
   x = __builtin_elementwise_maximum(__builtin_elementwise_minimum(x, 8.0f * b), -8.0f * b);
   const float c = x * inverse, s = c * c;
   float p = 1.1475112e-05f * k, q = 2.4732324e-07f * k;
@@ -113,8 +115,8 @@ template <int KIND>
 __device__ __forceinline__ float act(float g, float u, const RowK& k) {
   if constexpr (KIND == SITU_ACTIVATION_SITU) {
     float n1, d1, n3, d3;
-    tanh_parts(g, k.b, k.ib, n1, d1);
-    tanh_parts(u, k.l, k.il, n3, d3);
+    tanh_parts<12>(g, k.b, k.ib, n1, d1);
+    tanh_parts<4>(u, k.l, k.il, n3, d3);
     const float e = __builtin_amdgcn_exp2f(g * -kL2e), t = d1 * d3;
     return n1 * __builtin_amdgcn_rcpf(fmaf(t, e, t)) * n3;      // the factor that may be 0 first: n1 n3 may overflow
   } else {

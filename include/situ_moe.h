@@ -456,7 +456,7 @@ situ_status situ_moe_router_backward(const situ_moe_router_backward_t* args, voi
  * beta, alpha and their like are the model's constants: they get no gradient.
  * The formulas are fp32; h and d_gate_up are rounded once, to bf16.  SiTU's
  * beta and linear beta are not 0; their signs do not matter, and a magnitude past
- * 2^100, infinity too, is taken for 2^100 (beta t(g / beta) is g there).  Rows
+ * 2^123, infinity too, is taken for 2^123 (beta t(g / beta) is g there).  Rows
  * outside every group are not written.  I a multiple of 8, up to 2^17;
  * rows 0 .. 2^24; experts 1 .. 1024.  gate_up, h, dh and d_gate_up 16-byte
  * aligned with strides of a multiple of 8; codes 8-byte aligned and dense.

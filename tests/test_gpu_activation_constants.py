@@ -78,25 +78,28 @@ def test_without_saturation_it_is_swiglu():
         assert ((a.double() - w.double()).abs() <= 2 * 2.0 ** -8 * w.double().abs() + 400 * 2.0 ** -24 * m + 2.0 ** -120).all()
 
 
-@pytest.mark.parametrize("betas", [(1.7, 25.0), (1e20, 1e20), (3e38, 3e38), (INF, INF)])
+@pytest.mark.parametrize("betas", [(1.7, 25.0), (1e20, 1e20), (1e35, 2.0), (2.0, 1e35), (1e35, 1e35), (2.0 ** 123, 2.0 ** 123),
+                                   (3e38, 3e38), (INF, INF)])
 def test_lowest_values(betas):
     """Gates and ups of the type's largest magnitudes and infinite ones: the limits, with any betas."""
     low = torch.finfo(BF).min
     con = dict(zip(("situ_beta", "situ_linear_beta"), (torch.tensor([v], device="cuda") for v in betas)))
-    vals = torch.tensor([low, -1e20, -1000.0, 1.0, 3.0, 2.0 ** 21, 1e20], dtype=BF, device="cuda")
-    g, u = torch.meshgrid(vals, torch.cat([vals, torch.zeros(1, dtype=BF, device="cuda")]), indexing="ij")
-    g, u = (t.reshape(1, -1) for t in (g, u))                   # 56 columns
+    vals = torch.tensor([low, -1e20, -1000.0, 1.0, 3.0, 2.0 ** 21, 1e20, 1e33, -low], dtype=BF, device="cuda")
+    g, u = torch.meshgrid(vals, torch.cat([vals, torch.tensor([0.0, 1e-3, -1e-10], dtype=BF, device="cuda")]), indexing="ij")
+    g, u = (t[:, None].expand(-1, 2, -1).reshape(1, -1) for t in (g, u))                  # 216 columns
     dh = torch.full_like(g, -0.5)
     both_ = torch.cat([g, u], 1)
     h = B.situ_moe_activation(both_, **con)
     d, again = B.situ_moe_activation_backward(dh, both_, recompute=True, **con)
-    # past 2^100 a beta is taken for 2^100
-    p = [torch.tensor([[min(abs(v), 2.0 ** 100)]], dtype=D, device="cuda") for v in betas]
+    # past 2^123 a beta is taken for 2^123
+    p = [torch.tensor([[min(float(torch.tensor(abs(v))), 2.0 ** 123)]], dtype=D, device="cuda") for v in betas]
     wh, wg, wu, mag, _ = formulas("situ", g.to(D), u.to(D), dh.to(D), p)
-    for got, want, m in ((h, wh, wh.abs()), (again, wh, wh.abs()), (d[:, :56], wg, mag), (d[:, 56:], wu, wu.abs())):
+    n = g.shape[1]
+    for got, want, m in ((h, wh, wh.abs()), (again, wh, wh.abs()), (d[:, :n], wg, mag), (d[:, n:], wu, wu.abs())):
         over = want.abs() > torch.finfo(BF).max * (1 + 2.0 ** -10)
         assert torch.equal(got[over].float().sign(), want[over].float().sign()) and torch.isinf(got[over]).all()
         fits = want.abs() < torch.finfo(BF).max * (1 - 2.0 ** -10)
-        # arguments of exponentials up to 100 (past it they are 0): (12 * 100 + 128) u; 2^-126 of the factors, up to 2^101 each
-        tol = 1328 * 2.0 ** -24 * m + 2.0 ** -8 * want.abs() + 2.0 ** -120 * (1 + g.to(D).abs().clamp(max=2.0 ** 101)) * (1 + u.to(D).abs().clamp(max=2.0 ** 101))
-        assert ((got[fits].to(D) - want[fits]).abs() <= tol[fits]).all(), betas
+        # arguments of exponentials up to 100 (past it they are 0): (12 * 100 + 128) u; 2^-126 of up, and of the gate's 100
+        tol = 1328 * 2.0 ** -24 * m + 2.0 ** -8 * want.abs() + 2.0 ** -120 * 100 * (1 + u.to(D).abs())
+        bad = fits & ~((got.to(D) - want).abs() <= tol)
+        assert not bad.any(), (betas, g[bad].tolist(), u[bad].tolist(), got[bad].tolist(), want[bad].tolist())
